@@ -17,6 +17,9 @@ from ._binding import (ABI_FUNCTIONS, MODES, MOE_FLAG_FUSED, MOE_FLAG_NONE, MOE_
                        moe_prepare_weights, moe_prepared_weights_bytes, moe_status_string,
                        moe_tensor_peak_probe, moe_workspace_bytes, moe_workspace_layout)
 from ._binding import PEAK_KINDS  # noqa: F401
+from ._binding import (LAYER_WEIGHTS, MOE_LAYER_MAX_TOKENS, MoeGateOptions, gate_options, moe_fp8_matmul,  # noqa: F401
+                       moe_fp8_matmul_workspace_bytes, moe_fp8_quantize, moe_gate, moe_layer, moe_layer_workspace_bytes,
+                       moe_ops_workspace_init)
 
 
 def alloc_workspace(d: MoeDims, mode, device="cuda") -> torch.Tensor:
@@ -26,3 +29,11 @@ def alloc_workspace(d: MoeDims, mode, device="cuda") -> torch.Tensor:
     if n == 0:
         raise ValueError("dimensions outside the library's limits")
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def alloc_ops_workspace(nbytes: int, device="cuda") -> torch.Tensor:
+    """A zeroed device byte buffer for moe_fp8_matmul or moe_layer (nbytes from their *_workspace_bytes); kept and
+    passed again, it needs no further initialisation."""
+    if nbytes == 0:
+        raise ValueError("sizes outside the library's limits")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)

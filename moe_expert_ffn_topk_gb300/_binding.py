@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in ``include/moe_ffn.h``.
+"""ctypes binding of the C ABI in ``include/moe_ffn.h``, ``include/moe_ops.h`` and ``include/moe_peak.h``.
 
 Argument marshalling only: each function takes torch tensors (device memory allocated by
 the caller), checks placement and contiguity, passes their addresses and the current CUDA
@@ -28,9 +28,17 @@ ABI_FUNCTIONS = ("moe_workspace_bytes", "moe_plan", "moe_dispatch", "moe_expert_
                  "moe_combine", "moe_forward", "moe_check_device_error", "moe_status_string",
                  "moe_workspace_layout", "moe_debug_bounded_wait", "moe_plan_noalloc", "moe_dispatch_quantize",
                  "moe_expert_l1_ex", "moe_forward_ex", "moe_expert_ffn", "moe_tensor_peak_probe",
-                 "moe_prepared_weights_bytes", "moe_prepare_weights")
+                 "moe_prepared_weights_bytes", "moe_prepare_weights",
+                 "moe_ops_workspace_init", "moe_gate", "moe_fp8_quantize", "moe_fp8_matmul_workspace_bytes",
+                 "moe_fp8_matmul", "moe_layer_workspace_bytes", "moe_layer")
 # moe_peak_kind (include/moe_peak.h): the tcgen05 instruction kinds the probe measures
 PEAK_KINDS = {"bf16": 0, "f16": 1, "e4m3_e2m1": 2, "e4m3_e4m3": 3}
+# moe_ops.h: element types, router scores, weight formats of moe_layer
+MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
+LAYER_WEIGHTS = {"bf16": 0, "fp8_block": 1, "fp4_mx": 2}
+MOE_QUANT_POW2 = 1
+MOE_LAYER_MAX_TOKENS = 64
 
 
 class MoeDims(ctypes.Structure):
@@ -54,6 +62,24 @@ class MoeWorkspaceLayout(ctypes.Structure):
         "comb", "ffn_counters",
         "total")] + \
         [("pool_rows", ctypes.c_int64)]
+
+
+class MoeGateOptions(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("normalize", ctypes.c_int32), ("route_scale", ctypes.c_float)]
+
+
+class MoeFp8MatmulArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("a", "a_scale", "b", "b_scale", "offsets", "out")] + \
+        [(n, ctypes.c_int64) for n in ("M", "N", "K", "a_stride", "b_stride", "out_stride")] + \
+        [("groups", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
+class MoeLayerArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("router", ctypes.c_void_p), ("w1", MoeOperand), ("w2", MoeOperand),
+                ("gate", ctypes.POINTER(MoeGateOptions)), ("gate_bias", ctypes.c_void_p), ("topk_ids", ctypes.c_void_p),
+                ("topk_weights", ctypes.c_void_p), ("y", ctypes.c_void_p), ("router_type", ctypes.c_int32),
+                ("weights", ctypes.c_int32), ("has_activation_clamp", ctypes.c_uint32), ("activation_clamp", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -89,6 +115,13 @@ def _load():
         "moe_tensor_peak_probe": (st, [st, ctypes.c_int64, ctypes.c_int, ctypes.POINTER(ctypes.c_double), vp, sz, vp]),
         "moe_prepared_weights_bytes": (sz, [dims_p, st, ctypes.c_int]),
         "moe_prepare_weights": (st, [vp, dims_p, st, ctypes.c_int, vp, sz, vp]),
+        "moe_ops_workspace_init": (st, [vp, sz, vp]),
+        "moe_gate": (st, [vp, st, ctypes.c_int64, vp, ctypes.POINTER(MoeGateOptions), dims_p, vp, vp, vp]),
+        "moe_fp8_quantize": (st, [vp, st, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_int64, vp, u32, vp]),
+        "moe_fp8_matmul_workspace_bytes": (sz, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]),
+        "moe_fp8_matmul": (st, [ctypes.POINTER(MoeFp8MatmulArgs), vp, sz, vp]),
+        "moe_layer_workspace_bytes": (sz, [dims_p, st]),
+        "moe_layer": (st, [ctypes.POINTER(MoeLayerArgs), dims_p, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -286,3 +319,135 @@ def moe_plan_noalloc(topk_ids, d: MoeDims, counts, offsets, row_src, stream=None
     _check(LIB.moe_plan_noalloc(_ptr(topk_ids, "topk_ids"), ctypes.byref(d), _ptr(counts, "counts"),
                                 _ptr(offsets, "offsets"), _ptr(row_src, "row_src"), _stream(stream)),
            "moe_plan_noalloc")
+
+
+# ---------------------------------------------------------------------------------------
+# include/moe_ops.h: the router, the block-scaled FP8 product, the few-token layer
+# ---------------------------------------------------------------------------------------
+
+
+def _float_type(t, what):
+    if t.dtype == torch.bfloat16:
+        return MOE_TYPE_BF16
+    if t.dtype == torch.float32:
+        return MOE_TYPE_F32
+    raise TypeError(f"{what} must be bfloat16 or float32")
+
+
+def _typed(t, what, *dtypes):
+    if t is not None and t.dtype not in dtypes:
+        raise TypeError(f"{what} must be " + " or ".join(str(d).replace("torch.", "") for d in dtypes))
+    return _ptr(t, what)
+
+
+def _shaped(t, what, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
+
+
+def _rows(t, what, rows=None, cols=None):
+    """Address and row stride of a matrix whose rows are contiguous (a column slice of a wider one is)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be in device memory")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not ({rows}, {cols})")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return (t.data_ptr() if t.numel() else None), stride
+
+
+def moe_ops_workspace_init(workspace, stream=None):
+    ws, nb = _ws(workspace)
+    _check(LIB.moe_ops_workspace_init(ws, nb, _stream(stream)), "moe_ops_workspace_init")
+
+
+def gate_options(score="softmax", groups=1, topk_groups=1, group_top=1, normalize=True, route_scale=1.0) -> MoeGateOptions:
+    """Options of the router: score "softmax" or "sigmoid"; the experts in `groups` equal runs of which the `topk_groups`
+    with the largest sum of their `group_top` (1 or 2) best choice values stay; normalised weights; their scale."""
+    return MoeGateOptions(SCORES[score], int(groups), int(topk_groups), int(group_top), int(bool(normalize)), float(route_scale))
+
+
+def moe_gate(logits, d: MoeDims, topk_ids, topk_weights, bias=None, options=None, stream=None):
+    """topk_ids (int32 [T,K]) and topk_weights (fp32 [T,K]) from logits (bf16 or fp32 [T,E], rows may be strided)."""
+    T, E, K = d.num_tokens, d.num_experts, d.topk
+    ptr, stride = _rows(logits, "logits", T, E)
+    for t, what in ((topk_ids, "topk_ids"), (topk_weights, "topk_weights")):
+        _shaped(t, what, T, K)
+    _shaped(bias, "bias", E)
+    _check(LIB.moe_gate(ptr, _float_type(logits, "logits"), stride, _typed(bias, "bias", torch.float32),
+                        None if options is None else ctypes.byref(options), ctypes.byref(d),
+                        _typed(topk_ids, "topk_ids", torch.int32), _typed(topk_weights, "topk_weights", torch.float32),
+                        _stream(stream)), "moe_gate")
+
+
+def moe_fp8_quantize(x, q, scale, pow2=False, stream=None):
+    """Rows of x (bf16 or fp32 [M,K]) into q (e4m3 [M,K]) and scale (fp32 [M, ceil(K/128)]); rows of x and q may be strided."""
+    M, K = x.shape
+    xp, xs = _rows(x, "x")
+    if q.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError("q must be float8_e4m3fn or uint8")
+    qp, qs = _rows(q, "q", M, K)
+    _shaped(scale, "scale", M, -(-K // 128))
+    _check(LIB.moe_fp8_quantize(xp, _float_type(x, "x"), M, K, xs, qp, qs, _typed(scale, "scale", torch.float32),
+                                MOE_QUANT_POW2 if pow2 else 0, _stream(stream)), "moe_fp8_quantize")
+
+
+def moe_fp8_matmul_workspace_bytes(M: int, N: int, K: int, groups: int = 1) -> int:
+    return LIB.moe_fp8_matmul_workspace_bytes(M, N, K, groups)
+
+
+def moe_fp8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream=None):
+    """out[m,n] = sum over blocks of a_scale * b_scale * (a . b^T): a e4m3 [M,K], a_scale fp32 [M, ceil(K/128)], b e4m3
+    [groups,N,K] (or [N,K]), b_scale fp32 [groups, ceil(N/128), ceil(K/128)], out bf16 or fp32 [M,N]. With `offsets`
+    (int32 [groups+1]) rows [offsets[g], offsets[g+1]) are multiplied by b[g]. Rows of a, b and out may be strided."""
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    if a.dtype not in codes or b.dtype not in codes:
+        raise TypeError("a and b must be float8_e4m3fn (or uint8 codes)")
+    if b.dim() == 2:
+        b = b.unsqueeze(0)
+    if b_scale.dim() == 2:
+        b_scale = b_scale.unsqueeze(0)
+    (M, K), (G, N) = a.shape, b.shape[:2]
+    nb, kb = -(-N // 128), -(-K // 128)
+    if G > 1 and b.stride(0) != N * b.stride(1):
+        raise ValueError("the groups of b must follow each other")
+    ap, a_stride = _rows(a, "a")
+    bp, b_stride = _rows(b.flatten(0, 1), "b", G * N, K)
+    op, out_stride = _rows(out, "out", M, N)
+    _shaped(a_scale, "a_scale", M, kb)
+    _shaped(b_scale, "b_scale", G, nb, kb)
+    _shaped(offsets, "offsets", G + 1)
+    args = MoeFp8MatmulArgs(ap, _typed(a_scale, "a_scale", torch.float32), bp, _typed(b_scale, "b_scale", torch.float32),
+                            _typed(offsets, "offsets", torch.int32), op, M, N, K, a_stride, b_stride, out_stride, G,
+                            _float_type(out, "out"))
+    ws, nbytes = _ws(workspace)
+    _check(LIB.moe_fp8_matmul(ctypes.byref(args), ws, nbytes, _stream(stream)), "moe_fp8_matmul")
+
+
+def moe_layer_workspace_bytes(d: MoeDims, weights) -> int:
+    return LIB.moe_layer_workspace_bytes(ctypes.byref(d), LAYER_WEIGHTS[weights])
+
+
+def moe_layer(x, router, w1, w1_scale, w2, w2_scale, y, d: MoeDims, weights, workspace, options=None, bias=None,
+              topk_ids=None, topk_weights=None, activation_clamp=None, stream=None):
+    """The whole layer for up to MOE_LAYER_MAX_TOKENS tokens in one launch: router product, selection, experts, combine.
+    weights: "bf16", "fp8_block" or "fp4_mx". Without a router, topk_ids and topk_weights are inputs; with one they are
+    optional outputs."""
+    T, H, E, K = d.num_tokens, d.hidden, d.num_experts, d.topk
+    _shaped(x, "x", T, H)
+    _shaped(y, "y", T, H)
+    _shaped(router, "router", E, H)
+    _shaped(bias, "bias", E)
+    _shaped(topk_ids, "topk_ids", T, K)
+    _shaped(topk_weights, "topk_weights", T, K)
+    args = MoeLayerArgs(_typed(x, "x", torch.bfloat16), _ptr(router, "router"), _operand(w1, w1_scale, "w1"),
+                        _operand(w2, w2_scale, "w2"), None if options is None else ctypes.pointer(options),
+                        _typed(bias, "bias", torch.float32), _typed(topk_ids, "topk_ids", torch.int32),
+                        _typed(topk_weights, "topk_weights", torch.float32), _typed(y, "y", torch.bfloat16),
+                        MOE_TYPE_BF16 if router is None else _float_type(router, "router"), LAYER_WEIGHTS[weights],
+                        0 if activation_clamp is None else 1, 0.0 if activation_clamp is None else float(activation_clamp))
+    ws, nb = _ws(workspace)
+    _check(LIB.moe_layer(ctypes.byref(args), ctypes.byref(d), ws, nb, _stream(stream)), "moe_layer")

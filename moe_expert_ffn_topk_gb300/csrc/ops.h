@@ -1,0 +1,43 @@
+// Declarations shared by the operators of moe_ops.h: the launchers and the layout of their workspaces.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "moe_ops.h"
+
+namespace moe {
+
+// The head of an operator's workspace: [0] is the error word that moe_check_device_error reads; the rest are
+// counters that every call leaves at zero.
+constexpr int kOpsHeaderInts = 64;
+
+// Experts of a router and selected experts per token that fit a warp's registers.
+constexpr int kGateMaxExperts = 1024;
+constexpr int kGateMaxTopk = 32;
+
+inline moe_gate_options default_gate_options() {
+    moe_gate_options o = {};
+    o.score = MOE_SCORE_SOFTMAX;
+    o.num_groups = o.topk_groups = o.group_top = o.normalize = 1;
+    o.route_scale = 1.0f;
+    return o;
+}
+bool gate_options_ok(const moe_gate_options& o, int E, int K);
+
+cudaError_t launch_gate(const void* logits, int type, int64_t stride, const float* bias, const moe_gate_options& o, int T,
+                        int E, int K, int32_t* ids, float* weights, cudaStream_t s);
+cudaError_t launch_fp8_quantize(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, uint8_t* q,
+                                int64_t q_stride, float* scale, bool pow2, cudaStream_t s);
+size_t fp8_matmul_workspace(int64_t M, int64_t N, int64_t K, int groups);
+cudaError_t launch_fp8_matmul(const moe_fp8_matmul_args& a, void* workspace, cudaStream_t s);
+
+// Byte offsets of moe_layer's workspace.
+struct LayerLayout {
+    size_t header, counters, logits, ids, weights, act, act_amax, slots, total;
+};
+LayerLayout layer_layout(const moe_dims& d);
+cudaError_t launch_layer(const moe_layer_args& a, const moe_gate_options& gate, const moe_dims& d, void* workspace,
+                         cudaStream_t s);
+
+}  // namespace moe
