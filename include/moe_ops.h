@@ -92,7 +92,7 @@ MOE_API moe_status moe_fp8_quantize(const void* x, moe_type type, int64_t rows, 
  *   offsets  NULL with groups = 1: every row of a is multiplied by b. Else device int32 [groups + 1], not
  *            decreasing, offsets[0] = 0 and offsets[groups] <= M (the offsets of moe_plan, for rows in plan order): rows
  *            [offsets[g], offsets[g+1]) are multiplied by b[g]. Rows from offsets[groups] on are not written. Values
- *            outside [0, M] are taken as the nearest bound.
+ *            outside [0, M] are taken as the nearest bound, one below an earlier one as that one.
  *   out      bf16 or fp32 [M,N], out_stride apart
  * The sums over a block of K are the tensor core's fp32 sums, those over the blocks are fp32 fused multiply-adds.
  * Limits: 0 <= M < 2^31, 1 <= N <= 2^20, 16 <= K <= 2^20, 1 <= groups <= 1024, M * out_stride and the other
