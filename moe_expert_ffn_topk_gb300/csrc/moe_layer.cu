@@ -1,120 +1,1022 @@
-// The whole MoE layer for a few tokens (moe_layer in moe_ops.h).
+// The whole MoE layer for a few tokens in one cooperative launch (moe_layer in moe_ops.h):
+//
+//     y[t] = sum over the token's experts e of w[t,e] * (SiLU(x[t] W1g[e]) * (x[t] W1u[e])) W2[e]
+//
+// With few tokens every expert that is touched is multiplied by a handful of rows, so the time is that of reading its
+// weights once. The kernel is a stream of weights through shared memory: one CTA per SM, a producer warp that keeps a ring
+// of stages of 16 KB full by bulk copies, and eight warps that multiply each stage by the tokens' rows with mma.sync
+// (16 weight rows x 8 tokens x 16 of K), which at this shape is far from the tensor pipe's bound. The weight addresses
+// depend on the routes alone, so the producer runs ahead across items, experts and from the first product into the
+// second, while the consumers wait for activations.
+//
+// Phases:
+//   1. router: every warp takes (expert, part of H) dot products with all tokens in fp32 (CUDA cores: the selection
+//      compares these sums); one CTA per token also rounds x to the f16 operand of the FP8 and FP4 formats. Grid barrier.
+//   2. selection: each CTA selects for all tokens itself (up to 8 tokens), or for its share of them and a second barrier.
+//      Each CTA then lists the experts with rows and their rows in shared memory.
+//   3. first product: items of 16 outputs (16 gate and 16 up rows of W1; BF16: 64 and 64) of one expert, dealt to the CTAs in
+//      turn. The eight warps split K, their sums meet in shared memory, and SwiGLU of them goes to the workspace in fp32 with
+//      the row's largest magnitude. A counter per expert says when its rows are complete.
+//   4. second product: items of 32 hidden columns (BF16: 128) of one expert, ordered by columns first and dealt in equal
+//      runs, so that a CTA adds up the experts of its columns itself, in order, in shared memory. Columns whose experts are
+//      split between CTAs meet in the workspace: the last CTA to arrive adds the parts in order. No atomics on values:
+//      results do not depend on timing.
+//
+// Operands. BF16: x as it is; the activations as two bf16 (hi + lo, 16 bits of them) and two MMAs. FP8 and FP4: the weights are
+// exact in f16, x and the activations are scaled by a power of two of their row to below 2^15 and rounded once to f16 (11 bits;
+// bf16 x is exact down to 2^-39 of its row's maximum, activations lose 2^-12 a value against 2^-9 of the bf16 result). The
+// FP8 weight scale multiplies the fp32 sum over each 64 of K; the UE8M0 scales of FP4 multiply the f16 codes relative to the
+// largest of the four blocks that a stage's sum covers (exact while they lie within 2^20 of it) and that one the fp32 sum.
+//
+// Every wait is bounded (2 s): MOE_ERR_TIMEOUT; from then on the CTA skips its waits and its work, and still passes its barriers.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "common.cuh"
+#include "gate_select.cuh"
 #include "ops.h"
+#include "tc_common.cuh"
 
 namespace moe {
 
 namespace {
 
-struct Args {
-    moe_layer_args a;
-    int T, H, I, E, K, S;
-    float clamp;
-    int32_t* hdr;
-    float *logits, *weights, *act, *slots;
-    int32_t* ids;
+using namespace tc;
+
+constexpr int kWarps = 8;                       // consumers
+constexpr int kAllWarps = 12;                   // warp 8 is the producer, 9-11 only help in the first phases
+constexpr int kThreads = 32 * kAllWarps;
+// registers of warps 8-11 and of the consumers from phase 3 on: 128 * 40 + 256 * 232 = 384 * 168, what the launch holds
+constexpr int kFewRegs = 40, kManyRegs = 232;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "register split");
+constexpr int kMaxT = MOE_LAYER_MAX_TOKENS;
+constexpr int kMaxSlots = kMaxT * 32;
+constexpr int kMaxE = 1024;
+constexpr int kMaxChunks = 8;                   // parts of H in the router product
+
+// Stage geometry. K-contiguous formats: 32 rows x 512 bytes, rows 576 bytes apart (the 16-byte loads of 8 lanes, two rows of
+// 64 bytes, then touch every bank once). BF16: 64 of K x two boxes of 64 columns, 128-byte swizzle.
+template <int kFmt>
+struct Geo {
+    static constexpr bool kBf16 = kFmt == MOE_LAYER_BF16;
+    static constexpr bool kFp4 = kFmt == MOE_LAYER_FP4_MX;
+    static constexpr int kRows = kBf16 ? 128 : 32;  // weight rows of an item
+    static constexpr int kOut1 = kRows / 2;         // outputs of an item of the first product
+    static constexpr int kPitch = 576;
+    static constexpr int kStepK = kBf16 ? 64 : kFp4 ? 1024 : 512;
+    static constexpr int kStageBytes = kBf16 ? 16384 : 32 * kPitch;
+    static constexpr int kStages = 8;
+    static constexpr int kSlices = kBf16 ? 4 : 8;   // parts of K whose sums meet in shared memory
+    static constexpr int kMt = kBf16 ? 4 : 2;       // 16-row MMA tiles of a warp
+    static constexpr int kRedCol = kRows + 4;       // floats of a column of partial sums (two columns apart: 8 banks)
+    static constexpr int kRedSlice = 8 * kRedCol;
+    static constexpr int kRed = kSlices * kRedSlice;
+    // shared memory: ring | two sets of partial sums | y sums | tables
+    static constexpr int kRedOff = kStages * kStageBytes;
+    static constexpr int kTabOff = kRedOff + 2 * 4 * kRed;
 };
 
-// Weight (n, k) of expert e, layer 1 or 2, as fp32.
-template <int kFmt>
-__device__ __forceinline__ float weight(const moe_operand& w, int e, int n, int k, int N, int Kd) {
-    if constexpr (kFmt == MOE_LAYER_BF16) {
-        return bf16_bits_to_float(static_cast<const uint16_t*>(w.data)[((int64_t)e * Kd + k) * N + n]);
-    } else if constexpr (kFmt == MOE_LAYER_FP8_BLOCK) {
-        const float s = static_cast<const float*>(w.scale)[((int64_t)e * (N / 128) + n / 128) * (Kd / 128) + k / 128];
-        return e4m3_to_float(static_cast<const uint8_t*>(w.data)[((int64_t)e * N + n) * Kd + k]) * s;
-    } else {
-        const int64_t row = (int64_t)e * N + n;
-        const uint8_t b = static_cast<const uint8_t*>(w.data)[row * (Kd / 2) + k / 2];
-        return e2m1_to_float(k & 1 ? b >> 4 : b & 15) * ue8m0_to_float(static_cast<const uint8_t*>(w.scale)[row * (Kd / 32) + k / 32]);
-    }
-}
+struct Tables {
+    uint64_t bars[32];
+    int n_active, error, last;
+    int abort;
+    int expert[kMaxE], start[kMaxE + 1];  // active experts and where their rows begin in row[]
+    int count[kMaxE];
+    uint16_t row[kMaxSlots];              // slot = token * (K + S) + k
+    float weight[kMaxSlots];              // by slot
+    int16_t id[kMaxSlots];                // by slot, -1: none
+};
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+struct Args {
+    const uint16_t* x;
+    const void* router;
+    const void *w1, *w2;
+    const void *s1, *s2;
+    const float* bias;
+    int32_t* ids_io;
+    float* weights_io;
+    uint16_t* y;
+    moe_gate_options gate;
+    int router_bf16;
+    int T, H, I, E, K, S;
+    int chunks;  // parts of H in the router product
+    float clamp;
+    int32_t* hdr;      // [0] error word, [1] barrier, [2] CTAs finished
+    int32_t* dep;      // per active expert: finished items of the first product
+    int32_t* cols;     // per column group: parts that have arrived
+    uint32_t* amax;    // per slot: largest |activation| so far, as bits
+    float* logits;     // [chunks][T][E]
+    int32_t* ids;      // [T][K]
+    float* weights;    // [T][K]
+    uint16_t* x16;     // f16 [T][H]
+    float* xinv;       // [T]
+    float* act;        // [slots][I]
+    float* part;       // [CTA][2][T][rows of an item]
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
+// two e4m3 codes -> two f16 (exact)
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+    return r;
+}
+// the two e2m1 codes of byte i -> two f16 (exact), low nibble first
+template <int i>
+__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t word) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b%2;\n\t}" : "=r"(r) : "r"(word), "n"(i));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// 2^-d as f16 twice (d >= 0; 0 below the smallest subnormal)
+__device__ __forceinline__ uint32_t pow2_f16x2(int d) {
+    const uint32_t h = d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+    return h | (h << 16);
+}
+// The power of two that takes magnitudes up to `top` (bits) below 2^15, and its inverse. Zero, infinities and NaNs: 1.
+__device__ __forceinline__ float row_scale(uint32_t top, float* inverse) {
+    int e = (int)(top >> 23);
+    if (top == 0u || e == 255) e = 141;
+    e = max(e, 15);
+    *inverse = __uint_as_float((uint32_t)(e - 14) << 23);     // 2^(e - 141)
+    return __uint_as_float((uint32_t)(268 - e) << 23);        // 2^(141 - e)
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-__global__ void logits_kernel(Args p) {
-    const int w = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x & 31;
-    if (w >= p.T * p.E) return;
-    const int t = w / p.E, e = w % p.E;
-    float sum = 0.0f;
-    for (int h = lane; h < p.H; h += 32) {
-        const float r = p.a.router_type == MOE_TYPE_BF16
-                            ? bf16_bits_to_float(static_cast<const uint16_t*>(p.a.router)[(int64_t)e * p.H + h])
-                            : static_cast<const float*>(p.a.router)[(int64_t)e * p.H + h];
-        sum = fmaf(bf16_bits_to_float(static_cast<const uint16_t*>(p.a.x)[(int64_t)t * p.H + h]), r, sum);
+// All CTAs have arrived n times (n counts the barriers of this launch); one thread waits, bounded.
+__device__ __forceinline__ void grid_barrier(const Args& p, int n, volatile int* abort_flag) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(p.hdr + 1, 1);
+        wait_count(p.hdr + 1, n * (int)gridDim.x, p.hdr, abort_flag);
+        __threadfence();
     }
-    sum = warp_sum(sum);
-    if (lane == 0) p.logits[(int64_t)t * p.E + e] = sum;
+    __syncthreads();
 }
 
-__device__ __forceinline__ int slot_expert(const Args& p, int t, int k) {
-    if (k >= p.K) return p.E + k - p.K;
-    const int e = p.ids[t * p.K + k];
-    if (e < -1 || e >= p.E) {
-        record_error(p.hdr, MOE_ERR_BAD_ROUTE);
-        return -1;
+// ---------------------------------------------------------------------------------------
+// phase 1: the router product
+// ---------------------------------------------------------------------------------------
+
+// Dot products of one expert's router row with 8 tokens over vectors [v0, v1) of 8 values.
+template <bool kRouterBf16>
+__device__ __forceinline__ void router_dots(const Args& p, int e, int t0, int v0, int v1, int lane, float (&sum)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    for (int v = v0 + lane; v < v1; v += 32) {
+        float r[8];
+        if constexpr (kRouterBf16) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.router) + (int64_t)e * p.H) + v);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r[2 * i] = __uint_as_float(u[i] << 16);
+                r[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        } else {
+            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.router) + (int64_t)e * p.H) + 2 * v;
+            const float4 a = __ldg(q), b = __ldg(q + 1);
+            r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (t0 + j >= p.T) break;
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + j) * p.H) + v);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum[j] = fmaf(__uint_as_float(u[i] << 16), r[2 * i], sum[j]);
+                sum[j] = fmaf(__uint_as_float(u[i] & 0xffff0000u), r[2 * i + 1], sum[j]);
+            }
+        }
     }
-    return e;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+}
+
+__device__ void router_phase(const Args& p, int warp, int lane) {
+    const int vecs = p.H / 8, per = (vecs + p.chunks - 1) / p.chunks, groups = (p.T + 7) / 8;
+    const int units = p.E * p.chunks * groups;
+    for (int u = blockIdx.x + warp * gridDim.x; u < units; u += gridDim.x * kAllWarps) {
+        const int e = u % p.E, c = u / p.E % p.chunks, t0 = u / (p.E * p.chunks) * 8;
+        float sum[8];
+        const int v0 = c * per, v1 = min(vecs, v0 + per);
+        if (p.router_bf16) router_dots<true>(p, e, t0, v0, v1, lane, sum);
+        else router_dots<false>(p, e, t0, v0, v1, lane, sum);
+        if (lane == 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (t0 + j < p.T) p.logits[((int64_t)c * p.T + t0 + j) * p.E + e] = sum[j];
+    }
+}
+
+// x of one token as f16, scaled by a power of two (all threads of the CTA).
+__device__ void round_x(const Args& p, int t, uint32_t* scratch) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.H);
+    uint32_t top = 0;
+    for (int v = threadIdx.x; v < p.H / 8; v += kThreads) {
+        const uint4 w = __ldg(src + v);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7fff0000u, (u[i] << 16) & 0x7fff0000u));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAllWarps; ++i) top = max(top, scratch[i]);
+    float inverse;
+    const float s = row_scale(top, &inverse);
+    uint4* dst = reinterpret_cast<uint4*>(p.x16 + (int64_t)t * p.H);
+    for (int v = threadIdx.x; v < p.H / 8; v += kThreads) {
+        const uint4 w = __ldg(src + v);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_f16(__uint_as_float(u[i] << 16) * s, __uint_as_float(u[i] & 0xffff0000u) * s);
+        dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (threadIdx.x == 0) p.xinv[t] = inverse;
+}
+
+// ---------------------------------------------------------------------------------------
+// phase 2: selection and the list of experts
+// ---------------------------------------------------------------------------------------
+
+template <int kV>
+__device__ void select_token(const Args& p, int t, float* scratch, int lane, int32_t* ids, float* weights) {
+    float v[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = i * 32 + lane < p.E ? 0.0f : -INFINITY;
+    for (int c = 0; c < p.chunks; ++c)
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const int e = i * 32 + lane;
+            if (e < p.E) v[i] += __ldcg(p.logits + ((int64_t)c * p.T + t) * p.E + e);
+        }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = v[i] == v[i] ? v[i] : -INFINITY;
+    gate_token<kV>(v, p.bias, p.gate, p.E, p.K, scratch, lane, ids, weights);
+}
+
+// ids and weights (of the routed slots) -> the experts with rows, in order, and their rows.
+__device__ void list_experts(const Args& p, Tables& tb, const int32_t* ids, const float* weights, bool cg) {
+    const int Kt = p.K + p.S, Et = p.E + p.S, slots = p.T * Kt;
+    for (int e = threadIdx.x; e < Et; e += kThreads) tb.count[e] = 0;
+    for (int s = threadIdx.x; s < slots; s += kThreads) {
+        const int t = s / Kt, k = s % Kt;
+        int e;
+        float w = 1.0f;
+        if (k >= p.K) {
+            e = p.E + k - p.K;
+        } else {
+            auto id = [&](int i) { return cg ? __ldcg(ids + t * p.K + i) : ids[t * p.K + i]; };
+            auto wt = [&](int i) { return cg ? __ldcg(weights + t * p.K + i) : weights[t * p.K + i]; };
+            e = id(k);
+            w = wt(k);
+            if (e < -1 || e >= p.E) {
+                record_error(p.hdr, MOE_ERR_BAD_ROUTE);
+                e = -1;
+            }
+            // an expert named twice by a token: one row with the sum of the weights
+            if (e >= 0) {
+                for (int i = 0; i < k && e >= 0; ++i)
+                    if (id(i) == e) e = -1;
+                if (e >= 0)
+                    for (int i = k + 1; i < p.K; ++i)
+                        if (id(i) == e) w += wt(i);
+            }
+        }
+        tb.id[s] = (int16_t)e;
+        tb.weight[s] = w;
+    }
+    __syncthreads();
+    // place within the expert in any order: rows are independent of each other
+    for (int s = threadIdx.x; s < slots; s += kThreads) {
+        const int e = tb.id[s];
+        if (e >= 0) atomicAdd(&tb.count[e], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int active = 0, rows = 0;
+        for (int b = 0; b < Et; b += 32) {
+            const int e = b + lane;
+            const int n = e < Et ? tb.count[e] : 0;
+            const uint32_t on = __ballot_sync(0xffffffffu, n > 0);
+            int sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += u;
+            }
+            if (n > 0) {
+                const int a = active + __popc(on & ((1u << lane) - 1u));
+                tb.expert[a] = e;
+                tb.start[a] = rows + sum - n;
+            }
+            if (e < Et) tb.count[e] = rows + sum - n;  // the next free place
+            active += __popc(on);
+            rows += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) {
+            tb.n_active = active;
+            tb.start[active] = rows;
+        }
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < slots; s += kThreads) {
+        const int e = tb.id[s];
+        if (e >= 0) tb.row[atomicAdd(&tb.count[e], 1)] = (uint16_t)s;
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------------------
+// phases 3 and 4
+// ---------------------------------------------------------------------------------------
+
+// The items of a CTA in order: those of the first product (dealt in turn), then its run of the second.
+template <int kFmt>
+struct Work {
+    int per1, n1;       // items of the first product per expert, in all
+    int n_active;
+    int lo2, hi2;       // this CTA's run of the second product: item = column group * n_active + expert
+    __device__ Work(const Args& p, int active) {
+        per1 = p.I / Geo<kFmt>::kOut1;
+        n_active = active;
+        n1 = per1 * active;
+        lo2 = first(p, active, blockIdx.x);
+        hi2 = first(p, active, blockIdx.x + 1);
+    }
+    static __device__ int first(const Args& p, int active, int cta) {
+        return (int)((int64_t)(p.H / Geo<kFmt>::kRows) * active * cta / (int)gridDim.x);
+    }
+    // the CTA whose run holds item i
+    static __device__ int owner(const Args& p, int active, int i) {
+        const int64_t n = (int64_t)(p.H / Geo<kFmt>::kRows) * active;
+        int c = (int)((int64_t)i * (int)gridDim.x / n);
+        while (first(p, active, c + 1) <= i) ++c;
+        while (first(p, active, c) > i) --c;
+        return c;
+    }
+};
+
+template <int kFmt>
+struct Ring {
+    uint32_t base, bars;
+    int it = 0;
+    __device__ uint32_t full(int s) const { return bars + 8u * s; }
+    __device__ uint32_t empty(int s) const { return bars + 8u * (Geo<kFmt>::kStages + s); }
+};
+
+// One item's stages, by the producer warp.
+template <int kFmt, bool kSecond>
+__device__ __forceinline__ bool produce(const Args& p, const CUtensorMap* map, Ring<kFmt>& ring, int expert, int r0, int lane,
+                                        volatile int* abort_flag) {
+    using G = Geo<kFmt>;
+    const int K = kSecond ? p.I : p.H, N = kSecond ? p.H : 2 * p.I;
+    const int steps = (K + G::kStepK - 1) / G::kStepK;
+    for (int st = 0; st < steps; ++st, ++ring.it) {
+        const int s = ring.it % G::kStages;
+        const bool ok = mbar_wait(ring.empty(s), ((uint32_t)(ring.it / G::kStages) & 1u) ^ 1u, p.hdr, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        const uint32_t dst = ring.base + (uint32_t)(s * G::kStageBytes);
+        if constexpr (G::kBf16) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(ring.full(s), 16384);
+                const int y = expert * K + st * 64;
+                tma_load_2d(dst, map, r0, y, ring.full(s));
+                tma_load_2d(dst + 8192, map, kSecond ? r0 + 64 : p.I + r0, y, ring.full(s));
+            }
+        } else {
+            const int row_bytes = G::kFp4 ? K / 2 : K;
+            const int bytes = min(512, row_bytes - st * 512);
+            // rows 0-7 and 16-23 of an item of the first product are gate rows, the others the up rows of the same outputs
+            const int row = kSecond ? r0 + lane : ((lane & 8) ? p.I : 0) + r0 + (lane >> 4) * 8 + (lane & 7);
+            const uint8_t* src = static_cast<const uint8_t*>(kSecond ? p.w2 : p.w1) + ((int64_t)expert * N + row) * row_bytes + st * 512;
+            if (lane == 0) mbar_arrive_expect_tx(ring.full(s), 32u * (uint32_t)bytes);
+            __syncwarp();
+            bulk_load(dst + (uint32_t)(lane * G::kPitch), src, (uint32_t)bytes, ring.full(s));
+        }
+    }
+    return true;
+}
+
+// One column tile's values for a warp's part of a stage: B words as they are in memory (fp32 activations: two to a word of B).
+template <int kFmt, bool kSecond>
+struct Columns {
+    using G = Geo<kFmt>;
+    static constexpr int kB = G::kBf16 ? 2 : G::kFp4 ? 16 : 8;  // 16-bit pairs of the tile
+    static constexpr int kWords = kSecond ? 2 * kB : kB;
+    uint32_t w[kWords];
+
+    // row: the x row or activation row of this lane's column, or null
+    __device__ __forceinline__ void load(const void* row, int k, int lane) {
+        if constexpr (G::kBf16) {
+            const int at = k + 2 * (lane & 3);
+            if constexpr (kSecond) {
+                const float* q = static_cast<const float*>(row) + at;
+                const float2 u = row ? *reinterpret_cast<const float2*>(q) : make_float2(0.0f, 0.0f);
+                const float2 v = row ? *reinterpret_cast<const float2*>(q + 8) : make_float2(0.0f, 0.0f);
+                w[0] = __float_as_uint(u.x), w[1] = __float_as_uint(u.y);
+                w[2] = __float_as_uint(v.x), w[3] = __float_as_uint(v.y);
+            } else {
+                const uint16_t* q = static_cast<const uint16_t*>(row) + at;
+                w[0] = row ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+                w[1] = row ? *reinterpret_cast<const uint32_t*>(q + 8) : 0u;
+            }
+        } else {
+            const int at = k + (G::kFp4 ? 32 : 16) * (lane & 3);
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (kSecond ? 4 : 2) * (int64_t)at);
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = row ? q[i] : make_uint4(0, 0, 0, 0);
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        }
+    }
+};
+
+// The weight scales of a warp's part of a stage. FP8: of the item's two 128-row blocks (gate, up). FP4: four bytes, one for
+// each 32 of K, of the rows g and g + 8 of both 16-row tiles.
+template <int kFmt, bool kSecond>
+struct Scales {
+    using G = Geo<kFmt>;
+    uint32_t s[G::kFp4 ? 4 : 2];
+    __device__ __forceinline__ void load(const Args& p, int k, int K, int expert, int r0, int lane) {
+        const int N = kSecond ? p.H : 2 * p.I;
+        if constexpr (G::kFp4) {
+            const uint8_t* q = static_cast<const uint8_t*>(kSecond ? p.s2 : p.s1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 8 + (lane >> 2);
+                const int row = kSecond ? r0 + r : ((r & 8) ? p.I : 0) + r0 + (r >> 4) * 8 + (r & 7);
+                s[i] = __ldg(reinterpret_cast<const uint32_t*>(q + ((int64_t)expert * N + row) * (K / 32) + k / 32));
+            }
+        } else if constexpr (!G::kBf16) {
+            const float* q = static_cast<const float*>(kSecond ? p.s2 : p.s1) + (int64_t)expert * (N / 128) * (K / 128) + k / 128;
+            s[0] = __float_as_uint(__ldg(q + (int64_t)(r0 / 128) * (K / 128)));
+            s[1] = kSecond ? s[0] : __float_as_uint(__ldg(q + (int64_t)((p.I + r0) / 128) * (K / 128)));
+        }
+    }
+};
+
+// The sums of one item over its K: the stages' weights times the rows. acc[m][n]: 16-row tile m, 8-column tile n.
+template <int kFmt, bool kSecond, int NT>
+__device__ __forceinline__ void multiply(const Args& p, Ring<kFmt> ring, const void* const (&rows)[NT], const float (&ascale)[NT],
+                                         int expert, int r0, int warp, int lane, volatile int* abort_flag,
+                                         float (&acc)[Geo<kFmt>::kMt][NT][4]) {
+    using G = Geo<kFmt>;
+    using Cols = Columns<kFmt, kSecond>;
+    const int K = kSecond ? p.I : p.H;
+    const int steps = (K + G::kStepK - 1) / G::kStepK;
+    constexpr int kSliceK = G::kStepK / G::kSlices;  // K of a warp in a stage
+    const int off = (G::kBf16 ? warp & 3 : warp) * kSliceK;
+    // the next stage's columns are loaded during this one while registers last
+    constexpr bool kAhead = NT * Cols::kWords <= 32;
+#pragma unroll
+    for (int m = 0; m < G::kMt; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+    Cols cols[kAhead ? NT : 1], next[kAhead ? NT : 1];
+    Scales<kFmt, kSecond> sc, sc_next;
+    if (off < K) {
+        sc.load(p, off, K, expert, r0, lane);
+        if constexpr (kAhead)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cols[n].load(rows[n], off, lane);
+    }
+    for (int st = 0; st < steps; ++st, ++ring.it) {
+        const int s = ring.it % G::kStages, k = st * G::kStepK + off;
+        const bool on = k < K;
+        if (k + G::kStepK < K) {
+            sc_next.load(p, k + G::kStepK, K, expert, r0, lane);
+            if constexpr (kAhead)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) next[n].load(rows[n], k + G::kStepK, lane);
+        }
+        // a wait that ran out skips the stage: the warps still meet at the barriers that follow
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(ring.full(s), (uint32_t)(ring.it / G::kStages) & 1u, p.hdr, abort_flag));
+        const uint32_t stage = ring.base + (uint32_t)(s * G::kStageBytes);
+        if (on && ok) {
+            // the weights as MMA operands: a[m][j] for the j-th 16 of K
+            constexpr int kMmas = Cols::kB / 2;
+            uint32_t a[G::kMt][kMmas][4];
+            float f0[G::kMt], f1[G::kMt];  // scales of the sums of rows g and g + 8
+#pragma unroll
+            for (int m = 0; m < G::kMt; ++m) {
+                f0[m] = f1[m] = 1.0f;
+                if constexpr (G::kBf16) {
+                    // [K row][64 columns] boxes: lane l gives row l % 8 (+ 8 for matrices 2, 3) and columns + 8 for 1, 3
+                    const int krow = off + (lane & 7) + ((lane >> 4) & 1) * 8, c8 = (lane >> 3) & 1;
+                    ldmatrix_x4_trans(a[m][0], stage + (uint32_t)((warp >> 2) * 8192 + krow * 128 + (((2 * m + c8) ^ (krow & 7)) << 4)));
+                } else {
+                    const uint32_t at = stage + (uint32_t)((m * 16 + (lane >> 2)) * G::kPitch + warp * 64 + (lane & 3) * 16);
+                    const uint4 u = lds128(at), v = lds128(at + 8 * G::kPitch);  // rows g and g + 8
+                    const uint32_t ug[4] = {u.x, u.y, u.z, u.w}, vg[4] = {v.x, v.y, v.z, v.w};
+                    if constexpr (G::kFp4) {
+                        // this lane's codes relative to the largest scale of the four blocks
+                        auto most = [](uint32_t w) { return max(max(w & 255u, (w >> 8) & 255u), max((w >> 16) & 255u, w >> 24)); };
+                        const uint32_t w0 = sc.s[2 * m], w1 = sc.s[2 * m + 1], m0 = most(w0), m1 = most(w1);
+                        const uint32_t p0 = pow2_f16x2((int)(m0 - ((w0 >> (8 * (lane & 3))) & 255u)));
+                        const uint32_t p1 = pow2_f16x2((int)(m1 - ((w1 >> (8 * (lane & 3))) & 255u)));
+                        f0[m] = ue8m0_to_float((uint8_t)m0);
+                        f1[m] = ue8m0_to_float((uint8_t)m1);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            a[m][2 * q][0] = mul_f16x2(e2m1x2_f16x2<0>(ug[q]), p0);
+                            a[m][2 * q][1] = mul_f16x2(e2m1x2_f16x2<0>(vg[q]), p1);
+                            a[m][2 * q][2] = mul_f16x2(e2m1x2_f16x2<1>(ug[q]), p0);
+                            a[m][2 * q][3] = mul_f16x2(e2m1x2_f16x2<1>(vg[q]), p1);
+                            a[m][2 * q + 1][0] = mul_f16x2(e2m1x2_f16x2<2>(ug[q]), p0);
+                            a[m][2 * q + 1][1] = mul_f16x2(e2m1x2_f16x2<2>(vg[q]), p1);
+                            a[m][2 * q + 1][2] = mul_f16x2(e2m1x2_f16x2<3>(ug[q]), p0);
+                            a[m][2 * q + 1][3] = mul_f16x2(e2m1x2_f16x2<3>(vg[q]), p1);
+                        }
+                    } else {
+                        f0[m] = __uint_as_float(sc.s[0]);
+                        f1[m] = __uint_as_float(sc.s[1]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            a[m][q][0] = e4m3x2_f16x2(ug[q]);
+                            a[m][q][1] = e4m3x2_f16x2(vg[q]);
+                            a[m][q][2] = e4m3x2_f16x2(ug[q] >> 16);
+                            a[m][q][3] = e4m3x2_f16x2(vg[q] >> 16);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if constexpr (!kAhead) cols[0].load(rows[n], k, lane);
+                const Cols& c = cols[kAhead ? n : 0];
+                if constexpr (G::kBf16) {
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (kSecond) {
+                            const float u = __uint_as_float(c.w[2 * i]), v = __uint_as_float(c.w[2 * i + 1]);
+                            hi[i] = pack_bf16(u, v);
+                            // an infinity or NaN stays in the high part alone
+                            const float du = u - __uint_as_float(hi[i] << 16), dv = v - __uint_as_float(hi[i] & 0xffff0000u);
+                            lo[i] = pack_bf16(fabsf(u) < INFINITY ? du : 0.0f, fabsf(v) < INFINITY ? dv : 0.0f);
+                        } else {
+                            hi[i] = c.w[i];
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < G::kMt; ++m) {
+                        mma_bf16(acc[m][n], a[m][0], hi[0], hi[1]);
+                        if constexpr (kSecond) mma_bf16(acc[m][n], a[m][0], lo[0], lo[1]);
+                    }
+                } else {
+                    uint32_t bw[Cols::kB];
+#pragma unroll
+                    for (int i = 0; i < Cols::kB; ++i) {
+                        if constexpr (kSecond)
+                            bw[i] = pack_f16(__uint_as_float(c.w[2 * i]) * ascale[n], __uint_as_float(c.w[2 * i + 1]) * ascale[n]);
+                        else
+                            bw[i] = c.w[i];
+                    }
+#pragma unroll
+                    for (int m = 0; m < G::kMt; ++m) {
+                        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int j = 0; j < kMmas; ++j) mma_f16(part, a[m][j], bw[2 * j], bw[2 * j + 1]);
+                        acc[m][n][0] = fmaf(part[0], f0[m], acc[m][n][0]);
+                        acc[m][n][1] = fmaf(part[1], f0[m], acc[m][n][1]);
+                        acc[m][n][2] = fmaf(part[2], f1[m], acc[m][n][2]);
+                        acc[m][n][3] = fmaf(part[3], f1[m], acc[m][n][3]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.empty(s));
+        sc = sc_next;
+        if constexpr (kAhead)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cols[n] = next[n];
+    }
+}
+
+struct Shared {
+    float* red;    // two sets of partial sums
+    float* y;      // [T][rows of an item]
+    Tables* tb;
+    int red_at = 0;
+};
+
+// A warp's sums of column tile n to the next set of partial sums, and wait for everybody's.
+template <int kFmt, int NT>
+__device__ __forceinline__ const float* gather(Shared& sh, const float (&acc)[Geo<kFmt>::kMt][NT][4], int n, int warp, int lane) {
+    using G = Geo<kFmt>;
+    float* red = sh.red + sh.red_at * G::kRed;
+    sh.red_at ^= 1;
+    float* dst = red + (G::kBf16 ? warp & 3 : warp) * G::kRedSlice + (G::kBf16 ? (warp >> 2) * 64 : 0);
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int m = 0; m < G::kMt; ++m) {
+        dst[(2 * t) * G::kRedCol + m * 16 + g] = acc[m][n][0];
+        dst[(2 * t + 1) * G::kRedCol + m * 16 + g] = acc[m][n][1];
+        dst[(2 * t) * G::kRedCol + m * 16 + g + 8] = acc[m][n][2];
+        dst[(2 * t + 1) * G::kRedCol + m * 16 + g + 8] = acc[m][n][3];
+    }
+    consumer_sync();
+    return red;
+}
+template <int kFmt>
+__device__ __forceinline__ float red_sum(const float* red, int col, int row) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Geo<kFmt>::kSlices; ++i) s += red[i * Geo<kFmt>::kRedSlice + col * Geo<kFmt>::kRedCol + row];
+    return s;
+}
+
+// An item of the first product: outputs [r0, r0 + kOut1) of active expert a for its rows.
+template <int kFmt, int NT>
+__device__ __forceinline__ void first_item(const Args& p, Ring<kFmt> ring, Shared sh, int a, int r0, int warp, int lane,
+                                        volatile int* abort_flag) {
+    using G = Geo<kFmt>;
+    Tables& tb = *sh.tb;
+    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, Kt = p.K + p.S;
+    const void* rows[NT];
+    float ascale[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int c = n * 8 + (lane >> 2);
+        rows[n] = nullptr;
+        ascale[n] = 1.0f;
+        if (c < n_rows) rows[n] = (G::kBf16 ? p.x : p.x16) + (int64_t)(tb.row[begin + c] / Kt) * p.H;
+    }
+    float acc[G::kMt][NT][4];
+    multiply<kFmt, false, NT>(p, ring, rows, ascale, tb.expert[a], r0, warp, lane, abort_flag, acc);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float* red = gather<kFmt, NT>(sh, acc, n, warp, lane);
+        // warp w: column w of the tile
+        const int c = n * 8 + warp;
+        const bool on = c < n_rows;
+        const int slot = on ? tb.row[begin + c] : 0;
+        const float inv = G::kBf16 || !on ? 1.0f : __ldcg(p.xinv + slot / Kt);
+        uint32_t top = 0;
+        float* dst = p.act + (int64_t)slot * p.I + r0;
+        if constexpr (G::kBf16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = i * 32 + lane;
+                const float v = swiglu1(red_sum<kFmt>(red, warp, j), red_sum<kFmt>(red, warp, 64 + j), p.clamp);
+                if (on) dst[j] = v;
+            }
+        } else {
+            // rows 0-7, 16-23: gate; 8-15, 24-31: up of the same outputs
+            const float h = red_sum<kFmt>(red, warp, lane) * inv;
+            const float u = __shfl_down_sync(0xffffffffu, h, 8);
+            const bool gate = !(lane & 8);
+            const float v = swiglu1(h, u, p.clamp);
+            if (on && gate) dst[(lane >> 4) * 8 + (lane & 7)] = v;
+            top = __reduce_max_sync(0xffffffffu, gate ? __float_as_uint(v) & 0x7fffffffu : 0u);
+            if (on && lane == 0) atomicMax(p.amax + slot, top);
+        }
+    }
+    consumer_sync();  // every warp's values are written
+    if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(p.dep + a, 1);
+    }
+}
+
+// An item of the second product: hidden columns [r0, r0 + kRows) of active expert a, added to the CTA's sums.
+template <int kFmt, int NT>
+__device__ __forceinline__ void second_item(const Args& p, Ring<kFmt> ring, Shared sh, int a, int r0, int warp, int lane,
+                                         volatile int* abort_flag) {
+    using G = Geo<kFmt>;
+    Tables& tb = *sh.tb;
+    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, Kt = p.K + p.S;
+    const void* rows[NT];
+    float ascale[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int c = n * 8 + (lane >> 2);
+        rows[n] = nullptr;
+        ascale[n] = 1.0f;
+        if (c < n_rows) {
+            const int slot = tb.row[begin + c];
+            rows[n] = p.act + (int64_t)slot * p.I;
+            float inverse;
+            if constexpr (!G::kBf16) ascale[n] = row_scale(__ldcg(p.amax + slot), &inverse);
+        }
+    }
+    float acc[G::kMt][NT][4];
+    multiply<kFmt, true, NT>(p, ring, rows, ascale, tb.expert[a], r0, warp, lane, abort_flag, acc);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float* red = gather<kFmt, NT>(sh, acc, n, warp, lane);
+        const int c = n * 8 + warp;
+        if (c < n_rows) {
+            const int slot = tb.row[begin + c];
+            float w = tb.weight[slot];
+            if constexpr (!G::kBf16) {
+                float inverse;
+                row_scale(__ldcg(p.amax + slot), &inverse);
+                float* y = sh.y + (slot / Kt) * G::kRows + lane;
+                *y = fmaf(red_sum<kFmt>(red, warp, lane) * inverse, w, *y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < G::kRows / 32; ++i) {
+                    float* y = sh.y + (slot / Kt) * G::kRows + i * 32 + lane;
+                    *y = fmaf(red_sum<kFmt>(red, warp, i * 32 + lane), w, *y);
+                }
+            }
+        }
+    }
+}
+
+template <int kFmt, bool kSecond>
+__device__ __forceinline__ void run_item(const Args& p, Ring<kFmt>& at, Shared& now, int a, int r0, int warp, int lane,
+                                         volatile int* abort_flag) {
+    const int n = now.tb->start[a + 1] - now.tb->start[a];
+    const Ring<kFmt> ring = at;
+    const Shared sh = now;
+    at.it += ((kSecond ? p.I : p.H) + Geo<kFmt>::kStepK - 1) / Geo<kFmt>::kStepK;
+    if (n <= 8) now.red_at ^= 1;  // one set of partial sums a column tile: 1, 2, 4 or 8
+    if constexpr (kSecond) {
+        if (n <= 8) return second_item<kFmt, 1>(p, ring, sh, a, r0, warp, lane, abort_flag);
+        if (n <= 16) return second_item<kFmt, 2>(p, ring, sh, a, r0, warp, lane, abort_flag);
+        if (n <= 32) return second_item<kFmt, 4>(p, ring, sh, a, r0, warp, lane, abort_flag);
+        return second_item<kFmt, 8>(p, ring, sh, a, r0, warp, lane, abort_flag);
+    } else {
+        if (n <= 8) return first_item<kFmt, 1>(p, ring, sh, a, r0, warp, lane, abort_flag);
+        if (n <= 16) return first_item<kFmt, 2>(p, ring, sh, a, r0, warp, lane, abort_flag);
+        if (n <= 32) return first_item<kFmt, 4>(p, ring, sh, a, r0, warp, lane, abort_flag);
+        return first_item<kFmt, 8>(p, ring, sh, a, r0, warp, lane, abort_flag);
+    }
+}
+
+// The CTA's sums of column group g are complete as far as its run goes: to y, or to the workspace where other CTAs have
+// experts of these columns too.
+template <int kFmt>
+__device__ void finish_columns(const Args& p, Shared& sh, const Work<kFmt>& wk, int g) {
+    using G = Geo<kFmt>;
+    constexpr int R = G::kRows;
+    const int first = g * wk.n_active, last = first + wk.n_active - 1, n = p.T * R;
+    consumer_sync();  // the last item's sums are in place
+    if (wk.lo2 <= first && wk.hi2 > last) {
+        for (int i = threadIdx.x; i < n; i += 256) {
+            p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(sh.y[i]);
+            sh.y[i] = 0.0f;
+        }
+        return;
+    }
+    // the CTAs with experts of these columns, in order (with fewer items than CTAs, some in between have none)
+    if (threadIdx.x == 0) {
+        int parts = 0;
+        for (int i = first; i <= last; ++parts) {
+            const int c = Work<kFmt>::owner(p, wk.n_active, i);
+            sh.tb->count[parts] = c;
+            i = Work<kFmt>::first(p, wk.n_active, c + 1);
+        }
+        sh.tb->last = parts;
+    }
+    consumer_sync();
+    const int parts = sh.tb->last;
+    // a CTA's first column group goes to its first buffer, its last to the second
+    auto buffer = [&](int cta) {
+        const int at = Work<kFmt>::first(p, wk.n_active, cta);
+        return p.part + ((int64_t)cta * 2 + (at / wk.n_active == g ? 0 : 1)) * kMaxT * R;
+    };
+    float* mine = buffer(blockIdx.x);
+    for (int i = threadIdx.x; i < n; i += 256) {
+        mine[i] = sh.y[i];
+        sh.y[i] = 0.0f;
+    }
+    consumer_sync();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        // counts up to the last part and is zero again then
+        sh.tb->last = atomicInc(reinterpret_cast<unsigned*>(p.cols) + g, (unsigned)(parts - 1)) == (unsigned)(parts - 1);
+        __threadfence();
+    }
+    consumer_sync();
+    if (!sh.tb->last) return;
+    for (int i = threadIdx.x; i < n; i += 256) {
+        float s = 0.0f;
+        for (int c = 0; c < parts; ++c) s += __ldcg(buffer(sh.tb->count[c]) + i);
+        p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(s);
+    }
 }
 
 template <int kFmt>
-__global__ void up_kernel(Args p) {
-    const int w = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x & 31;
-    const int Kt = p.K + p.S;
-    if (w >= p.T * Kt * p.I) return;
-    const int slot = w / p.I, j = w % p.I, t = slot / Kt;
-    const int e = slot_expert(p, t, slot % Kt);
-    if (e < 0) return;
-    float g = 0.0f, u = 0.0f;
-    for (int h = lane; h < p.H; h += 32) {
-        const float x = bf16_bits_to_float(static_cast<const uint16_t*>(p.a.x)[(int64_t)t * p.H + h]);
-        g = fmaf(x, weight<kFmt>(p.a.w1, e, j, h, 2 * p.I, p.H), g);
-        u = fmaf(x, weight<kFmt>(p.a.w1, e, p.I + j, h, 2 * p.I, p.H), u);
+__global__ void __launch_bounds__(kThreads, 1)
+    layer_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2,
+                 const __grid_constant__ Args p) {
+    using G = Geo<kFmt>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    Tables& tb = *reinterpret_cast<Tables*>(smem + G::kTabOff);
+    Shared sh;
+    sh.red = reinterpret_cast<float*>(smem + G::kRedOff);
+    sh.tb = &tb;
+    sh.y = reinterpret_cast<float*>(smem + G::kTabOff + ((sizeof(Tables) + 15) & ~size_t(15)));
+    volatile int* abort_flag = &tb.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Ring<kFmt> ring;
+    ring.base = base;
+    ring.bars = smem_u32(tb.bars);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(ring.full(s), 1);
+            mbar_init(ring.empty(s), kWarps);
+        }
+        tb.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    g = warp_sum(g);
-    u = warp_sum(u);
-    if (lane == 0) p.act[(int64_t)slot * p.I + j] = swiglu1(g, u, p.clamp);
-}
+    for (int i = threadIdx.x; i < p.T * G::kRows; i += kThreads) sh.y[i] = 0.0f;
+    __syncthreads();
 
-template <int kFmt>
-__global__ void down_kernel(Args p) {
-    const int w = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x & 31;
-    const int Kt = p.K + p.S;
-    if (w >= p.T * p.H) return;
-    const int t = w / p.H, h = w % p.H;
-    float y = 0.0f;
-    for (int k = 0; k < Kt; ++k) {
-        const int e = slot_expert(p, t, k);
-        if (e < 0) continue;
-        float sum = 0.0f;
-        for (int i = lane; i < p.I; i += 32)
-            sum = fmaf(p.act[(int64_t)(t * Kt + k) * p.I + i], weight<kFmt>(p.a.w2, e, h, i, p.H, p.I), sum);
-        sum = warp_sum(sum);
-        y += k < p.K ? p.weights[t * p.K + k] * sum : sum;
+    // ---- phase 1
+    int barriers = 0;
+    if (p.router) router_phase(p, warp, lane);
+    if constexpr (!G::kBf16)
+        for (int t = (int)gridDim.x - 1 - (int)blockIdx.x; t < p.T; t += gridDim.x)
+            round_x(p, t, reinterpret_cast<uint32_t*>(sh.red));
+    if (p.router || !G::kBf16) grid_barrier(p, ++barriers, abort_flag);
+
+    // ---- phase 2
+    const int32_t* ids = p.ids_io;
+    const float* weights = p.weights_io;
+    if (p.router) {
+        const bool all = p.T <= kWarps;  // every CTA selects for all tokens
+        int32_t* to_ids = all ? reinterpret_cast<int32_t*>(sh.red) : p.ids;
+        float* to_w = all ? sh.red + kWarps * 32 : p.weights;
+        float* scratch = reinterpret_cast<float*>(smem) + warp * (kMaxE + 32);
+        const int t0 = all ? warp : (int)blockIdx.x + warp * (int)gridDim.x;
+        if (warp < kWarps && t0 < p.T) {
+            if (p.E <= 256) select_token<8>(p, t0, scratch, lane, to_ids + t0 * p.K, to_w + t0 * p.K);
+            else select_token<32>(p, t0, scratch, lane, to_ids + t0 * p.K, to_w + t0 * p.K);
+        }
+        if (all) __syncthreads();
+        else grid_barrier(p, ++barriers, abort_flag);
+        ids = to_ids;
+        weights = to_w;
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < p.T * p.K; i += kThreads) {
+                if (p.ids_io) p.ids_io[i] = all ? ids[i] : __ldcg(ids + i);
+                if (p.weights_io) p.weights_io[i] = all ? weights[i] : __ldcg(weights + i);
+            }
+        list_experts(p, tb, ids, weights, !all);
+    } else {
+        list_experts(p, tb, ids, weights, true);
     }
-    if (lane == 0) static_cast<uint16_t*>(p.a.y)[(int64_t)t * p.H + h] = float_to_bf16_bits(y);
-}
+    // the ring's memory was scratch until here: ordered before the copies that fill it
+    fence_proxy_async_smem();
+    __syncthreads();
+    const Work<kFmt> wk(p, tb.n_active);
 
-template <int kFmt>
-cudaError_t launch_ffn(const Args& p, cudaStream_t s) {
-    up_kernel<kFmt><<<(unsigned)(((int64_t)p.T * (p.K + p.S) * p.I + 7) / 8), 256, 0, s>>>(p);
-    down_kernel<kFmt><<<(unsigned)(((int64_t)p.T * p.H + 7) / 8), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    // ---- phases 3 and 4
+    if (warp >= kWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        bool ok = warp == kWarps;
+        for (int i = blockIdx.x; i < wk.n1 && ok; i += gridDim.x)
+            ok = produce<kFmt, false>(p, &map1, ring, tb.expert[i / wk.per1], i % wk.per1 * G::kOut1, lane, abort_flag);
+        for (int i = wk.lo2; i < wk.hi2 && ok; ++i)
+            ok = produce<kFmt, true>(p, &map2, ring, tb.expert[i % wk.n_active], i / wk.n_active * G::kRows, lane, abort_flag);
+        // drain: every copy issued has landed (bounded)
+        for (int j = max(0, ring.it - G::kStages); j < ring.it; ++j)
+            if (!mbar_drain(ring.full(j % G::kStages), (uint32_t)(j / G::kStages) & 1u, p.hdr)) break;
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        for (int i = blockIdx.x; i < wk.n1; i += gridDim.x)
+            run_item<kFmt, false>(p, ring, sh, i / wk.per1, i % wk.per1 * G::kOut1, warp, lane, abort_flag);
+        for (int i = wk.lo2; i < wk.hi2; ++i) {
+            const int a = i % wk.n_active, g = i / wk.n_active;
+            if (i - wk.lo2 < wk.n_active) {  // the run's first item of this expert: wait for its rows
+                if (threadIdx.x == 0) {
+                    wait_count(p.dep + a, wk.per1, p.hdr, abort_flag);
+                    __threadfence();
+                }
+                consumer_sync();
+            }
+            run_item<kFmt, true>(p, ring, sh, a, g * G::kRows, warp, lane, abort_flag);
+            if (i + 1 == wk.hi2 || (i + 1) % wk.n_active == 0) finish_columns<kFmt>(p, sh, wk, g);
+        }
+    }
+    if (wk.n_active == 0)
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (int64_t)p.T * p.H; i += (int64_t)gridDim.x * kThreads)
+            p.y[i] = 0;
+
+    // ---- the last CTA leaves the counters at zero
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        tb.last = atomicInc(reinterpret_cast<unsigned*>(p.hdr) + 2, gridDim.x - 1) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (tb.last) {
+        for (int i = threadIdx.x; i < tb.n_active; i += kThreads) p.dep[i] = 0;
+        for (int i = threadIdx.x; i < p.T * (p.K + p.S); i += kThreads) p.amax[i] = 0u;
+        if (threadIdx.x == 0) p.hdr[1] = 0;
+    }
 }
 
 size_t align_up(size_t v) { return (v + 255) & ~size_t(255); }
 
+template <int kFmt>
+constexpr size_t smem_bytes(int T) {
+    return 1024 + (size_t)Geo<kFmt>::kTabOff + ((sizeof(Tables) + 15) & ~size_t(15)) + (size_t)T * Geo<kFmt>::kRows * 4;
+}
+
+template <int kFmt>
+cudaError_t launch_fmt(const Args& p, cudaStream_t s) {
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    static_assert(smem_bytes<kFmt>(kMaxT) <= 232448, "shared memory");
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(layer_kernel<kFmt>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<kFmt>(kMaxT));
+    });
+    if (err != cudaSuccess) return err;
+    CUtensorMap m1 = {}, m2 = {};
+    if constexpr (kFmt == MOE_LAYER_BF16) {
+        const uint64_t Et = (uint64_t)p.E + p.S;
+        if (!tc_make_map_2d(&m1, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.w1, 2 * (uint64_t)p.I, Et * p.H, 64, 64,
+                            CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !tc_make_map_2d(&m2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.w2, (uint64_t)p.H, Et * p.I, 64, 64,
+                            CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tc_num_sms());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<kFmt>(p.T);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another: all of them are resident
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, layer_kernel<kFmt>, m1, m2, p);
+}
+
 }  // namespace
 
-LayerLayout layer_layout(const moe_dims& d) {
+LayerLayout layer_layout(const moe_dims& d, int weights) {
     const size_t T = d.num_tokens, R = T * (d.topk + d.num_shared_experts);
+    const size_t rows = weights == MOE_LAYER_BF16 ? 128 : 32;
     LayerLayout L = {};
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -122,11 +1024,18 @@ LayerLayout layer_layout(const moe_dims& d) {
         off = align_up(off + bytes);
         return at;
     };
+    // the counters: the same place whatever the sizes, so that one workspace serves calls of different sizes
     L.header = take(sizeof(int32_t) * kOpsHeaderInts);
-    L.logits = take(sizeof(float) * T * d.num_experts);
+    L.dep = take(sizeof(int32_t) * kMaxE);
+    L.cols = take(sizeof(int32_t) * ((1 << 16) / 32));
+    L.amax = take(sizeof(uint32_t) * kMaxSlots);
+    L.logits = take(sizeof(float) * kMaxChunks * T * d.num_experts);
     L.ids = take(sizeof(int32_t) * T * d.topk);
     L.weights = take(sizeof(float) * T * d.topk);
+    L.x16 = take(2 * T * d.hidden);
+    L.xinv = take(sizeof(float) * T);
     L.act = take(sizeof(float) * R * d.intermediate);
+    L.part = take(sizeof(float) * 2 * kMaxT * rows * kMaxSms);
     L.total = off;
     return L;
 }
@@ -134,31 +1043,47 @@ LayerLayout layer_layout(const moe_dims& d) {
 cudaError_t launch_layer(const moe_layer_args& a, const moe_gate_options& gate, const moe_dims& d, void* workspace,
                          cudaStream_t s) {
     if (d.num_tokens == 0) return cudaSuccess;
-    const LayerLayout L = layer_layout(d);
+    const int sms = tc_num_sms();
+    if (sms > kMaxSms) return cudaErrorInvalidValue;
+    const LayerLayout L = layer_layout(d, a.weights);
     uint8_t* b = static_cast<uint8_t*>(workspace);
     Args p = {};
-    p.a = a;
+    p.x = static_cast<const uint16_t*>(a.x);
+    p.router = a.router;
+    p.w1 = a.w1.data;
+    p.w2 = a.w2.data;
+    p.s1 = a.w1.scale;
+    p.s2 = a.w2.scale;
+    p.bias = a.gate_bias;
+    p.ids_io = a.topk_ids;
+    p.weights_io = a.topk_weights;
+    p.y = static_cast<uint16_t*>(a.y);
+    p.gate = gate;
+    p.router_bf16 = a.router_type == MOE_TYPE_BF16;
     p.T = d.num_tokens;
     p.H = d.hidden;
     p.I = d.intermediate;
     p.E = d.num_experts;
     p.K = d.topk;
     p.S = d.num_shared_experts;
+    // as many parts of H as give every warp of the GPU a dot product
+    p.chunks = std::max(1, std::min({kMaxChunks, sms * kAllWarps / p.E, p.H / 256}));
     p.clamp = a.has_activation_clamp ? a.activation_clamp : INFINITY;
     p.hdr = reinterpret_cast<int32_t*>(b + L.header);
+    p.dep = reinterpret_cast<int32_t*>(b + L.dep);
+    p.cols = reinterpret_cast<int32_t*>(b + L.cols);
+    p.amax = reinterpret_cast<uint32_t*>(b + L.amax);
     p.logits = reinterpret_cast<float*>(b + L.logits);
+    p.ids = reinterpret_cast<int32_t*>(b + L.ids);
+    p.weights = reinterpret_cast<float*>(b + L.weights);
+    p.x16 = reinterpret_cast<uint16_t*>(b + L.x16);
+    p.xinv = reinterpret_cast<float*>(b + L.xinv);
     p.act = reinterpret_cast<float*>(b + L.act);
-    p.ids = a.topk_ids ? a.topk_ids : reinterpret_cast<int32_t*>(b + L.ids);
-    p.weights = a.topk_weights ? a.topk_weights : reinterpret_cast<float*>(b + L.weights);
-    if (a.router) {
-        logits_kernel<<<(p.T * p.E + 7) / 8, 256, 0, s>>>(p);
-        const cudaError_t e = launch_gate(p.logits, MOE_TYPE_F32, p.E, a.gate_bias, gate, p.T, p.E, p.K, p.ids, p.weights, s);
-        if (e != cudaSuccess) return e;
-    }
+    p.part = reinterpret_cast<float*>(b + L.part);
     switch (a.weights) {
-        case MOE_LAYER_BF16: return launch_ffn<MOE_LAYER_BF16>(p, s);
-        case MOE_LAYER_FP8_BLOCK: return launch_ffn<MOE_LAYER_FP8_BLOCK>(p, s);
-        default: return launch_ffn<MOE_LAYER_FP4_MX>(p, s);
+        case MOE_LAYER_BF16: return launch_fmt<MOE_LAYER_BF16>(p, s);
+        case MOE_LAYER_FP8_BLOCK: return launch_fmt<MOE_LAYER_FP8_BLOCK>(p, s);
+        default: return launch_fmt<MOE_LAYER_FP4_MX>(p, s);
     }
 }
 

@@ -89,7 +89,7 @@ moe_status moe_fp8_matmul(const moe_fp8_matmul_args* a, void* workspace, size_t 
 
 size_t moe_layer_workspace_bytes(const moe_dims* d, moe_layer_weights weights) {
     if (!layer_dims_ok(d, weights) || d->num_tokens > MOE_LAYER_MAX_TOKENS) return 0;
-    return layer_layout(*d).total;
+    return layer_layout(*d, weights).total;
 }
 
 moe_status moe_layer(const moe_layer_args* a, const moe_dims* d, void* workspace, size_t workspace_bytes,
@@ -106,7 +106,7 @@ moe_status moe_layer(const moe_layer_args* a, const moe_dims* d, void* workspace
     for (const void* p : {a->x, a->router, a->w1.data, a->w1.scale, a->w2.data, a->w2.scale, (const void*)a->y})
         if (!aligned(p, 16)) return MOE_ERR_INVALID_ARG;
     if (!aligned(a->topk_ids, 4) || !aligned(a->topk_weights, 4) || !aligned(a->gate_bias, 4)) return MOE_ERR_INVALID_ARG;
-    if (!workspace_ok(workspace, workspace_bytes, layer_layout(*d).total)) return MOE_ERR_WORKSPACE;
+    if (!workspace_ok(workspace, workspace_bytes, layer_layout(*d, a->weights).total)) return MOE_ERR_WORKSPACE;
     return from_cuda(launch_layer(*a, o, *d, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
