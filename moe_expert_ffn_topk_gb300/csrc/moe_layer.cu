@@ -4,7 +4,7 @@
 //
 // With few tokens every expert that is touched is multiplied by a handful of rows, so the time is that of reading its
 // weights once. The kernel is a stream of weights through shared memory: one CTA per SM, a producer warp that keeps a ring
-// of stages of 16 KB full by bulk copies, and eight warps that multiply each stage by the tokens' rows with mma.sync
+// of stages of 16 KB full by TMA, and eight warps that multiply each stage by the tokens' rows with mma.sync
 // (16 weight rows x 8 tokens x 16 of K), which at this shape is far from the tensor pipe's bound. The weight addresses
 // depend on the routes alone, so the producer runs ahead across items, experts and from the first product into the
 // second, while the consumers wait for activations.
@@ -58,17 +58,16 @@ constexpr int kMaxSlots = kMaxT * 32;
 constexpr int kMaxE = 1024;
 constexpr int kMaxChunks = 8;                   // parts of H in the router product
 
-// Stage geometry. K-contiguous formats: 32 rows x 512 bytes, rows 576 bytes apart (the 16-byte loads of 8 lanes, two rows of
-// 64 bytes, then touch every bank once). BF16: 64 of K x two boxes of 64 columns, 128-byte swizzle.
+// Stage geometry. K-contiguous formats: four boxes of 32 rows x 128 bytes. BF16: 64 of K x two boxes of 64 columns. All boxes
+// have the 128-byte swizzle (the 16-byte unit u of line r is at u ^ (r % 8)).
 template <int kFmt>
 struct Geo {
     static constexpr bool kBf16 = kFmt == MOE_LAYER_BF16;
     static constexpr bool kFp4 = kFmt == MOE_LAYER_FP4_MX;
     static constexpr int kRows = kBf16 ? 128 : 32;  // weight rows of an item
     static constexpr int kOut1 = kRows / 2;         // outputs of an item of the first product
-    static constexpr int kPitch = 576;
     static constexpr int kStepK = kBf16 ? 64 : kFp4 ? 1024 : 512;
-    static constexpr int kStageBytes = kBf16 ? 16384 : 32 * kPitch;
+    static constexpr int kStageBytes = 16384;
     static constexpr int kStages = 8;
     static constexpr int kSlices = kBf16 ? 4 : 8;   // parts of K whose sums meet in shared memory
     static constexpr int kMt = kBf16 ? 4 : 2;       // 16-row MMA tiles of a warp
@@ -118,11 +117,6 @@ struct Args {
     float* part;       // [CTA][2][T][rows of an item]
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -440,18 +434,25 @@ __device__ __forceinline__ bool produce(const Args& p, const CUtensorMap* map, R
                 tma_load_2d(dst + 8192, map, kSecond ? r0 + 64 : p.I + r0, y, ring.full(s));
             }
         } else {
-            const int row_bytes = G::kFp4 ? K / 2 : K;
-            const int bytes = min(512, row_bytes - st * 512);
-            // rows 0-7 and 16-23 of an item of the first product are gate rows, the others the up rows of the same outputs
-            const int row = kSecond ? r0 + lane : ((lane & 8) ? p.I : 0) + r0 + (lane >> 4) * 8 + (lane & 7);
-            const uint8_t* src = static_cast<const uint8_t*>(kSecond ? p.w2 : p.w1) + ((int64_t)expert * N + row) * row_bytes + st * 512;
-            if (lane == 0) mbar_arrive_expect_tx(ring.full(s), 32u * (uint32_t)bytes);
-            __syncwarp();
-            bulk_load(dst + (uint32_t)(lane * G::kPitch), src, (uint32_t)bytes, ring.full(s));
+            if (lane == 0) {
+                const int row_bytes = G::kFp4 ? K / 2 : K;
+                const int boxes = min(4, (row_bytes - st * 512 + 127) / 128);  // the last one may end inside: zeros
+                mbar_arrive_expect_tx(ring.full(s), 4096u * (uint32_t)boxes);
+                for (int c = 0; c < boxes; ++c) {
+                    const int x = st * 512 + c * 128;
+                    // first product: 16 gate rows, then the up rows of the same outputs (the map's third coordinate)
+                    if constexpr (kSecond) tma_load_2d(dst + c * 4096, map, x, expert * N + r0, ring.full(s));
+                    else tma_load_3d(dst + c * 4096, map, x, expert * N + r0, 0, ring.full(s));
+                }
+            }
         }
     }
     return true;
 }
+
+// MMA rows g and g + 8 of 16-row tile m are the stage's rows 8 m + perm(g) and 16 + 8 m + perm(g): lanes 4 g .. 4 g + 3 read 64
+// bytes of a row, and the rows of two neighbouring g, four apart, lie in different halves of the swizzled lines.
+__device__ __forceinline__ int perm(int g) { return (g >> 1) | ((g & 1) << 2); }
 
 // One column tile's values for a warp's part of a stage: B words as they are in memory (fp32 activations: two to a word of B).
 template <int kFmt, bool kSecond>
@@ -500,8 +501,8 @@ struct Scales {
             const uint8_t* q = static_cast<const uint8_t*>(kSecond ? p.s2 : p.s1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = i * 8 + (lane >> 2);
-                const int row = kSecond ? r0 + r : ((r & 8) ? p.I : 0) + r0 + (r >> 4) * 8 + (r & 7);
+                // i = 2 m: the tile's row g, 2 m + 1: its row g + 8
+                const int row = r0 + (i >> 1) * 8 + perm(lane >> 2) + ((i & 1) ? (kSecond ? 16 : p.I) : 0);
                 s[i] = __ldg(reinterpret_cast<const uint32_t*>(q + ((int64_t)expert * N + row) * (K / 32) + k / 32));
             }
         } else if constexpr (!G::kBf16) {
@@ -564,8 +565,9 @@ __device__ __forceinline__ void multiply(const Args& p, Ring<kFmt> ring, const v
                     const int krow = off + (lane & 7) + ((lane >> 4) & 1) * 8, c8 = (lane >> 3) & 1;
                     ldmatrix_x4_trans(a[m][0], stage + (uint32_t)((warp >> 2) * 8192 + krow * 128 + (((2 * m + c8) ^ (krow & 7)) << 4)));
                 } else {
-                    const uint32_t at = stage + (uint32_t)((m * 16 + (lane >> 2)) * G::kPitch + warp * 64 + (lane & 3) * 16);
-                    const uint4 u = lds128(at), v = lds128(at + 8 * G::kPitch);  // rows g and g + 8
+                    const int r = m * 8 + perm(lane >> 2), unit = (warp & 1) * 4 + (lane & 3);
+                    const uint32_t at = stage + (uint32_t)((warp >> 1) * 4096 + r * 128 + ((unit ^ (r & 7)) << 4));
+                    const uint4 u = lds128(at), v = lds128(at + 16 * 128);  // rows g and g + 8 of the tile
                     const uint32_t ug[4] = {u.x, u.y, u.z, u.w}, vg[4] = {v.x, v.y, v.z, v.w};
                     if constexpr (G::kFp4) {
                         // this lane's codes relative to the largest scale of the four blocks
@@ -670,10 +672,11 @@ __device__ __forceinline__ const float* gather(Shared& sh, const float (&acc)[Ge
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int m = 0; m < G::kMt; ++m) {
-        dst[(2 * t) * G::kRedCol + m * 16 + g] = acc[m][n][0];
-        dst[(2 * t + 1) * G::kRedCol + m * 16 + g] = acc[m][n][1];
-        dst[(2 * t) * G::kRedCol + m * 16 + g + 8] = acc[m][n][2];
-        dst[(2 * t + 1) * G::kRedCol + m * 16 + g + 8] = acc[m][n][3];
+        const int r0 = G::kBf16 ? m * 16 + g : m * 8 + perm(g), r1 = G::kBf16 ? r0 + 8 : r0 + 16;
+        dst[(2 * t) * G::kRedCol + r0] = acc[m][n][0];
+        dst[(2 * t + 1) * G::kRedCol + r0] = acc[m][n][1];
+        dst[(2 * t) * G::kRedCol + r1] = acc[m][n][2];
+        dst[(2 * t + 1) * G::kRedCol + r1] = acc[m][n][3];
     }
     consumer_sync();
     return red;
@@ -722,12 +725,12 @@ __device__ __forceinline__ void first_item(const Args& p, Ring<kFmt> ring, Share
                 if (on) dst[j] = v;
             }
         } else {
-            // rows 0-7, 16-23: gate; 8-15, 24-31: up of the same outputs
+            // rows 0-15: gate; 16-31: up of the same outputs
             const float h = red_sum<kFmt>(red, warp, lane) * inv;
-            const float u = __shfl_down_sync(0xffffffffu, h, 8);
-            const bool gate = !(lane & 8);
+            const float u = __shfl_down_sync(0xffffffffu, h, 16);
+            const bool gate = lane < 16;
             const float v = swiglu1(h, u, p.clamp);
-            if (on && gate) dst[(lane >> 4) * 8 + (lane & 7)] = v;
+            if (on && gate) dst[lane] = v;
             top = __reduce_max_sync(0xffffffffu, gate ? __float_as_uint(v) & 0x7fffffffu : 0u);
             if (on && lane == 0) atomicMax(p.amax + slot, top);
         }
@@ -997,6 +1000,17 @@ cudaError_t launch_fmt(const Args& p, cudaStream_t s) {
                             CU_TENSOR_MAP_SWIZZLE_128B) ||
             !tc_make_map_2d(&m2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.w2, (uint64_t)p.H, Et * p.I, 64, 64,
                             CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    } else {
+        const uint64_t Et = (uint64_t)p.E + p.S, half = kFmt == MOE_LAYER_FP4_MX ? 2 : 1;
+        const uint64_t b1 = p.H / half, b2 = p.I / half;  // bytes of a row
+        // W1 as [gate or up][row][bytes]: a box takes 16 rows of each
+        const uint64_t d1[3] = {b1, Et * 2 * p.I - p.I, 2}, s1[2] = {b1, b1 * p.I};
+        const uint32_t box1[3] = {128, 16, 2};
+        const uint64_t d2[2] = {b2, Et * p.H}, s2[1] = {b2};
+        const uint32_t box2[2] = {128, 32};
+        if (!tc_make_map_nd(&m1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.w1, d1, s1, box1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !tc_make_map_nd(&m2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.w2, d2, s2, box2, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
     cudaLaunchConfig_t cfg = {};
