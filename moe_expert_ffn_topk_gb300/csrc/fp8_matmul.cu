@@ -458,6 +458,7 @@ cudaError_t prepare_kernel(int* resident) {
     static int clusters = 0;
     std::call_once(once, [] {
         err = cudaFuncSetAttribute(fp8_matmul_kernel<C, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (err == cudaSuccess) err = check_register_split(reinterpret_cast<const void*>(fp8_matmul_kernel<C, Out>), kLaunchRegs);
         if (C::kCtas == 1 || err != cudaSuccess) return;
         // pairs that can be resident at once (a pair needs two free SMs of one GPC)
         cudaLaunchConfig_t cfg = {};

@@ -15,8 +15,10 @@
 //   2. selection: each CTA selects for all tokens itself (up to 8 tokens), or for its share of them and a second barrier.
 //      Each CTA then lists the experts with rows and their rows in shared memory.
 //   3. first product: items of 16 outputs (16 gate and 16 up rows of W1; BF16: 64 and 64) of one expert, dealt to the CTAs in
-//      turn. The eight warps split K, their sums meet in shared memory, and SwiGLU of them goes to the workspace in fp32 with
-//      the row's largest magnitude. A counter per expert says when its rows are complete.
+//      turn. Each warp (BF16: pair of warps) takes every eighth (fourth) stage whole, so that a stage costs one wait and one
+//      arrival and its latencies have the time of eight stages; the warps' sums of an item meet in shared memory, where two
+//      epilogue warps add them up. SwiGLU of them goes to the workspace in fp32 with the row's largest magnitude. A counter per
+//      expert says when its rows are complete.
 //   4. second product: items of 32 hidden columns (BF16: 128) of one expert, ordered by columns first and dealt in equal
 //      runs, so that a CTA adds up the experts of its columns itself, in order, in shared memory. Columns whose experts are
 //      split between CTAs meet in the workspace: the last CTA to arrive adds the parts in order. No atomics on values:
@@ -48,43 +50,52 @@ namespace {
 using namespace tc;
 
 constexpr int kWarps = 8;                       // consumers
-constexpr int kAllWarps = 12;                   // warp 8 is the producer, 9-11 only help in the first phases
+constexpr int kAllWarps = 12;                   // warp 8 is the producer, 9 and 10 the epilogue, 11 only helps in the first phases
 constexpr int kThreads = 32 * kAllWarps;
-// registers of warps 8-11 and of the consumers from phase 3 on: 128 * 40 + 256 * 232 = 384 * 168, what the launch holds
-constexpr int kFewRegs = 40, kManyRegs = 232;
-static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "register split");
+// registers of warps 8-11 and of the consumers from phase 3 on: 128 * 104 + 256 * 200 = 384 * 168, what the launch holds
+constexpr int kLaunchRegs = 168, kFewRegs = 104, kManyRegs = 200;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kMaxT = MOE_LAYER_MAX_TOKENS;
 constexpr int kMaxSlots = kMaxT * 32;
+constexpr int kEpiWarps = 2;                    // warps 9 and 10 take the sums of an item further
 constexpr int kMaxE = 1024;
 constexpr int kMaxChunks = 8;                   // parts of H in the router product
 
-// Stage geometry. K-contiguous formats: four boxes of 32 rows x 128 bytes. BF16: 64 of K x two boxes of 64 columns. All boxes
-// have the 128-byte swizzle (the 16-byte unit u of line r is at u ^ (r % 8)).
+// Stage geometry. K-contiguous formats: two boxes of 32 rows x 128 bytes. BF16: 64 of K x two boxes of 64 columns. All boxes
+// have the 128-byte swizzle (the 16-byte unit u of line r is at u ^ (r % 8)). A warp multiplies a stage in four slices of K.
 template <int kFmt>
 struct Geo {
     static constexpr bool kBf16 = kFmt == MOE_LAYER_BF16;
     static constexpr bool kFp4 = kFmt == MOE_LAYER_FP4_MX;
     static constexpr int kRows = kBf16 ? 128 : 32;  // weight rows of an item
     static constexpr int kOut1 = kRows / 2;         // outputs of an item of the first product
-    static constexpr int kStepK = kBf16 ? 64 : kFp4 ? 1024 : 512;
-    static constexpr int kStageBytes = 16384;
-    static constexpr int kStages = 8;
-    static constexpr int kSlices = kBf16 ? 4 : 8;   // parts of K whose sums meet in shared memory
+    static constexpr int kStepK = kBf16 ? 64 : kFp4 ? 512 : 256;
+    static constexpr int kSlices = 4, kSliceK = kStepK / kSlices;
+    static constexpr int kStageBytes = kBf16 ? 16384 : 8192;
+    static constexpr int kStages = kBf16 ? 8 : 16;
+    static constexpr int kGroups = kBf16 ? 4 : 8;   // consumer groups: stage i is group i % kGroups's
+    // a slot of the ring is always the same group's: two groups may be more than a use of the slot apart, and a wait for a
+    // phase's parity cannot tell it from the phase two before
+    static_assert(kStages % kGroups == 0, "slots and groups");
+    static constexpr int kGroupWarps = kWarps / kGroups;
     static constexpr int kMt = kBf16 ? 4 : 2;       // 16-row MMA tiles of a warp
     static constexpr int kRedCol = kRows + 4;       // floats of a column of partial sums (two columns apart: 8 banks)
-    static constexpr int kRedSlice = 8 * kRedCol;
-    static constexpr int kRed = kSlices * kRedSlice;
-    // shared memory: ring | two sets of partial sums | y sums | tables
+    static constexpr int kRedGroup = 8 * kRedCol;
+    static constexpr int kRed = kGroups * kRedGroup + 8;  // and the inverse scale of each column's activations
+    static constexpr int kReds = kBf16 ? 2 : 3;     // sets of partial sums on their way to the epilogue
+    // shared memory: ring | sets of partial sums | tables | y sums
     static constexpr int kRedOff = kStages * kStageBytes;
-    static constexpr int kTabOff = kRedOff + 2 * 4 * kRed;
+    static constexpr int kTabOff = kRedOff + kReds * 4 * kRed;
 };
 
+constexpr int kMaxBars = 48;
+
 struct Tables {
-    uint64_t bars[32];
-    int n_active, error, last;
-    int abort;
-    int expert[kMaxE], start[kMaxE + 1];  // active experts and where their rows begin in row[]
+    uint64_t bars[kMaxBars];
+    int n_active, last, abort, unused;
     int count[kMaxE];
+    int16_t expert[kMaxE];                // active experts
+    int16_t start[kMaxE + 2];             // where their rows begin in row[]
     uint16_t row[kMaxSlots];              // slot = token * (K + S) + k
     float weight[kMaxSlots];              // by slot
     int16_t id[kMaxSlots];                // by slot, -1: none
@@ -181,7 +192,7 @@ __device__ __forceinline__ float row_scale(uint32_t top, float* inverse) {
     *inverse = __uint_as_float((uint32_t)(e - 14) << 23);     // 2^(e - 141)
     return __uint_as_float((uint32_t)(268 - e) << 23);        // 2^(141 - e)
 }
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 64;" ::: "memory"); }
 
 // All CTAs have arrived n times (n counts the barriers of this launch); one thread waits, bounded.
 __device__ __forceinline__ void grid_barrier(const Args& p, int n, volatile int* abort_flag) {
@@ -356,8 +367,8 @@ __device__ void list_experts(const Args& p, Tables& tb, const int32_t* ids, cons
             }
             if (n > 0) {
                 const int a = active + __popc(on & ((1u << lane) - 1u));
-                tb.expert[a] = e;
-                tb.start[a] = rows + sum - n;
+                tb.expert[a] = (int16_t)e;
+                tb.start[a] = (int16_t)(rows + sum - n);
             }
             if (e < Et) tb.count[e] = rows + sum - n;  // the next free place
             active += __popc(on);
@@ -365,7 +376,7 @@ __device__ void list_experts(const Args& p, Tables& tb, const int32_t* ids, cons
         }
         if (lane == 0) {
             tb.n_active = active;
-            tb.start[active] = rows;
+            tb.start[active] = (int16_t)rows;
         }
     }
     __syncthreads();
@@ -408,10 +419,14 @@ struct Work {
 
 template <int kFmt>
 struct Ring {
+    static_assert(2 * (Geo<kFmt>::kStages + Geo<kFmt>::kReds) <= kMaxBars, "barriers");
     uint32_t base, bars;
     int it = 0;
     __device__ uint32_t full(int s) const { return bars + 8u * s; }
     __device__ uint32_t empty(int s) const { return bars + 8u * (Geo<kFmt>::kStages + s); }
+    // sets of partial sums: written by all consumers; read by the epilogue
+    __device__ uint32_t red_full(int s) const { return bars + 8u * (2 * Geo<kFmt>::kStages + s); }
+    __device__ uint32_t red_empty(int s) const { return bars + 8u * (2 * Geo<kFmt>::kStages + Geo<kFmt>::kReds + s); }
 };
 
 // One item's stages, by the producer warp.
@@ -436,10 +451,10 @@ __device__ __forceinline__ bool produce(const Args& p, const CUtensorMap* map, R
         } else {
             if (lane == 0) {
                 const int row_bytes = G::kFp4 ? K / 2 : K;
-                const int boxes = min(4, (row_bytes - st * 512 + 127) / 128);  // the last one may end inside: zeros
+                const int boxes = min(2, (row_bytes - st * 256 + 127) / 128);  // the last one may end inside: zeros
                 mbar_arrive_expect_tx(ring.full(s), 4096u * (uint32_t)boxes);
                 for (int c = 0; c < boxes; ++c) {
-                    const int x = st * 512 + c * 128;
+                    const int x = st * 256 + c * 128;
                     // first product: 16 gate rows, then the up rows of the same outputs (the map's third coordinate)
                     if constexpr (kSecond) tma_load_2d(dst + c * 4096, map, x, expert * N + r0, ring.full(s));
                     else tma_load_3d(dst + c * 4096, map, x, expert * N + r0, 0, ring.full(s));
@@ -462,24 +477,26 @@ struct Columns {
     static constexpr int kWords = kSecond ? 2 * kB : kB;
     uint32_t w[kWords];
 
-    // row: the x row or activation row of this lane's column, or null
-    __device__ __forceinline__ void load(const void* row, int k, int lane) {
+    // r: the x row (a token) or activation row (a slot) of this lane's column, -1: none
+    __device__ __forceinline__ void load(const Args& p, int r, int k, int lane) {
+        const bool row = r >= 0;
         if constexpr (G::kBf16) {
             const int at = k + 2 * (lane & 3);
             if constexpr (kSecond) {
-                const float* q = static_cast<const float*>(row) + at;
+                const float* q = p.act + (int64_t)r * p.I + at;
                 const float2 u = row ? *reinterpret_cast<const float2*>(q) : make_float2(0.0f, 0.0f);
                 const float2 v = row ? *reinterpret_cast<const float2*>(q + 8) : make_float2(0.0f, 0.0f);
                 w[0] = __float_as_uint(u.x), w[1] = __float_as_uint(u.y);
                 w[2] = __float_as_uint(v.x), w[3] = __float_as_uint(v.y);
             } else {
-                const uint16_t* q = static_cast<const uint16_t*>(row) + at;
+                const uint16_t* q = p.x + (int64_t)r * p.H + at;
                 w[0] = row ? *reinterpret_cast<const uint32_t*>(q) : 0u;
                 w[1] = row ? *reinterpret_cast<const uint32_t*>(q + 8) : 0u;
             }
         } else {
             const int at = k + (G::kFp4 ? 32 : 16) * (lane & 3);
-            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (kSecond ? 4 : 2) * (int64_t)at);
+            const uint4* q = kSecond ? reinterpret_cast<const uint4*>(p.act + (int64_t)r * p.I + at)
+                                     : reinterpret_cast<const uint4*>(p.x16 + (int64_t)r * p.H + at);
 #pragma unroll
             for (int i = 0; i < kWords / 4; ++i) {
                 const uint4 v = row ? q[i] : make_uint4(0, 0, 0, 0);
@@ -513,356 +530,365 @@ struct Scales {
     }
 };
 
-// The sums of one item over its K: the stages' weights times the rows. acc[m][n]: 16-row tile m, 8-column tile n.
+// The weights of a warp's slice of a stage as MMA operands and their products with the column tiles, added to acc. The first
+// tile's values are there (most experts have no more than its 8 rows), the others' are loaded here.
 template <int kFmt, bool kSecond, int NT>
-__device__ __forceinline__ void multiply(const Args& p, Ring<kFmt> ring, const void* const (&rows)[NT], const float (&ascale)[NT],
-                                         int expert, int r0, int warp, int lane, volatile int* abort_flag,
-                                         float (&acc)[Geo<kFmt>::kMt][NT][4]) {
+__device__ __forceinline__ void multiply_slice(const Args& p, uint32_t stage, int slice, int k, const Columns<kFmt, kSecond>& first,
+                                               const Scales<kFmt, kSecond>& sc, const int (&rows)[NT], const float (&ascale)[NT],
+                                               int tiles, int warp, int lane, float (&acc)[Geo<kFmt>::kMt][NT][4]) {
     using G = Geo<kFmt>;
     using Cols = Columns<kFmt, kSecond>;
-    const int K = kSecond ? p.I : p.H;
-    const int steps = (K + G::kStepK - 1) / G::kStepK;
-    constexpr int kSliceK = G::kStepK / G::kSlices;  // K of a warp in a stage
-    const int off = (G::kBf16 ? warp & 3 : warp) * kSliceK;
-    // the next stage's columns are loaded during this one while registers last
-    constexpr bool kAhead = NT * Cols::kWords <= 32;
+    constexpr int kMmas = Cols::kB / 2;
+    uint32_t a[G::kMt][kMmas][4];
+    float f0[G::kMt], f1[G::kMt];  // scales of the sums of rows g and g + 8
 #pragma unroll
-    for (int m = 0; m < G::kMt; ++m)
+    for (int m = 0; m < G::kMt; ++m) {
+        f0[m] = f1[m] = 1.0f;
+        if constexpr (G::kBf16) {
+            // [K row][64 columns] boxes: lane l gives row l % 8 (+ 8 for matrices 2, 3) and columns + 8 for 1, 3
+            const int krow = slice * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, c8 = (lane >> 3) & 1;
+            ldmatrix_x4_trans(a[m][0], stage + (uint32_t)((warp & 1) * 8192 + krow * 128 + (((2 * m + c8) ^ (krow & 7)) << 4)));
+        } else {
+            const int r = m * 8 + perm(lane >> 2), unit = (slice & 1) * 4 + (lane & 3);
+            const uint32_t at = stage + (uint32_t)((slice >> 1) * 4096 + r * 128 + ((unit ^ (r & 7)) << 4));
+            const uint4 u = lds128(at), v = lds128(at + 16 * 128);  // rows g and g + 8 of the tile
+            const uint32_t ug[4] = {u.x, u.y, u.z, u.w}, vg[4] = {v.x, v.y, v.z, v.w};
+            if constexpr (G::kFp4) {
+                // this lane's codes relative to the largest scale of the four blocks
+                auto most = [](uint32_t w) { return max(max(w & 255u, (w >> 8) & 255u), max((w >> 16) & 255u, w >> 24)); };
+                const uint32_t w0 = sc.s[2 * m], w1 = sc.s[2 * m + 1], m0 = most(w0), m1 = most(w1);
+                const uint32_t p0 = pow2_f16x2((int)(m0 - ((w0 >> (8 * (lane & 3))) & 255u)));
+                const uint32_t p1 = pow2_f16x2((int)(m1 - ((w1 >> (8 * (lane & 3))) & 255u)));
+                f0[m] = ue8m0_to_float((uint8_t)m0);
+                f1[m] = ue8m0_to_float((uint8_t)m1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                for (int q = 0; q < 4; ++q) {
+                    a[m][2 * q][0] = mul_f16x2(e2m1x2_f16x2<0>(ug[q]), p0);
+                    a[m][2 * q][1] = mul_f16x2(e2m1x2_f16x2<0>(vg[q]), p1);
+                    a[m][2 * q][2] = mul_f16x2(e2m1x2_f16x2<1>(ug[q]), p0);
+                    a[m][2 * q][3] = mul_f16x2(e2m1x2_f16x2<1>(vg[q]), p1);
+                    a[m][2 * q + 1][0] = mul_f16x2(e2m1x2_f16x2<2>(ug[q]), p0);
+                    a[m][2 * q + 1][1] = mul_f16x2(e2m1x2_f16x2<2>(vg[q]), p1);
+                    a[m][2 * q + 1][2] = mul_f16x2(e2m1x2_f16x2<3>(ug[q]), p0);
+                    a[m][2 * q + 1][3] = mul_f16x2(e2m1x2_f16x2<3>(vg[q]), p1);
+                }
+            } else {
+                f0[m] = __uint_as_float(sc.s[0]);
+                f1[m] = __uint_as_float(sc.s[1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-    Cols cols[kAhead ? NT : 1], next[kAhead ? NT : 1];
-    Scales<kFmt, kSecond> sc, sc_next;
-    if (off < K) {
-        sc.load(p, off, K, expert, r0, lane);
-        if constexpr (kAhead)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) cols[n].load(rows[n], off, lane);
-    }
-    for (int st = 0; st < steps; ++st, ++ring.it) {
-        const int s = ring.it % G::kStages, k = st * G::kStepK + off;
-        const bool on = k < K;
-        if (k + G::kStepK < K) {
-            sc_next.load(p, k + G::kStepK, K, expert, r0, lane);
-            if constexpr (kAhead)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) next[n].load(rows[n], k + G::kStepK, lane);
+                for (int q = 0; q < 4; ++q) {
+                    a[m][q][0] = e4m3x2_f16x2(ug[q]);
+                    a[m][q][1] = e4m3x2_f16x2(vg[q]);
+                    a[m][q][2] = e4m3x2_f16x2(ug[q] >> 16);
+                    a[m][q][3] = e4m3x2_f16x2(vg[q] >> 16);
+                }
+            }
         }
-        // a wait that ran out skips the stage: the warps still meet at the barriers that follow
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(ring.full(s), (uint32_t)(ring.it / G::kStages) & 1u, p.hdr, abort_flag));
-        const uint32_t stage = ring.base + (uint32_t)(s * G::kStageBytes);
-        if (on && ok) {
-            // the weights as MMA operands: a[m][j] for the j-th 16 of K
-            constexpr int kMmas = Cols::kB / 2;
-            uint32_t a[G::kMt][kMmas][4];
-            float f0[G::kMt], f1[G::kMt];  // scales of the sums of rows g and g + 8
+    }
 #pragma unroll
-            for (int m = 0; m < G::kMt; ++m) {
-                f0[m] = f1[m] = 1.0f;
-                if constexpr (G::kBf16) {
-                    // [K row][64 columns] boxes: lane l gives row l % 8 (+ 8 for matrices 2, 3) and columns + 8 for 1, 3
-                    const int krow = off + (lane & 7) + ((lane >> 4) & 1) * 8, c8 = (lane >> 3) & 1;
-                    ldmatrix_x4_trans(a[m][0], stage + (uint32_t)((warp >> 2) * 8192 + krow * 128 + (((2 * m + c8) ^ (krow & 7)) << 4)));
+    for (int n = 0; n < NT; ++n) {
+        if (n >= tiles) break;
+        Cols c;
+        if (n == 0) c = first;
+        else c.load(p, rows[n], k, lane);
+        if constexpr (G::kBf16) {
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (kSecond) {
+                    const float u = __uint_as_float(c.w[2 * i]), v = __uint_as_float(c.w[2 * i + 1]);
+                    hi[i] = pack_bf16(u, v);
+                    // an infinity or NaN stays in the high part alone
+                    const float du = u - __uint_as_float(hi[i] << 16), dv = v - __uint_as_float(hi[i] & 0xffff0000u);
+                    lo[i] = pack_bf16(fabsf(u) < INFINITY ? du : 0.0f, fabsf(v) < INFINITY ? dv : 0.0f);
                 } else {
-                    const int r = m * 8 + perm(lane >> 2), unit = (warp & 1) * 4 + (lane & 3);
-                    const uint32_t at = stage + (uint32_t)((warp >> 1) * 4096 + r * 128 + ((unit ^ (r & 7)) << 4));
-                    const uint4 u = lds128(at), v = lds128(at + 16 * 128);  // rows g and g + 8 of the tile
-                    const uint32_t ug[4] = {u.x, u.y, u.z, u.w}, vg[4] = {v.x, v.y, v.z, v.w};
-                    if constexpr (G::kFp4) {
-                        // this lane's codes relative to the largest scale of the four blocks
-                        auto most = [](uint32_t w) { return max(max(w & 255u, (w >> 8) & 255u), max((w >> 16) & 255u, w >> 24)); };
-                        const uint32_t w0 = sc.s[2 * m], w1 = sc.s[2 * m + 1], m0 = most(w0), m1 = most(w1);
-                        const uint32_t p0 = pow2_f16x2((int)(m0 - ((w0 >> (8 * (lane & 3))) & 255u)));
-                        const uint32_t p1 = pow2_f16x2((int)(m1 - ((w1 >> (8 * (lane & 3))) & 255u)));
-                        f0[m] = ue8m0_to_float((uint8_t)m0);
-                        f1[m] = ue8m0_to_float((uint8_t)m1);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            a[m][2 * q][0] = mul_f16x2(e2m1x2_f16x2<0>(ug[q]), p0);
-                            a[m][2 * q][1] = mul_f16x2(e2m1x2_f16x2<0>(vg[q]), p1);
-                            a[m][2 * q][2] = mul_f16x2(e2m1x2_f16x2<1>(ug[q]), p0);
-                            a[m][2 * q][3] = mul_f16x2(e2m1x2_f16x2<1>(vg[q]), p1);
-                            a[m][2 * q + 1][0] = mul_f16x2(e2m1x2_f16x2<2>(ug[q]), p0);
-                            a[m][2 * q + 1][1] = mul_f16x2(e2m1x2_f16x2<2>(vg[q]), p1);
-                            a[m][2 * q + 1][2] = mul_f16x2(e2m1x2_f16x2<3>(ug[q]), p0);
-                            a[m][2 * q + 1][3] = mul_f16x2(e2m1x2_f16x2<3>(vg[q]), p1);
-                        }
-                    } else {
-                        f0[m] = __uint_as_float(sc.s[0]);
-                        f1[m] = __uint_as_float(sc.s[1]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            a[m][q][0] = e4m3x2_f16x2(ug[q]);
-                            a[m][q][1] = e4m3x2_f16x2(vg[q]);
-                            a[m][q][2] = e4m3x2_f16x2(ug[q] >> 16);
-                            a[m][q][3] = e4m3x2_f16x2(vg[q] >> 16);
-                        }
-                    }
+                    hi[i] = c.w[i];
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if constexpr (!kAhead) cols[0].load(rows[n], k, lane);
-                const Cols& c = cols[kAhead ? n : 0];
-                if constexpr (G::kBf16) {
-                    uint32_t hi[2], lo[2];
+            for (int m = 0; m < G::kMt; ++m) {
+                mma_bf16(acc[m][n], a[m][0], hi[0], hi[1]);
+                if constexpr (kSecond) mma_bf16(acc[m][n], a[m][0], lo[0], lo[1]);
+            }
+        } else {
+            uint32_t bw[Cols::kB];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if constexpr (kSecond) {
-                            const float u = __uint_as_float(c.w[2 * i]), v = __uint_as_float(c.w[2 * i + 1]);
-                            hi[i] = pack_bf16(u, v);
-                            // an infinity or NaN stays in the high part alone
-                            const float du = u - __uint_as_float(hi[i] << 16), dv = v - __uint_as_float(hi[i] & 0xffff0000u);
-                            lo[i] = pack_bf16(fabsf(u) < INFINITY ? du : 0.0f, fabsf(v) < INFINITY ? dv : 0.0f);
-                        } else {
-                            hi[i] = c.w[i];
-                        }
-                    }
+            for (int i = 0; i < Cols::kB; ++i) {
+                if constexpr (kSecond)
+                    bw[i] = pack_f16(__uint_as_float(c.w[2 * i]) * ascale[n], __uint_as_float(c.w[2 * i + 1]) * ascale[n]);
+                else
+                    bw[i] = c.w[i];
+            }
 #pragma unroll
-                    for (int m = 0; m < G::kMt; ++m) {
-                        mma_bf16(acc[m][n], a[m][0], hi[0], hi[1]);
-                        if constexpr (kSecond) mma_bf16(acc[m][n], a[m][0], lo[0], lo[1]);
-                    }
+            for (int m = 0; m < G::kMt; ++m) {
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < kMmas; ++j) mma_f16(part, a[m][j], bw[2 * j], bw[2 * j + 1]);
+                acc[m][n][0] = fmaf(part[0], f0[m], acc[m][n][0]);
+                acc[m][n][1] = fmaf(part[1], f0[m], acc[m][n][1]);
+                acc[m][n][2] = fmaf(part[2], f1[m], acc[m][n][2]);
+                acc[m][n][3] = fmaf(part[3], f1[m], acc[m][n][3]);
+            }
+        }
+    }
+}
+
+// One item by a consumer warp: its group's stages (i % kGroups of the CTA's sequence) times the expert's rows, then its sums to
+// the epilogue, one set a column tile. Groups without a stage of the item only sign for their part of the set.
+template <int kFmt, bool kSecond, int NT>
+__device__ __forceinline__ void consume(const Args& p, const Ring<kFmt>& ring, float* reds, const Tables& tb, int a, int r0, int set,
+                                        int warp, int lane, volatile int* abort_flag) {
+    using G = Geo<kFmt>;
+    using Cols = Columns<kFmt, kSecond>;
+    // so many slices' columns of the first tile are on their way at a time, as far as registers go
+    constexpr int kSums = G::kMt * 4 * NT;
+    constexpr int kAhead = 4 * Cols::kWords + kSums <= 80 ? 4 : 2 * Cols::kWords + kSums <= 80 ? 2 : 1;
+    const int K = kSecond ? p.I : p.H;
+    const int steps = (K + G::kStepK - 1) / G::kStepK;
+    const int group = warp / G::kGroupWarps;
+    int st = (group - ring.it % G::kGroups + G::kGroups) % G::kGroups;  // this group's first stage of the item
+    const bool part = st < steps;
+    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, tiles = (n_rows + 7) / 8;
+    float acc[G::kMt][NT][4], ainv[NT];
+    if (part) {
+        const int Kt = p.K + p.S, expert = tb.expert[a];
+        int rows[NT];  // of this lane's column of each tile; -1 past the expert's rows
+        float ascale[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int c = n * 8 + (lane >> 2);
+            rows[n] = -1;
+            ascale[n] = ainv[n] = 1.0f;
+            if (c < n_rows) {
+                const int slot = tb.row[begin + c];
+                if constexpr (kSecond) {
+                    rows[n] = slot;
+                    if constexpr (!G::kBf16) ascale[n] = row_scale(__ldcg(p.amax + slot), &ainv[n]);
                 } else {
-                    uint32_t bw[Cols::kB];
+                    rows[n] = slot / Kt;
+                }
+            }
+        }
 #pragma unroll
-                    for (int i = 0; i < Cols::kB; ++i) {
-                        if constexpr (kSecond)
-                            bw[i] = pack_f16(__uint_as_float(c.w[2 * i]) * ascale[n], __uint_as_float(c.w[2 * i + 1]) * ascale[n]);
-                        else
-                            bw[i] = c.w[i];
+        for (int m = 0; m < G::kMt; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+        for (; st < steps; st += G::kGroups) {
+            const int it = ring.it + st, s = it % G::kStages, k = st * G::kStepK;
+            const int slices = min(G::kSlices, (K - k) / G::kSliceK);
+            Cols cols[kAhead];
+            Scales<kFmt, kSecond> sc[G::kSlices];
+#pragma unroll
+            for (int i = 0; i < G::kSlices; ++i)
+                if (i < slices) {
+                    sc[i].load(p, k + i * G::kSliceK, K, expert, r0, lane);
+                    if (i < kAhead) cols[i].load(p, rows[0], k + i * G::kSliceK, lane);
+                }
+            // a wait that ran out skips the stage: the set is still signed for
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(ring.full(s), (uint32_t)(it / G::kStages) & 1u, p.hdr, abort_flag));
+            const uint32_t stage = ring.base + (uint32_t)(s * G::kStageBytes);
+            if (ok)
+#pragma unroll
+                for (int i = 0; i < G::kSlices; ++i)
+                    if (i < slices) {
+                        multiply_slice<kFmt, kSecond, NT>(p, stage, i, k + i * G::kSliceK, cols[i % kAhead], sc[i], rows, ascale,
+                                                          tiles, warp, lane, acc);
+                        if (i + kAhead < slices) cols[i % kAhead].load(p, rows[0], k + (i + kAhead) * G::kSliceK, lane);
                     }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ring.empty(s));
+        }
+    }
 #pragma unroll
-                    for (int m = 0; m < G::kMt; ++m) {
-                        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int n = 0; n < NT; ++n, ++set) {
+        if (n >= tiles) break;
+        const int q = set % G::kReds;
+        mbar_wait(ring.red_empty(q), ((uint32_t)(set / G::kReds) & 1u) ^ 1u, p.hdr, abort_flag);
+        if (part) {
+            float* dst = reds + q * G::kRed + group * G::kRedGroup + (G::kBf16 ? (warp & 1) * 64 : 0);
+            const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-                        for (int j = 0; j < kMmas; ++j) mma_f16(part, a[m][j], bw[2 * j], bw[2 * j + 1]);
-                        acc[m][n][0] = fmaf(part[0], f0[m], acc[m][n][0]);
-                        acc[m][n][1] = fmaf(part[1], f0[m], acc[m][n][1]);
-                        acc[m][n][2] = fmaf(part[2], f1[m], acc[m][n][2]);
-                        acc[m][n][3] = fmaf(part[3], f1[m], acc[m][n][3]);
-                    }
+            for (int m = 0; m < G::kMt; ++m) {
+                const int r = G::kBf16 ? m * 16 + g : m * 8 + perm(g), r8 = G::kBf16 ? r + 8 : r + 16;
+                dst[(2 * t) * G::kRedCol + r] = acc[m][n][0];
+                dst[(2 * t + 1) * G::kRedCol + r] = acc[m][n][1];
+                dst[(2 * t) * G::kRedCol + r8] = acc[m][n][2];
+                dst[(2 * t + 1) * G::kRedCol + r8] = acc[m][n][3];
+            }
+            // once per set: by the group that holds the item's first stage
+            if (kSecond && !G::kBf16 && ring.it % G::kGroups == group && t == 0) reds[(q + 1) * G::kRed - 8 + g] = ainv[n];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.red_full(q));
+    }
+}
+
+template <int kFmt, bool kSecond, int NT>
+__device__ __forceinline__ void consume_item(const Args& p, Ring<kFmt>& ring, int& set, float* reds, const Tables& tb, int a, int r0,
+                                             int warp, int lane, volatile int* abort_flag) {
+    consume<kFmt, kSecond, NT>(p, ring, reds, tb, a, r0, set, warp, lane, abort_flag);
+    set += (tb.start[a + 1] - tb.start[a] + 7) / 8;
+    ring.it += ((kSecond ? p.I : p.H) + Geo<kFmt>::kStepK - 1) / Geo<kFmt>::kStepK;
+}
+
+// The sum of the groups' parts of one value of a set; the item's stages begin at `it` and are `steps` many.
+template <int kFmt>
+__device__ __forceinline__ float red_sum(const float* red, int it, int steps, int col, int row) {
+    using G = Geo<kFmt>;
+    float s = 0.0f;
+    if (steps >= G::kGroups) {
+#pragma unroll
+        for (int i = 0; i < G::kGroups; ++i) s += red[i * G::kRedGroup + col * G::kRedCol + row];
+    } else {
+        for (int i = 0; i < steps; ++i) s += red[(it + i) % G::kGroups * G::kRedGroup + col * G::kRedCol + row];
+    }
+    return s;
+}
+
+// Epilogue warp w (0 or 1) of an item of the first product: half of its outputs, SwiGLU and the row's largest magnitude.
+template <int kFmt>
+__device__ __forceinline__ void finish_first(const Args& p, Ring<kFmt>& ring, int& set, const float* reds, const Tables& tb, int a,
+                                             int r0, int w, int lane, volatile int* abort_flag) {
+    using G = Geo<kFmt>;
+    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, Kt = p.K + p.S;
+    const int steps = (p.H + G::kStepK - 1) / G::kStepK, tiles = (n_rows + 7) / 8;
+    for (int n = 0; n < tiles; ++n, ++set) {
+        const int q = set % G::kReds;
+        const float* red = reds + q * G::kRed;
+        // FP8, FP4: 8 outputs of four columns at a time; BF16: 32 outputs of one column
+        constexpr int kCols = G::kBf16 ? 1 : 4;
+        const int j = G::kBf16 ? w * 32 + lane : w * 8 + (lane & 7);
+        float inv[8 / kCols];
+#pragma unroll
+        for (int i = 0; i < 8 / kCols; ++i) {
+            const int c = n * 8 + i * kCols + (G::kBf16 ? 0 : lane >> 3);
+            inv[i] = !G::kBf16 && c < n_rows ? __ldcg(p.xinv + tb.row[begin + c] / Kt) : 1.0f;
+        }
+        mbar_wait(ring.red_full(q), (uint32_t)(set / G::kReds) & 1u, p.hdr, abort_flag);
+#pragma unroll
+        for (int i = 0; i < 8 / kCols; ++i) {
+            const int cc = i * kCols + (G::kBf16 ? 0 : lane >> 3), c = n * 8 + cc;
+            const float g = red_sum<kFmt>(red, ring.it, steps, cc, j) * inv[i];
+            const float u = red_sum<kFmt>(red, ring.it, steps, cc, G::kOut1 + j) * inv[i];
+            const float v = swiglu1(g, u, p.clamp);
+            if (c < n_rows) {
+                const int slot = tb.row[begin + c];
+                p.act[(int64_t)slot * p.I + r0 + j] = v;
+                if constexpr (!G::kBf16) {
+                    uint32_t top = __float_as_uint(v) & 0x7fffffffu;
+                    const uint32_t eight = 0xffu << (lane & 24);
+                    top = __reduce_max_sync(eight, top);
+                    if ((lane & 7) == 0) atomicMax(p.amax + slot, top);
                 }
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(ring.empty(s));
-        sc = sc_next;
-        if constexpr (kAhead)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) cols[n] = next[n];
+        if (lane == 0) mbar_arrive(ring.red_empty(q));
     }
-}
-
-struct Shared {
-    float* red;    // two sets of partial sums
-    float* y;      // [T][rows of an item]
-    Tables* tb;
-    int red_at = 0;
-};
-
-// A warp's sums of column tile n to the next set of partial sums, and wait for everybody's.
-template <int kFmt, int NT>
-__device__ __forceinline__ const float* gather(Shared& sh, const float (&acc)[Geo<kFmt>::kMt][NT][4], int n, int warp, int lane) {
-    using G = Geo<kFmt>;
-    float* red = sh.red + sh.red_at * G::kRed;
-    sh.red_at ^= 1;
-    float* dst = red + (G::kBf16 ? warp & 3 : warp) * G::kRedSlice + (G::kBf16 ? (warp >> 2) * 64 : 0);
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int m = 0; m < G::kMt; ++m) {
-        const int r0 = G::kBf16 ? m * 16 + g : m * 8 + perm(g), r1 = G::kBf16 ? r0 + 8 : r0 + 16;
-        dst[(2 * t) * G::kRedCol + r0] = acc[m][n][0];
-        dst[(2 * t + 1) * G::kRedCol + r0] = acc[m][n][1];
-        dst[(2 * t) * G::kRedCol + r1] = acc[m][n][2];
-        dst[(2 * t + 1) * G::kRedCol + r1] = acc[m][n][3];
-    }
-    consumer_sync();
-    return red;
-}
-template <int kFmt>
-__device__ __forceinline__ float red_sum(const float* red, int col, int row) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < Geo<kFmt>::kSlices; ++i) s += red[i * Geo<kFmt>::kRedSlice + col * Geo<kFmt>::kRedCol + row];
-    return s;
-}
-
-// An item of the first product: outputs [r0, r0 + kOut1) of active expert a for its rows.
-template <int kFmt, int NT>
-__device__ __forceinline__ void first_item(const Args& p, Ring<kFmt> ring, Shared sh, int a, int r0, int warp, int lane,
-                                        volatile int* abort_flag) {
-    using G = Geo<kFmt>;
-    Tables& tb = *sh.tb;
-    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, Kt = p.K + p.S;
-    const void* rows[NT];
-    float ascale[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int c = n * 8 + (lane >> 2);
-        rows[n] = nullptr;
-        ascale[n] = 1.0f;
-        if (c < n_rows) rows[n] = (G::kBf16 ? p.x : p.x16) + (int64_t)(tb.row[begin + c] / Kt) * p.H;
-    }
-    float acc[G::kMt][NT][4];
-    multiply<kFmt, false, NT>(p, ring, rows, ascale, tb.expert[a], r0, warp, lane, abort_flag, acc);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const float* red = gather<kFmt, NT>(sh, acc, n, warp, lane);
-        // warp w: column w of the tile
-        const int c = n * 8 + warp;
-        const bool on = c < n_rows;
-        const int slot = on ? tb.row[begin + c] : 0;
-        const float inv = G::kBf16 || !on ? 1.0f : __ldcg(p.xinv + slot / Kt);
-        uint32_t top = 0;
-        float* dst = p.act + (int64_t)slot * p.I + r0;
-        if constexpr (G::kBf16) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = i * 32 + lane;
-                const float v = swiglu1(red_sum<kFmt>(red, warp, j), red_sum<kFmt>(red, warp, 64 + j), p.clamp);
-                if (on) dst[j] = v;
-            }
-        } else {
-            // rows 0-15: gate; 16-31: up of the same outputs
-            const float h = red_sum<kFmt>(red, warp, lane) * inv;
-            const float u = __shfl_down_sync(0xffffffffu, h, 16);
-            const bool gate = lane < 16;
-            const float v = swiglu1(h, u, p.clamp);
-            if (on && gate) dst[lane] = v;
-            top = __reduce_max_sync(0xffffffffu, gate ? __float_as_uint(v) & 0x7fffffffu : 0u);
-            if (on && lane == 0) atomicMax(p.amax + slot, top);
-        }
-    }
-    consumer_sync();  // every warp's values are written
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
         __threadfence();
         atomicAdd(p.dep + a, 1);
     }
+    ring.it += steps;
 }
 
-// An item of the second product: hidden columns [r0, r0 + kRows) of active expert a, added to the CTA's sums.
-template <int kFmt, int NT>
-__device__ __forceinline__ void second_item(const Args& p, Ring<kFmt> ring, Shared sh, int a, int r0, int warp, int lane,
-                                         volatile int* abort_flag) {
+// Epilogue warp w of an item of the second product: half of its hidden columns, added to the CTA's sums of these columns.
+template <int kFmt>
+__device__ __forceinline__ void finish_second(const Args& p, Ring<kFmt>& ring, int& set, const float* reds, const Tables& tb, float* y,
+                                              int a, int w, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
-    Tables& tb = *sh.tb;
     const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, Kt = p.K + p.S;
-    const void* rows[NT];
-    float ascale[NT];
+    const int steps = (p.I + G::kStepK - 1) / G::kStepK, tiles = (n_rows + 7) / 8;
+    for (int n = 0; n < tiles; ++n, ++set) {
+        const int q = set % G::kReds;
+        const float* red = reds + q * G::kRed;
+        // FP8, FP4: 16 hidden columns of two rows at a time; BF16: 64 of one row, two a lane
+        constexpr int kCols = G::kBf16 ? 1 : 2;
+        int slot[8 / kCols];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int c = n * 8 + (lane >> 2);
-        rows[n] = nullptr;
-        ascale[n] = 1.0f;
-        if (c < n_rows) {
-            const int slot = tb.row[begin + c];
-            rows[n] = p.act + (int64_t)slot * p.I;
-            float inverse;
-            if constexpr (!G::kBf16) ascale[n] = row_scale(__ldcg(p.amax + slot), &inverse);
+        for (int i = 0; i < 8 / kCols; ++i) {
+            const int c = n * 8 + i * kCols + (G::kBf16 ? 0 : lane >> 4);
+            slot[i] = c < n_rows ? tb.row[begin + c] : -1;
         }
-    }
-    float acc[G::kMt][NT][4];
-    multiply<kFmt, true, NT>(p, ring, rows, ascale, tb.expert[a], r0, warp, lane, abort_flag, acc);
+        mbar_wait(ring.red_full(q), (uint32_t)(set / G::kReds) & 1u, p.hdr, abort_flag);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const float* red = gather<kFmt, NT>(sh, acc, n, warp, lane);
-        const int c = n * 8 + warp;
-        if (c < n_rows) {
-            const int slot = tb.row[begin + c];
-            float w = tb.weight[slot];
-            if constexpr (!G::kBf16) {
-                float inverse;
-                row_scale(__ldcg(p.amax + slot), &inverse);
-                float* y = sh.y + (slot / Kt) * G::kRows + lane;
-                *y = fmaf(red_sum<kFmt>(red, warp, lane) * inverse, w, *y);
-            } else {
+        for (int i = 0; i < 8 / kCols; ++i) {
+            const int cc = i * kCols + (G::kBf16 ? 0 : lane >> 4);
+            if (slot[i] >= 0) {
+                const float weight = tb.weight[slot[i]], f = G::kBf16 ? 1.0f : red[G::kRed - 8 + cc];
 #pragma unroll
-                for (int i = 0; i < G::kRows / 32; ++i) {
-                    float* y = sh.y + (slot / Kt) * G::kRows + i * 32 + lane;
-                    *y = fmaf(red_sum<kFmt>(red, warp, i * 32 + lane), w, *y);
+                for (int h = 0; h < (G::kBf16 ? 2 : 1); ++h) {
+                    const int r = G::kBf16 ? w * 64 + h * 32 + lane : w * 16 + (lane & 15);
+                    float* dst = y + slot[i] / Kt * G::kRows + r;
+                    *dst = fmaf(red_sum<kFmt>(red, ring.it, steps, cc, r) * f, weight, *dst);
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.red_empty(q));
     }
+    ring.it += steps;
 }
 
-template <int kFmt, bool kSecond>
-__device__ __forceinline__ void run_item(const Args& p, Ring<kFmt>& at, Shared& now, int a, int r0, int warp, int lane,
-                                         volatile int* abort_flag) {
-    const int n = now.tb->start[a + 1] - now.tb->start[a];
-    const Ring<kFmt> ring = at;
-    const Shared sh = now;
-    at.it += ((kSecond ? p.I : p.H) + Geo<kFmt>::kStepK - 1) / Geo<kFmt>::kStepK;
-    if (n <= 8) now.red_at ^= 1;  // one set of partial sums a column tile: 1, 2, 4 or 8
-    if constexpr (kSecond) {
-        if (n <= 8) return second_item<kFmt, 1>(p, ring, sh, a, r0, warp, lane, abort_flag);
-        if (n <= 16) return second_item<kFmt, 2>(p, ring, sh, a, r0, warp, lane, abort_flag);
-        if (n <= 32) return second_item<kFmt, 4>(p, ring, sh, a, r0, warp, lane, abort_flag);
-        return second_item<kFmt, 8>(p, ring, sh, a, r0, warp, lane, abort_flag);
-    } else {
-        if (n <= 8) return first_item<kFmt, 1>(p, ring, sh, a, r0, warp, lane, abort_flag);
-        if (n <= 16) return first_item<kFmt, 2>(p, ring, sh, a, r0, warp, lane, abort_flag);
-        if (n <= 32) return first_item<kFmt, 4>(p, ring, sh, a, r0, warp, lane, abort_flag);
-        return first_item<kFmt, 8>(p, ring, sh, a, r0, warp, lane, abort_flag);
-    }
-}
-
-// The CTA's sums of column group g are complete as far as its run goes: to y, or to the workspace where other CTAs have
-// experts of these columns too.
+// The CTA's sums of column group g are complete as far as its run goes (both epilogue warps): to y, or to the workspace where
+// other CTAs have experts of these columns too.
 template <int kFmt>
-__device__ void finish_columns(const Args& p, Shared& sh, const Work<kFmt>& wk, int g) {
+__device__ void finish_columns(const Args& p, Tables& tb, float* y, const Work<kFmt>& wk, int g, int tid) {
     using G = Geo<kFmt>;
     constexpr int R = G::kRows;
     const int first = g * wk.n_active, last = first + wk.n_active - 1, n = p.T * R;
-    consumer_sync();  // the last item's sums are in place
+    epilogue_sync();  // both warps' sums are in place
     if (wk.lo2 <= first && wk.hi2 > last) {
-        for (int i = threadIdx.x; i < n; i += 256) {
-            p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(sh.y[i]);
-            sh.y[i] = 0.0f;
+        for (int i = tid; i < n; i += 32 * kEpiWarps) {
+            p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(y[i]);
+            y[i] = 0.0f;
         }
+        epilogue_sync();
         return;
     }
     // the CTAs with experts of these columns, in order (with fewer items than CTAs, some in between have none)
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         int parts = 0;
         for (int i = first; i <= last; ++parts) {
             const int c = Work<kFmt>::owner(p, wk.n_active, i);
-            sh.tb->count[parts] = c;
+            tb.count[parts] = c;
             i = Work<kFmt>::first(p, wk.n_active, c + 1);
         }
-        sh.tb->last = parts;
+        tb.last = parts;
     }
-    consumer_sync();
-    const int parts = sh.tb->last;
+    epilogue_sync();
+    const int parts = tb.last;
     // a CTA's first column group goes to its first buffer, its last to the second
     auto buffer = [&](int cta) {
         const int at = Work<kFmt>::first(p, wk.n_active, cta);
         return p.part + ((int64_t)cta * 2 + (at / wk.n_active == g ? 0 : 1)) * kMaxT * R;
     };
     float* mine = buffer(blockIdx.x);
-    for (int i = threadIdx.x; i < n; i += 256) {
-        mine[i] = sh.y[i];
-        sh.y[i] = 0.0f;
+    for (int i = tid; i < n; i += 32 * kEpiWarps) {
+        mine[i] = y[i];
+        y[i] = 0.0f;
     }
-    consumer_sync();
-    if (threadIdx.x == 0) {
+    epilogue_sync();
+    if (tid == 0) {
         __threadfence();
         // counts up to the last part and is zero again then
-        sh.tb->last = atomicInc(reinterpret_cast<unsigned*>(p.cols) + g, (unsigned)(parts - 1)) == (unsigned)(parts - 1);
+        tb.last = atomicInc(reinterpret_cast<unsigned*>(p.cols) + g, (unsigned)(parts - 1)) == (unsigned)(parts - 1);
         __threadfence();
     }
-    consumer_sync();
-    if (!sh.tb->last) return;
-    for (int i = threadIdx.x; i < n; i += 256) {
-        float s = 0.0f;
-        for (int c = 0; c < parts; ++c) s += __ldcg(buffer(sh.tb->count[c]) + i);
-        p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(s);
-    }
+    epilogue_sync();
+    if (tb.last)
+        for (int i = tid; i < n; i += 32 * kEpiWarps) {
+            float s = 0.0f;
+            for (int c = 0; c < parts; ++c) s += __ldcg(buffer(tb.count[c]) + i);
+            p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(s);
+        }
+    epilogue_sync();
 }
 
-template <int kFmt>
+// NT: column tiles that an expert can have (T <= 8 NT).
+template <int kFmt, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     layer_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2,
                  const __grid_constant__ Args p) {
@@ -872,10 +898,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     Tables& tb = *reinterpret_cast<Tables*>(smem + G::kTabOff);
-    Shared sh;
-    sh.red = reinterpret_cast<float*>(smem + G::kRedOff);
-    sh.tb = &tb;
-    sh.y = reinterpret_cast<float*>(smem + G::kTabOff + ((sizeof(Tables) + 15) & ~size_t(15)));
+    float* reds = reinterpret_cast<float*>(smem + G::kRedOff);
+    float* y = reinterpret_cast<float*>(smem + G::kTabOff + ((sizeof(Tables) + 15) & ~size_t(15)));
     volatile int* abort_flag = &tb.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Ring<kFmt> ring;
@@ -884,12 +908,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
             mbar_init(ring.full(s), 1);
-            mbar_init(ring.empty(s), kWarps);
+            mbar_init(ring.empty(s), G::kGroupWarps);
+        }
+        for (int s = 0; s < G::kReds; ++s) {
+            mbar_init(ring.red_full(s), kWarps);
+            mbar_init(ring.red_empty(s), kEpiWarps);
         }
         tb.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int i = threadIdx.x; i < p.T * G::kRows; i += kThreads) sh.y[i] = 0.0f;
+    for (int i = threadIdx.x; i < p.T * G::kRows; i += kThreads) y[i] = 0.0f;
     __syncthreads();
 
     // ---- phase 1
@@ -897,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.router) router_phase(p, warp, lane);
     if constexpr (!G::kBf16)
         for (int t = (int)gridDim.x - 1 - (int)blockIdx.x; t < p.T; t += gridDim.x)
-            round_x(p, t, reinterpret_cast<uint32_t*>(sh.red));
+            round_x(p, t, reinterpret_cast<uint32_t*>(reds));
     if (p.router || !G::kBf16) grid_barrier(p, ++barriers, abort_flag);
 
     // ---- phase 2
@@ -905,8 +933,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float* weights = p.weights_io;
     if (p.router) {
         const bool all = p.T <= kWarps;  // every CTA selects for all tokens
-        int32_t* to_ids = all ? reinterpret_cast<int32_t*>(sh.red) : p.ids;
-        float* to_w = all ? sh.red + kWarps * 32 : p.weights;
+        int32_t* to_ids = all ? reinterpret_cast<int32_t*>(reds) : p.ids;
+        float* to_w = all ? reds + kWarps * 32 : p.weights;
         float* scratch = reinterpret_cast<float*>(smem) + warp * (kMaxE + 32);
         const int t0 = all ? warp : (int)blockIdx.x + warp * (int)gridDim.x;
         if (warp < kWarps && t0 < p.T) {
@@ -934,29 +962,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- phases 3 and 4
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
-        bool ok = warp == kWarps;
-        for (int i = blockIdx.x; i < wk.n1 && ok; i += gridDim.x)
-            ok = produce<kFmt, false>(p, &map1, ring, tb.expert[i / wk.per1], i % wk.per1 * G::kOut1, lane, abort_flag);
-        for (int i = wk.lo2; i < wk.hi2 && ok; ++i)
-            ok = produce<kFmt, true>(p, &map2, ring, tb.expert[i % wk.n_active], i / wk.n_active * G::kRows, lane, abort_flag);
-        // drain: every copy issued has landed (bounded)
-        for (int j = max(0, ring.it - G::kStages); j < ring.it; ++j)
-            if (!mbar_drain(ring.full(j % G::kStages), (uint32_t)(j / G::kStages) & 1u, p.hdr)) break;
+        if (warp == kWarps) {
+            bool ok = true;
+            for (int i = blockIdx.x; i < wk.n1 && ok; i += gridDim.x)
+                ok = produce<kFmt, false>(p, &map1, ring, tb.expert[i / wk.per1], i % wk.per1 * G::kOut1, lane, abort_flag);
+            for (int i = wk.lo2; i < wk.hi2 && ok; ++i)
+                ok = produce<kFmt, true>(p, &map2, ring, tb.expert[i % wk.n_active], i / wk.n_active * G::kRows, lane, abort_flag);
+            // drain: every copy issued has landed (bounded)
+            for (int j = max(0, ring.it - G::kStages); j < ring.it; ++j)
+                if (!mbar_drain(ring.full(j % G::kStages), (uint32_t)(j / G::kStages) & 1u, p.hdr)) break;
+        } else if (warp <= kWarps + kEpiWarps) {
+            const int w = warp - kWarps - 1;
+            int set = 0;
+            for (int i = blockIdx.x; i < wk.n1; i += gridDim.x)
+                finish_first<kFmt>(p, ring, set, reds, tb, i / wk.per1, i % wk.per1 * G::kOut1, w, lane, abort_flag);
+            for (int i = wk.lo2; i < wk.hi2; ++i) {
+                finish_second<kFmt>(p, ring, set, reds, tb, y, i % wk.n_active, w, lane, abort_flag);
+                if (i + 1 == wk.hi2 || (i + 1) % wk.n_active == 0) finish_columns<kFmt>(p, tb, y, wk, i / wk.n_active, w * 32 + lane);
+            }
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        int set = 0;
         for (int i = blockIdx.x; i < wk.n1; i += gridDim.x)
-            run_item<kFmt, false>(p, ring, sh, i / wk.per1, i % wk.per1 * G::kOut1, warp, lane, abort_flag);
+            consume_item<kFmt, false, NT>(p, ring, set, reds, tb, i / wk.per1, i % wk.per1 * G::kOut1, warp, lane, abort_flag);
         for (int i = wk.lo2; i < wk.hi2; ++i) {
-            const int a = i % wk.n_active, g = i / wk.n_active;
-            if (i - wk.lo2 < wk.n_active) {  // the run's first item of this expert: wait for its rows
-                if (threadIdx.x == 0) {
-                    wait_count(p.dep + a, wk.per1, p.hdr, abort_flag);
-                    __threadfence();
-                }
-                consumer_sync();
+            const int a = i % wk.n_active;
+            if (i - wk.lo2 < wk.n_active) {  // the run's first item of this expert: wait for its rows (both epilogue warps count)
+                if (lane == 0) wait_count(p.dep + a, kEpiWarps * wk.per1, p.hdr, abort_flag);
+                __syncwarp();
             }
-            run_item<kFmt, true>(p, ring, sh, a, g * G::kRows, warp, lane, abort_flag);
-            if (i + 1 == wk.hi2 || (i + 1) % wk.n_active == 0) finish_columns<kFmt>(p, sh, wk, g);
+            consume_item<kFmt, true, NT>(p, ring, set, reds, tb, a, i / wk.n_active * G::kRows, warp, lane, abort_flag);
         }
     }
     if (wk.n_active == 0)
@@ -984,13 +1020,14 @@ constexpr size_t smem_bytes(int T) {
     return 1024 + (size_t)Geo<kFmt>::kTabOff + ((sizeof(Tables) + 15) & ~size_t(15)) + (size_t)T * Geo<kFmt>::kRows * 4;
 }
 
-template <int kFmt>
-cudaError_t launch_fmt(const Args& p, cudaStream_t s) {
+template <int kFmt, int NT>
+cudaError_t launch_tiles(const Args& p, cudaStream_t s) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     static_assert(smem_bytes<kFmt>(kMaxT) <= 232448, "shared memory");
     std::call_once(once, [] {
-        err = cudaFuncSetAttribute(layer_kernel<kFmt>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<kFmt>(kMaxT));
+        err = cudaFuncSetAttribute(layer_kernel<kFmt, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<kFmt>(kMaxT));
+        if (err == cudaSuccess) err = check_register_split(reinterpret_cast<const void*>(layer_kernel<kFmt, NT>), kLaunchRegs);
     });
     if (err != cudaSuccess) return err;
     CUtensorMap m1 = {}, m2 = {};
@@ -1023,7 +1060,15 @@ cudaError_t launch_fmt(const Args& p, cudaStream_t s) {
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, layer_kernel<kFmt>, m1, m2, p);
+    return cudaLaunchKernelEx(&cfg, layer_kernel<kFmt, NT>, m1, m2, p);
+}
+
+template <int kFmt>
+cudaError_t launch_fmt(const Args& p, cudaStream_t s) {
+    if (p.T <= 8) return launch_tiles<kFmt, 1>(p, s);
+    if (p.T <= 16) return launch_tiles<kFmt, 2>(p, s);
+    if (p.T <= 32) return launch_tiles<kFmt, 4>(p, s);
+    return launch_tiles<kFmt, 8>(p, s);
 }
 
 }  // namespace

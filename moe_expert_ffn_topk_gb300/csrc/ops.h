@@ -23,6 +23,14 @@ inline moe_gate_options default_gate_options() {
     o.route_scale = 1.0f;
     return o;
 }
+// setmaxnreg hands out the registers that a launch holds; a split made for `regs` a thread would wait for ever in a build of the
+// kernel that holds fewer, so such a build is refused before its first launch.
+inline cudaError_t check_register_split(const void* kernel, int regs) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    return e != cudaSuccess ? e : a.numRegs >= regs ? cudaSuccess : cudaErrorLaunchOutOfResources;
+}
+
 bool gate_options_ok(const moe_gate_options& o, int E, int K);
 
 cudaError_t launch_gate(const void* logits, int type, int64_t stride, const float* bias, const moe_gate_options& o, int T,

@@ -388,7 +388,8 @@ def layer_reference(x, ids, weights, w1, w2, E, S, clamp=None):
 
 LAYER_SHAPES = [(1, 128, 128, 1, 1, 0), (1, 256, 128, 8, 2, 1), (3, 512, 384, 8, 2, 0), (5, 384, 256, 60, 6, 0), (8, 1024, 128, 32, 4, 1),
                 (9, 256, 640, 16, 3, 2), (17, 640, 128, 300, 8, 0), (33, 256, 256, 12, 4, 1), (64, 384, 128, 5, 5, 0),
-                (64, 128, 256, 3, 1, 0), (40, 896, 384, 128, 8, 1)]
+                (64, 128, 256, 3, 1, 0), (40, 896, 384, 128, 8, 1), (1, 7168, 2048, 16, 8, 1), (12, 4224, 1152, 20, 3, 0),
+                (64, 2048, 4096, 4, 2, 1)]
 FORMATS = ["bf16", "fp8_block", "fp4_mx"]
 
 
