@@ -1,9 +1,8 @@
 // The router (moe_gate in moe_ops.h): expert ids and gate weights from logits, one warp per token.
 //
-// A row of up to 1024 logits lives in the warp's registers (E / 32 a lane), so it is read once, and every step after
-// that is a reduction over the warp: the maximum and sum of the softmax, the two best of every group (through shared
-// memory, as a group lies across lanes), and K rounds of "largest key, lowest index" (two warp-wide integer
-// reductions each). Bound by those rounds' latency, not by HBM.
+// A row of up to 1024 logits is read once, into shared memory, and every step after that is a reduction over the warp: the
+// maximum and sum of the softmax, the two best of every group, and K rounds of "largest key, lowest index" (two warp-wide
+// integer reductions each). Bound by those rounds' latency, not by HBM.
 #include "gate_select.cuh"
 
 namespace moe {
@@ -18,42 +17,28 @@ __device__ __forceinline__ float load_logit(const T* p) {
     else return *p;
 }
 
-template <typename T, int kV>
+template <typename T>
 __global__ void __launch_bounds__(32 * kWarps)
     gate_kernel(const T* __restrict__ logits, int64_t stride, const float* __restrict__ bias, moe_gate_options o, int tokens,
                 int E, int K, int32_t* __restrict__ ids, float* __restrict__ weights) {
-    extern __shared__ float scratch[];
+    extern __shared__ float smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarps + warp;
     if (t >= tokens) return;
     const T* row = logits + (int64_t)t * stride;
-    float v[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int e = i * 32 + lane;
-        const float l = e < E ? load_logit(row + e) : -INFINITY;
-        v[i] = l == l ? l : -INFINITY;
-    }
-    gate_token<kV>(v, bias, o, E, K, scratch + warp * (E + 32), lane, ids + (int64_t)t * K, weights + (int64_t)t * K);
-}
-
-template <typename T, int kV>
-cudaError_t launch_v(const void* logits, int64_t stride, const float* bias, const moe_gate_options& o, int T_, int E, int K,
-                     int32_t* ids, float* weights, cudaStream_t s) {
-    const size_t smem = o.num_groups > 1 ? sizeof(float) * kWarps * (E + 32) : 0;
-    gate_kernel<T, kV><<<(T_ + kWarps - 1) / kWarps, 32 * kWarps, smem, s>>>(static_cast<const T*>(logits), stride, bias, o, T_,
-                                                                            E, K, ids, weights);
-    return cudaGetLastError();
+    float* scratch = smem + warp * gate_scratch(E);
+#pragma unroll 8
+    for (int e = lane; e < E; e += 32) scratch[e] = load_logit(row + e);
+    gate_token(scratch, bias, o, E, K, lane, ids + (int64_t)t * K, weights + (int64_t)t * K);
 }
 
 template <typename T>
 cudaError_t launch_t(const void* logits, int64_t stride, const float* bias, const moe_gate_options& o, int T_, int E, int K,
                      int32_t* ids, float* weights, cudaStream_t s) {
-    if (E <= 64) return launch_v<T, 2>(logits, stride, bias, o, T_, E, K, ids, weights, s);
-    if (E <= 128) return launch_v<T, 4>(logits, stride, bias, o, T_, E, K, ids, weights, s);
-    if (E <= 256) return launch_v<T, 8>(logits, stride, bias, o, T_, E, K, ids, weights, s);
-    if (E <= 512) return launch_v<T, 16>(logits, stride, bias, o, T_, E, K, ids, weights, s);
-    return launch_v<T, 32>(logits, stride, bias, o, T_, E, K, ids, weights, s);
+    const size_t smem = sizeof(float) * kWarps * gate_scratch(E);
+    gate_kernel<T><<<(T_ + kWarps - 1) / kWarps, 32 * kWarps, smem, s>>>(static_cast<const T*>(logits), stride, bias, o, T_, E, K, ids,
+                                                                        weights);
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -20,65 +20,74 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // divide of the activations are not used here)
 __device__ __forceinline__ float gate_sigmoid(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
 
-// One token. v: this lane's logits, expert i * 32 + lane in v[i], -inf where masked or past E. Selected experts go to
-// ids[0..K) and weights[0..K). scratch: E + 32 floats of shared memory of this warp (groups > 1 only).
-template <int kV>
-__device__ __forceinline__ void gate_token(float (&v)[kV], const float* bias, const moe_gate_options& o, int E, int K,
-                                           float* scratch, int lane, int32_t* ids, float* weights) {
+// Floats of shared memory that gate_token works in, per warp: logits, then choice keys (a few words apart per group, see there).
+__host__ __device__ inline int gate_scratch(int E) { return 2 * E + 32; }
+
+// One token, by one warp. scratch: gate_scratch(E) words of shared memory of this warp, its first E holding the logits (this
+// function separates its reads from their writes). Selected experts go to ids[0..K) and weights[0..K).
+//
+// Rows stay in shared memory, not in registers, and every loop is kept rolled: few tokens run this once, and then what counts
+// is how much code has to be fetched (with the row in registers and everything unrolled: twice the time for 7 tokens).
+__device__ __forceinline__ void gate_token(float* scratch, const float* bias, const moe_gate_options& o, int E, int K, int lane,
+                                           int32_t* ids, float* weights) {
     constexpr uint32_t kAll = 0xffffffffu;
+    const float* logit = scratch;
+    uint32_t* key = reinterpret_cast<uint32_t*>(scratch + E);
     const bool softmax = o.score == MOE_SCORE_SOFTMAX;
+    const bool groups = o.num_groups > 1;
+    // group of expert e: (e + 0.5) / size truncated, exact for e < 1024; `per` lanes scan a group, and keys of a group are `per`
+    // words further on than those of the one before, which keeps the lanes' banks apart
+    const int size = E / o.num_groups;
+    const float inv_size = __fdividef(1.0f, (float)size);
+    int per = 32;
+    while (per * o.num_groups > 32) per >>= 1;
+    const int pad = groups ? per : 0;
+    auto group_of = [&](int e) { return (int)(((float)e + 0.5f) * inv_size); };
+    __syncwarp();
+
     float top = -INFINITY, total = 1.0f;
-    bool inf = false;
     if (softmax) {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) top = fmaxf(top, v[i]);
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) top = fmaxf(top, logit[e]);  // fmaxf passes over NaNs
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-        inf = top == INFINITY;
+    }
+    const bool inf = top == INFINITY;
+    auto exp_of = [&](float l) { return inf ? (l == INFINITY ? 1.0f : 0.0f) : expf(l - top); };
+    if (softmax) {
         float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-            sum += inf ? (v[i] == INFINITY ? 1.0f : 0.0f) : v[i] == -INFINITY ? 0.0f : expf(v[i] - top);
+#pragma unroll 2
+        for (int e = lane; e < E; e += 32) {
+            const float l = logit[e];
+            sum += l > -INFINITY ? exp_of(l) : 0.0f;
+        }
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
         total = sum;
     }
-    auto score = [&](float l) {
-        if (!softmax) return gate_sigmoid(l);
-        return __fdiv_rn(inf ? (l == INFINITY ? 1.0f : 0.0f) : expf(l - top), total);
-    };
+    auto score = [&](float l) { return softmax ? __fdiv_rn(exp_of(l), total) : gate_sigmoid(l); };
 
     // choice keys: 0 = not available
-    uint32_t key[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int e = i * 32 + lane;
-        float c = v[i];
-        const bool on = e < E && c > -INFINITY;  // false for a NaN too
-        if (on && (bias || !softmax)) {
-            c = score(c);
-            if (bias) c += __ldg(bias + e);
-        }
-        key[i] = on && c == c ? order_key(c) : 0u;
+#pragma unroll 2
+    for (int e = lane; e < E; e += 32) {
+        float c = logit[e];
+        const float b = bias ? __ldg(bias + e) : 0.0f;
+        const bool on = c > -INFINITY;  // false for a NaN too
+        if (bias || !softmax) c = score(c);
+        if (bias) c += b;
+        key[e + group_of(e) * pad] = on && c == c ? order_key(c) : 0u;
     }
 
-    if (o.num_groups > 1) {
-        // every group is scanned by `per` lanes; padding by `per` floats a group keeps their banks apart
-        const int G = o.num_groups, size = E / G;
-        int per = 1;
-        while (per * 2 * G <= 32) per *= 2;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int e = i * 32 + lane;
-            if (e < E) scratch[e + e / size * per] = key[i] ? key_value(key[i]) : -INFINITY;
-        }
+    uint32_t kept = ~0u;  // bit g: the experts of group g are eligible
+    if (groups) {
         __syncwarp();
-        const int g = lane / per, sub = lane % per;
-        float a = -INFINITY, b = -INFINITY;  // the two largest, a >= b
-        if (g < G) {
-            const int first = g * (size + per);
+        const int g = lane / per, sub = lane & (per - 1);
+        float a = -INFINITY, b = -INFINITY;  // the group's two largest, a >= b
+        if (g < o.num_groups) {
+#pragma unroll 4
             for (int j = sub; j < size; j += per) {
-                const float c = scratch[first + j];
+                const uint32_t k = key[g * (size + pad) + j];
+                const float c = k ? key_value(k) : -INFINITY;
                 b = fmaxf(b, fminf(a, c));
                 a = fmaxf(a, c);
             }
@@ -88,61 +97,46 @@ __device__ __forceinline__ void gate_token(float (&v)[kV], const float* bias, co
             b = fmaxf(fminf(a, a2), fmaxf(b, b2));
             a = fmaxf(a, a2);
         }
-        const float rank = o.group_top == 1 || size == 1 ? a : a + b;
-        uint32_t rk = g < G && sub == 0 ? order_key(rank) : 0u;  // of -inf too: a fully masked group still has a rank
-        uint32_t kept = 0;                                       // bit g
+        // of a fully masked group too: -inf is a rank
+        uint32_t rank = g < o.num_groups && sub == 0 ? order_key(o.group_top == 1 || size == 1 ? a : a + b) : 0u;
+        kept = 0u;
         for (int k = 0; k < o.topk_groups; ++k) {
-            const uint32_t best = __reduce_max_sync(kAll, rk);
-            const int win = __ffs(__ballot_sync(kAll, rk == best)) - 1;  // the lowest lane: the lowest group
-            kept |= 1u << (win / per);
-            if (lane == win) rk = 0u;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int e = i * 32 + lane;
-            if (e < E && !((kept >> (e / size)) & 1u)) key[i] = 0u;
+            const uint32_t best = __reduce_max_sync(kAll, rank);
+            const int win = __ffs(__ballot_sync(kAll, rank == best)) - 1;  // the lowest lane: the lowest group
+            kept |= 1u << __shfl_sync(kAll, g, win);
+            if (lane == win) rank = 0u;
         }
     }
 
-    // K rounds of "largest key, lowest index"; lane k keeps the k-th
+    // K rounds of "largest key, lowest index"; lane k keeps the k-th. Each lane knows the best of its own experts.
     uint32_t mine = 0;
     int at = 0;
-    auto local_best = [&]() {
+    auto own_best = [&]() {
         mine = 0;
-        at = 0;
-#pragma unroll
-        for (int i = 0; i < kV; ++i)
-            if (key[i] > mine) {
-                mine = key[i];
-                at = i;
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) {
+            const int g = group_of(e);
+            const uint32_t k = (kept >> g) & 1u ? key[e + g * pad] : 0u;
+            if (k > mine) {
+                mine = k;
+                at = e;
             }
+        }
     };
-    local_best();
+    own_best();
     int my_id = -1;
-    float my_logit = 0.0f;
     for (int k = 0; k < K; ++k) {
         const uint32_t best = __reduce_max_sync(kAll, mine);
         if (best == 0u) break;
-        const uint32_t e = __reduce_min_sync(kAll, mine == best ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
-        const int owner = (int)(e & 31u);
-        float l = 0.0f;
-        if (lane == owner) {
-#pragma unroll
-            for (int i = 0; i < kV; ++i)
-                if (i == at) {
-                    l = v[i];
-                    key[i] = 0u;
-                }
-            local_best();
+        const int e = (int)__reduce_min_sync(kAll, mine == best ? (uint32_t)at : 0xffffffffu);
+        if (lane == k) my_id = e;
+        if (lane == (e & 31)) {
+            key[e + group_of(e) * pad] = 0u;
+            own_best();
         }
-        l = __shfl_sync(kAll, l, owner);
-        if (lane == k) {
-            my_id = (int)e;
-            my_logit = l;
-        }
+        __syncwarp();
     }
-    float w = my_id >= 0 ? score(my_logit) : 0.0f;
+    float w = my_id >= 0 ? score(logit[my_id]) : 0.0f;
     if (o.normalize) {
         float sum = w;
 #pragma unroll

@@ -10,8 +10,8 @@
 // second, while the consumers wait for activations.
 //
 // Phases:
-//   1. router: every warp takes (expert, part of H) dot products with all tokens in fp32 (CUDA cores: the selection
-//      compares these sums); one CTA per token also rounds x to the f16 operand of the FP8 and FP4 formats. Grid barrier.
+//   1. router: every CTA takes its experts' dot products with all tokens in fp32, its warps on parts of H (CUDA cores: the
+//      selection compares these sums); one CTA per token also rounds x to the f16 operand of the FP8 and FP4 formats. Grid barrier.
 //   2. selection: each CTA selects for all tokens itself (up to 8 tokens), or for its share of them and a second barrier.
 //      Each CTA then lists the experts with rows and their rows in shared memory.
 //   3. first product: items of 16 outputs (16 gate and 16 up rows of W1; BF16: 64 and 64) of one expert, dealt to the CTAs in
@@ -59,7 +59,6 @@ constexpr int kMaxT = MOE_LAYER_MAX_TOKENS;
 constexpr int kMaxSlots = kMaxT * 32;
 constexpr int kEpiWarps = 2;                    // warps 9 and 10 take the sums of an item further
 constexpr int kMaxE = 1024;
-constexpr int kMaxChunks = 8;                   // parts of H in the router product
 
 // Stage geometry. K-contiguous formats: two boxes of 32 rows x 128 bytes. BF16: 64 of K x two boxes of 64 columns. All boxes
 // have the 128-byte swizzle (the 16-byte unit u of line r is at u ^ (r % 8)). A warp multiplies a stage in four slices of K.
@@ -113,13 +112,12 @@ struct Args {
     moe_gate_options gate;
     int router_bf16;
     int T, H, I, E, K, S;
-    int chunks;  // parts of H in the router product
     float clamp;
     int32_t* hdr;      // [0] error word, [1] barrier, [2] CTAs finished
     int32_t* dep;      // per active expert: finished items of the first product
     int32_t* cols;     // per column group: parts that have arrived
     uint32_t* amax;    // per slot: largest |activation| so far, as bits
-    float* logits;     // [chunks][T][E]
+    float* logits;     // [T][E]
     int32_t* ids;      // [T][K]
     float* weights;    // [T][K]
     uint16_t* x16;     // f16 [T][H]
@@ -210,57 +208,82 @@ __device__ __forceinline__ void grid_barrier(const Args& p, int n, volatile int*
 // phase 1: the router product
 // ---------------------------------------------------------------------------------------
 
-// Dot products of one expert's router row with 8 tokens over vectors [v0, v1) of 8 values.
-template <bool kRouterBf16>
-__device__ __forceinline__ void router_dots(const Args& p, int e, int t0, int v0, int v1, int lane, float (&sum)[8]) {
+// Adds the products of one 16-byte vector of x with 8 router values.
+__device__ __forceinline__ float dot8(uint4 w, const float (&r)[8], float sum) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-    for (int v = v0 + lane; v < v1; v += 32) {
-        float r[8];
-        if constexpr (kRouterBf16) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.router) + (int64_t)e * p.H) + v);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                r[2 * i] = __uint_as_float(u[i] << 16);
-                r[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            }
-        } else {
-            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.router) + (int64_t)e * p.H) + 2 * v;
-            const float4 a = __ldg(q), b = __ldg(q + 1);
-            r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (t0 + j >= p.T) break;
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + j) * p.H) + v);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum[j] = fmaf(__uint_as_float(u[i] << 16), r[2 * i], sum[j]);
-                sum[j] = fmaf(__uint_as_float(u[i] & 0xffff0000u), r[2 * i + 1], sum[j]);
-            }
-        }
+    for (int i = 0; i < 4; ++i) {
+        sum = fmaf(__uint_as_float(u[i] << 16), r[2 * i], sum);
+        sum = fmaf(__uint_as_float(u[i] & 0xffff0000u), r[2 * i + 1], sum);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+    return sum;
 }
 
-__device__ void router_phase(const Args& p, int warp, int lane) {
-    const int vecs = p.H / 8, per = (vecs + p.chunks - 1) / p.chunks, groups = (p.T + 7) / 8;
-    const int units = p.E * p.chunks * groups;
-    for (int u = blockIdx.x + warp * gridDim.x; u < units; u += gridDim.x * kAllWarps) {
-        const int e = u % p.E, c = u / p.E % p.chunks, t0 = u / (p.E * p.chunks) * 8;
-        float sum[8];
-        const int v0 = c * per, v1 = min(vecs, v0 + per);
-        if (p.router_bf16) router_dots<true>(p, e, t0, v0, v1, lane, sum);
-        else router_dots<false>(p, e, t0, v0, v1, lane, sum);
-        if (lane == 0)
+__device__ __forceinline__ void router_values(const Args& p, int e, int v, float (&r)[8]) {
+    if (p.router_bf16) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.router) + (int64_t)e * p.H) + v);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r[2 * i] = __uint_as_float(u[i] << 16);
+            r[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    } else {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.router) + (int64_t)e * p.H) + 2 * v;
+        const float4 a = __ldg(q), b = __ldg(q + 1);
+        r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+    }
+}
+
+// The CTA's experts (two at a time: they share the reads of x), all warps on parts of H, 8 tokens at a time. parts: shared
+// memory of kAllWarps * 16 floats.
+__device__ void router_phase(const Args& p, float* parts, int warp, int lane) {
+    const int vecs = p.H / 8, grid = (int)gridDim.x;
+    for (int e0 = blockIdx.x; e0 < p.E; e0 += 2 * grid) {
+        const int e1 = e0 + grid;
+        const bool two = e1 < p.E;
+        for (int t0 = 0; t0 < p.T; t0 += 8) {
+            const int nt = min(8, p.T - t0);
+            float s0[8], s1[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s0[j] = s1[j] = 0.0f;
+            for (int v = warp * 32 + lane; v < vecs; v += 32 * kAllWarps) {
+                uint4 w[8];
+                float r0[8], r1[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < nt) w[j] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + j) * p.H) + v);
+                router_values(p, e0, v, r0);
+                router_values(p, two ? e1 : e0, v, r1);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < nt) {
+                        s0[j] = dot8(w[j], r0, s0[j]);
+                        s1[j] = dot8(w[j], r1, s1[j]);
+                    }
+            }
+            __syncthreads();  // the parts of the tokens before have been read
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (t0 + j < p.T) p.logits[((int64_t)c * p.T + t0 + j) * p.E + e] = sum[j];
+                if (j < nt) {
+#pragma unroll
+                    for (int d = 16; d >= 1; d >>= 1) {
+                        s0[j] += __shfl_xor_sync(0xffffffffu, s0[j], d);
+                        s1[j] += __shfl_xor_sync(0xffffffffu, s1[j], d);
+                    }
+                    if (lane == 0) {
+                        parts[warp * 16 + j] = s0[j];
+                        parts[warp * 16 + 8 + j] = s1[j];
+                    }
+                }
+            __syncthreads();
+            const int j = threadIdx.x & 7, which = threadIdx.x >> 3;
+            if (which < (two ? 2 : 1) && j < nt) {
+                float s = 0.0f;
+                for (int i = 0; i < kAllWarps; ++i) s += parts[i * 16 + which * 8 + j];
+                p.logits[(int64_t)(t0 + j) * p.E + (which ? e1 : e0)] = s;
+            }
+        }
     }
 }
 
@@ -298,88 +321,91 @@ __device__ void round_x(const Args& p, int t, uint32_t* scratch) {
 // phase 2: selection and the list of experts
 // ---------------------------------------------------------------------------------------
 
-template <int kV>
-__device__ void select_token(const Args& p, int t, float* scratch, int lane, int32_t* ids, float* weights) {
-    float v[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) v[i] = i * 32 + lane < p.E ? 0.0f : -INFINITY;
-    for (int c = 0; c < p.chunks; ++c)
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int e = i * 32 + lane;
-            if (e < p.E) v[i] += __ldcg(p.logits + ((int64_t)c * p.T + t) * p.E + e);
-        }
-#pragma unroll
-    for (int i = 0; i < kV; ++i) v[i] = v[i] == v[i] ? v[i] : -INFINITY;
-    gate_token<kV>(v, p.bias, p.gate, p.E, p.K, scratch, lane, ids, weights);
+__device__ __forceinline__ void select_token(const Args& p, int t, float* scratch, int lane, int32_t* ids, float* weights) {
+#pragma unroll 8
+    for (int e = lane; e < p.E; e += 32) scratch[e] = __ldcg(p.logits + (int64_t)t * p.E + e);
+    gate_token(scratch, p.bias, p.gate, p.E, p.K, lane, ids, weights);
 }
 
-// ids and weights (of the routed slots) -> the experts with rows, in order, and their rows.
-__device__ void list_experts(const Args& p, Tables& tb, const int32_t* ids, const float* weights, bool cg) {
+// ids and weights (of the routed slots) -> the experts with rows, in order, and their rows. distinct: a token's ids are (as
+// selected ones are).
+__device__ void list_experts(const Args& p, Tables& tb, const int32_t* ids, const float* weights, bool distinct) {
     const int Kt = p.K + p.S, Et = p.E + p.S, slots = p.T * Kt;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < Et; e += kThreads) tb.count[e] = 0;
+    __syncthreads();
     for (int s = threadIdx.x; s < slots; s += kThreads) {
-        const int t = s / Kt, k = s % Kt;
-        int e;
+        const int t = s / Kt, k = s - t * Kt;
+        int e = p.E + k - p.K;
         float w = 1.0f;
-        if (k >= p.K) {
-            e = p.E + k - p.K;
-        } else {
-            auto id = [&](int i) { return cg ? __ldcg(ids + t * p.K + i) : ids[t * p.K + i]; };
-            auto wt = [&](int i) { return cg ? __ldcg(weights + t * p.K + i) : weights[t * p.K + i]; };
-            e = id(k);
-            w = wt(k);
+        if (k < p.K) {
+            const int32_t* id = ids + t * p.K;
+            const float* wt = weights + t * p.K;
+            e = id[k];
+            w = wt[k];
             if (e < -1 || e >= p.E) {
                 record_error(p.hdr, MOE_ERR_BAD_ROUTE);
                 e = -1;
             }
-            // an expert named twice by a token: one row with the sum of the weights
-            if (e >= 0) {
-                for (int i = 0; i < k && e >= 0; ++i)
-                    if (id(i) == e) e = -1;
-                if (e >= 0)
-                    for (int i = k + 1; i < p.K; ++i)
-                        if (id(i) == e) w += wt(i);
+            if (!distinct && e >= 0) {  // an expert named twice by a token: one row with the sum of the weights
+                bool first = true;
+                for (int i = 0; i < p.K; ++i)
+                    if (i != k && id[i] == e) {
+                        if (i < k) first = false;
+                        else w += wt[i];
+                    }
+                if (!first) e = -1;
             }
         }
         tb.id[s] = (int16_t)e;
         tb.weight[s] = w;
-    }
-    __syncthreads();
-    // place within the expert in any order: rows are independent of each other
-    for (int s = threadIdx.x; s < slots; s += kThreads) {
-        const int e = tb.id[s];
         if (e >= 0) atomicAdd(&tb.count[e], 1);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int active = 0, rows = 0;
-        for (int b = 0; b < Et; b += 32) {
-            const int e = b + lane;
-            const int n = e < Et ? tb.count[e] : 0;
-            const uint32_t on = __ballot_sync(0xffffffffu, n > 0);
-            int sum = n;
+    // running numbers of the experts with rows and of the rows, 32 experts a warp
+    int n[3], rows[3], active[3], chunks = 0;  // of this warp's chunks (at most 1024 + 31 experts over 12 warps)
+    __shared__ int chunk_rows[33], chunk_active[33];
+    for (int c = warp; c * 32 < Et; c += kAllWarps, ++chunks) {
+        const int e = c * 32 + lane;
+        const int v = e < Et ? tb.count[e] : 0;
+        int sum = v;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += u;
-            }
-            if (n > 0) {
-                const int a = active + __popc(on & ((1u << lane) - 1u));
-                tb.expert[a] = (int16_t)e;
-                tb.start[a] = (int16_t)(rows + sum - n);
-            }
-            if (e < Et) tb.count[e] = rows + sum - n;  // the next free place
-            active += __popc(on);
-            rows += __shfl_sync(0xffffffffu, sum, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
         }
-        if (lane == 0) {
-            tb.n_active = active;
-            tb.start[active] = (int16_t)rows;
+        const uint32_t on = __ballot_sync(0xffffffffu, v > 0);
+        n[chunks] = v;
+        rows[chunks] = sum - v;
+        active[chunks] = __popc(on & ((1u << lane) - 1u));
+        if (lane == 31) {
+            chunk_rows[c] = sum;
+            chunk_active[c] = __popc(on);
         }
     }
     __syncthreads();
+    chunks = 0;
+    for (int c = warp; c * 32 < Et; c += kAllWarps, ++chunks) {
+        int r = 0, a = 0;
+        for (int i = 0; i < c; ++i) {
+            r += chunk_rows[i];
+            a += chunk_active[i];
+        }
+        const int e = c * 32 + lane;
+        r += rows[chunks];
+        a += active[chunks];
+        if (n[chunks] > 0) {
+            tb.expert[a] = (int16_t)e;
+            tb.start[a] = (int16_t)r;
+        }
+        if (e < Et) tb.count[e] = r;  // the next free place
+        if (c * 32 + 32 >= Et && lane == 31) {
+            tb.n_active = a + (n[chunks] > 0);
+            tb.start[tb.n_active] = (int16_t)(r + n[chunks]);
+        }
+    }
+    __syncthreads();
+    // place within the expert in any order: rows are independent of each other
     for (int s = threadIdx.x; s < slots; s += kThreads) {
         const int e = tb.id[s];
         if (e >= 0) tb.row[atomicAdd(&tb.count[e], 1)] = (uint16_t)s;
@@ -429,40 +455,78 @@ struct Ring {
     __device__ uint32_t red_empty(int s) const { return bars + 8u * (2 * Geo<kFmt>::kStages + Geo<kFmt>::kReds + s); }
 };
 
-// One item's stages, by the producer warp.
-template <int kFmt, bool kSecond>
-__device__ __forceinline__ bool produce(const Args& p, const CUtensorMap* map, Ring<kFmt>& ring, int expert, int r0, int lane,
-                                        volatile int* abort_flag) {
+// The producer warp: four lanes take every fourth stage of the CTA's sequence each, so that the latencies of a stage's wait and
+// of its barrier's byte count (some 150 cycles each) are those of four stages.
+constexpr int kProducers = 4;
+
+template <int kFmt>
+__device__ __forceinline__ void produce(const Args& p, const CUtensorMap* map1, const CUtensorMap* map2, const Ring<kFmt>& ring,
+                                        const Tables& tb, const Work<kFmt>& wk, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
-    const int K = kSecond ? p.I : p.H, N = kSecond ? p.H : 2 * p.I;
-    const int steps = (K + G::kStepK - 1) / G::kStepK;
-    for (int st = 0; st < steps; ++st, ++ring.it) {
-        const int s = ring.it % G::kStages;
-        const bool ok = mbar_wait(ring.empty(s), ((uint32_t)(ring.it / G::kStages) & 1u) ^ 1u, p.hdr, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        const uint32_t dst = ring.base + (uint32_t)(s * G::kStageBytes);
-        if constexpr (G::kBf16) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(ring.full(s), 16384);
-                const int y = expert * K + st * 64;
-                tma_load_2d(dst, map, r0, y, ring.full(s));
-                tma_load_2d(dst + 8192, map, kSecond ? r0 + 64 : p.I + r0, y, ring.full(s));
-            }
-        } else {
-            if (lane == 0) {
-                const int row_bytes = G::kFp4 ? K / 2 : K;
-                const int boxes = min(2, (row_bytes - st * 256 + 127) / 128);  // the last one may end inside: zeros
-                mbar_arrive_expect_tx(ring.full(s), 4096u * (uint32_t)boxes);
-                for (int c = 0; c < boxes; ++c) {
-                    const int x = st * 256 + c * 128;
-                    // first product: 16 gate rows, then the up rows of the same outputs (the map's third coordinate)
-                    if constexpr (kSecond) tma_load_2d(dst + c * 4096, map, x, expert * N + r0, ring.full(s));
-                    else tma_load_3d(dst + c * 4096, map, x, expert * N + r0, 0, ring.full(s));
+    static_assert(G::kStages % kProducers == 0, "a slot of the ring is always the same lane's");
+    constexpr uint32_t kLanes = (1u << kProducers) - 1u;
+    const int steps1 = (p.H + G::kStepK - 1) / G::kStepK, steps2 = (p.I + G::kStepK - 1) / G::kStepK;
+    int it = lane, st = lane;             // this lane's stage: of the sequence, and of item i
+    int i = blockIdx.x, phase = 0;        // phase 0: first product, 1: second, 2: past the end
+    int last = -1;                        // the last stage this lane issued
+    for (;; it += kProducers, st += kProducers) {
+        while (phase < 2) {
+            if (phase == 0) {
+                if (i >= wk.n1) {
+                    phase = 1;
+                    i = wk.lo2;
+                    continue;
                 }
+                if (st < steps1) break;
+                st -= steps1;
+                i += gridDim.x;
+            } else {
+                if (i >= wk.hi2) {
+                    phase = 2;
+                    continue;
+                }
+                if (st < steps2) break;
+                st -= steps2;
+                ++i;
             }
         }
+        if (__all_sync(kLanes, phase == 2)) break;
+        if (phase < 2) {
+            const bool second = phase == 1;
+            const int a = second ? i % wk.n_active : i / wk.per1;
+            const int expert = tb.expert[a], r0 = second ? i / wk.n_active * G::kRows : (i - a * wk.per1) * G::kOut1;
+            const int s = it % G::kStages;
+            const uint32_t dst = ring.base + (uint32_t)(s * G::kStageBytes), bar = ring.full(s);
+            const CUtensorMap* map = second ? map2 : map1;
+            if (mbar_wait(ring.empty(s), ((uint32_t)(it / G::kStages) & 1u) ^ 1u, p.hdr, abort_flag)) {
+                if constexpr (G::kBf16) {
+                    mbar_arrive_expect_tx(bar, 16384);
+                    const int y = expert * (second ? p.I : p.H) + st * 64;
+                    tma_load_2d(dst, map, r0, y, bar);
+                    tma_load_2d(dst + 8192, map, second ? r0 + 64 : p.I + r0, y, bar);
+                } else {
+                    const int row_bytes = (second ? p.I : p.H) / (G::kFp4 ? 2 : 1);
+                    const int row = expert * (second ? p.H : 2 * p.I) + r0, x = st * 256;
+                    const bool two = x + 128 < row_bytes;  // a box that ends inside a row is filled up with zeros
+                    mbar_arrive_expect_tx(bar, two ? 8192u : 4096u);
+                    // first product: 16 gate rows, then the up rows of the same outputs (the map's third coordinate)
+                    if (second) tma_load_2d(dst, map, x, row, bar);
+                    else tma_load_3d(dst, map, x, row, 0, bar);
+                    if (two) {
+                        if (second) tma_load_2d(dst + 4096, map, x + 128, row, bar);
+                        else tma_load_3d(dst + 4096, map, x + 128, row, 0, bar);
+                    }
+                }
+                last = it;
+            } else {
+                phase = 2;  // gave up: what is in flight is waited for below
+            }
+        }
+        __syncwarp(kLanes);
     }
-    return true;
+    // drain: every copy this lane issued has landed (bounded)
+    for (int j = last; j >= 0 && j > last - G::kStages; j -= kProducers)
+        if (!mbar_drain(ring.full(j % G::kStages), (uint32_t)(j / G::kStages) & 1u, p.hdr)) break;
 }
 
 // MMA rows g and g + 8 of 16-row tile m are the stage's rows 8 m + perm(g) and 16 + 8 m + perm(g): lanes 4 g .. 4 g + 3 read 64
@@ -922,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---- phase 1
     int barriers = 0;
-    if (p.router) router_phase(p, warp, lane);
+    if (p.router) router_phase(p, reds, warp, lane);
     if constexpr (!G::kBf16)
         for (int t = (int)gridDim.x - 1 - (int)blockIdx.x; t < p.T; t += gridDim.x)
             round_x(p, t, reinterpret_cast<uint32_t*>(reds));
@@ -935,25 +999,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool all = p.T <= kWarps;  // every CTA selects for all tokens
         int32_t* to_ids = all ? reinterpret_cast<int32_t*>(reds) : p.ids;
         float* to_w = all ? reds + kWarps * 32 : p.weights;
-        float* scratch = reinterpret_cast<float*>(smem) + warp * (kMaxE + 32);
+        float* scratch = reinterpret_cast<float*>(smem) + warp * gate_scratch(kMaxE);
         const int t0 = all ? warp : (int)blockIdx.x + warp * (int)gridDim.x;
-        if (warp < kWarps && t0 < p.T) {
-            if (p.E <= 256) select_token<8>(p, t0, scratch, lane, to_ids + t0 * p.K, to_w + t0 * p.K);
-            else select_token<32>(p, t0, scratch, lane, to_ids + t0 * p.K, to_w + t0 * p.K);
-        }
+        if (warp < kWarps && t0 < p.T) select_token(p, t0, scratch, lane, to_ids + t0 * p.K, to_w + t0 * p.K);
         if (all) __syncthreads();
         else grid_barrier(p, ++barriers, abort_flag);
         ids = to_ids;
         weights = to_w;
         if (blockIdx.x == 0)
             for (int i = threadIdx.x; i < p.T * p.K; i += kThreads) {
-                if (p.ids_io) p.ids_io[i] = all ? ids[i] : __ldcg(ids + i);
-                if (p.weights_io) p.weights_io[i] = all ? weights[i] : __ldcg(weights + i);
+                if (p.ids_io) p.ids_io[i] = ids[i];
+                if (p.weights_io) p.weights_io[i] = weights[i];
             }
-        list_experts(p, tb, ids, weights, !all);
-    } else {
-        list_experts(p, tb, ids, weights, true);
     }
+    list_experts(p, tb, ids, weights, p.router != nullptr);
     // the ring's memory was scratch until here: ordered before the copies that fill it
     fence_proxy_async_smem();
     __syncthreads();
@@ -963,14 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (warp == kWarps) {
-            bool ok = true;
-            for (int i = blockIdx.x; i < wk.n1 && ok; i += gridDim.x)
-                ok = produce<kFmt, false>(p, &map1, ring, tb.expert[i / wk.per1], i % wk.per1 * G::kOut1, lane, abort_flag);
-            for (int i = wk.lo2; i < wk.hi2 && ok; ++i)
-                ok = produce<kFmt, true>(p, &map2, ring, tb.expert[i % wk.n_active], i / wk.n_active * G::kRows, lane, abort_flag);
-            // drain: every copy issued has landed (bounded)
-            for (int j = max(0, ring.it - G::kStages); j < ring.it; ++j)
-                if (!mbar_drain(ring.full(j % G::kStages), (uint32_t)(j / G::kStages) & 1u, p.hdr)) break;
+            if (lane < kProducers) produce<kFmt>(p, &map1, &map2, ring, tb, wk, lane, abort_flag);
         } else if (warp <= kWarps + kEpiWarps) {
             const int w = warp - kWarps - 1;
             int set = 0;
@@ -1088,7 +1140,7 @@ LayerLayout layer_layout(const moe_dims& d, int weights) {
     L.dep = take(sizeof(int32_t) * kMaxE);
     L.cols = take(sizeof(int32_t) * ((1 << 16) / 32));
     L.amax = take(sizeof(uint32_t) * kMaxSlots);
-    L.logits = take(sizeof(float) * kMaxChunks * T * d.num_experts);
+    L.logits = take(sizeof(float) * T * d.num_experts);
     L.ids = take(sizeof(int32_t) * T * d.topk);
     L.weights = take(sizeof(float) * T * d.topk);
     L.x16 = take(2 * T * d.hidden);
@@ -1125,8 +1177,6 @@ cudaError_t launch_layer(const moe_layer_args& a, const moe_gate_options& gate, 
     p.E = d.num_experts;
     p.K = d.topk;
     p.S = d.num_shared_experts;
-    // as many parts of H as give every warp of the GPU a dot product
-    p.chunks = std::max(1, std::min({kMaxChunks, sms * kAllWarps / p.E, p.H / 256}));
     p.clamp = a.has_activation_clamp ? a.activation_clamp : INFINITY;
     p.hdr = reinterpret_cast<int32_t*>(b + L.header);
     p.dep = reinterpret_cast<int32_t*>(b + L.dep);
