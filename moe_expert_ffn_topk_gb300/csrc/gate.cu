@@ -9,7 +9,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 4;  // tokens per CTA
+constexpr int kWarps = 4;  // tokens per CTA, while their rows fit 48 KB
 
 template <typename T>
 __device__ __forceinline__ float load_logit(const T* p) {
@@ -23,20 +23,24 @@ __global__ void __launch_bounds__(32 * kWarps)
                 int E, int K, int32_t* __restrict__ ids, float* __restrict__ weights) {
     extern __shared__ float smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kWarps + warp;
+    const int t = blockIdx.x * (blockDim.x >> 5) + warp;
     if (t >= tokens) return;
     const T* row = logits + (int64_t)t * stride;
     float* scratch = smem + warp * gate_scratch(E);
 #pragma unroll 8
     for (int e = lane; e < E; e += 32) scratch[e] = load_logit(row + e);
-    gate_token(scratch, bias, o, E, K, lane, ids + (int64_t)t * K, weights + (int64_t)t * K);
+    if (bias)
+#pragma unroll 8
+        for (int e = lane; e < E; e += 32) scratch[E + e] = __ldg(bias + e);
+    gate_token(scratch, bias != nullptr, o, E, K, lane, ids + (int64_t)t * K, weights + (int64_t)t * K);
 }
 
 template <typename T>
 cudaError_t launch_t(const void* logits, int64_t stride, const float* bias, const moe_gate_options& o, int T_, int E, int K,
                      int32_t* ids, float* weights, cudaStream_t s) {
-    const size_t smem = sizeof(float) * kWarps * gate_scratch(E);
-    gate_kernel<T><<<(T_ + kWarps - 1) / kWarps, 32 * kWarps, smem, s>>>(static_cast<const T*>(logits), stride, bias, o, T_, E, K, ids,
+    const int warps = E <= 512 ? kWarps : kWarps / 2;
+    const size_t smem = sizeof(float) * warps * gate_scratch(E);
+    gate_kernel<T><<<(T_ + warps - 1) / warps, 32 * warps, smem, s>>>(static_cast<const T*>(logits), stride, bias, o, T_, E, K, ids,
                                                                         weights);
     return cudaGetLastError();
 }

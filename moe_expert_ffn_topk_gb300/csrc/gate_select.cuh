@@ -20,19 +20,20 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // divide of the activations are not used here)
 __device__ __forceinline__ float gate_sigmoid(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
 
-// Floats of shared memory that gate_token works in, per warp: logits, then choice keys (a few words apart per group, see there).
-__host__ __device__ inline int gate_scratch(int E) { return 2 * E + 32; }
+// Floats of shared memory that gate_token works in, per warp: logits, bias, choice keys (a few words apart per group, see there).
+__host__ __device__ inline int gate_scratch(int E) { return 3 * E + 32; }
 
-// One token, by one warp. scratch: gate_scratch(E) words of shared memory of this warp, its first E holding the logits (this
-// function separates its reads from their writes). Selected experts go to ids[0..K) and weights[0..K).
+// One token, by one warp. scratch: gate_scratch(E) words of shared memory of this warp, the first E holding the logits, the
+// next E the bias where there is one (this function separates its reads from their writes). Selected experts go to ids[0..K) and weights[0..K).
 //
 // Rows stay in shared memory, not in registers, and every loop is kept rolled: few tokens run this once, and then what counts
 // is how much code has to be fetched (with the row in registers and everything unrolled: twice the time for 7 tokens).
-__device__ __forceinline__ void gate_token(float* scratch, const float* bias, const moe_gate_options& o, int E, int K, int lane,
+__device__ __forceinline__ void gate_token(float* scratch, bool has_bias, const moe_gate_options& o, int E, int K, int lane,
                                            int32_t* ids, float* weights) {
     constexpr uint32_t kAll = 0xffffffffu;
-    const float* logit = scratch;
-    uint32_t* key = reinterpret_cast<uint32_t*>(scratch + E);
+    const float *logit = scratch, *bias = scratch + E;
+    uint32_t* key = reinterpret_cast<uint32_t*>(scratch + 2 * E);
+    uint32_t* bias_key = reinterpret_cast<uint32_t*>(scratch + E);  // the bias is not needed once the keys are there
     const bool softmax = o.score == MOE_SCORE_SOFTMAX;
     const bool groups = o.num_groups > 1;
     // group of expert e: (e + 0.5) / size truncated, exact for e < 1024; `per` lanes scan a group, and keys of a group are `per`
@@ -71,14 +72,12 @@ __device__ __forceinline__ void gate_token(float* scratch, const float* bias, co
 #pragma unroll 2
     for (int e = lane; e < E; e += 32) {
         float c = logit[e];
-        const float b = bias ? __ldg(bias + e) : 0.0f;
         const bool on = c > -INFINITY;  // false for a NaN too
-        if (bias || !softmax) c = score(c);
-        if (bias) c += b;
+        if (has_bias || !softmax) c = score(c);
+        if (has_bias) c += bias[e];
         key[e + group_of(e) * pad] = on && c == c ? order_key(c) : 0u;
     }
 
-    uint32_t kept = ~0u;  // bit g: the experts of group g are eligible
     if (groups) {
         __syncwarp();
         const int g = lane / per, sub = lane & (per - 1);
@@ -99,13 +98,21 @@ __device__ __forceinline__ void gate_token(float* scratch, const float* bias, co
         }
         // of a fully masked group too: -inf is a rank
         uint32_t rank = g < o.num_groups && sub == 0 ? order_key(o.group_top == 1 || size == 1 ? a : a + b) : 0u;
-        kept = 0u;
+        uint32_t kept = 0u;  // bit g: the experts of group g stay eligible
         for (int k = 0; k < o.topk_groups; ++k) {
             const uint32_t best = __reduce_max_sync(kAll, rank);
             const int win = __ffs(__ballot_sync(kAll, rank == best)) - 1;  // the lowest lane: the lowest group
             kept |= 1u << __shfl_sync(kAll, g, win);
             if (lane == win) rank = 0u;
         }
+        // the keys of the groups that stay, packed (a lane's own experts again; every lane is past its scan)
+#pragma unroll 4
+        for (int e = lane; e < E; e += 32) {
+            const int h = group_of(e);
+            const uint32_t k = key[e + h * pad];
+            bias_key[e] = (kept >> h) & 1u ? k : 0u;
+        }
+        key = bias_key;
     }
 
     // K rounds of "largest key, lowest index"; lane k keeps the k-th. Each lane knows the best of its own experts.
@@ -113,10 +120,9 @@ __device__ __forceinline__ void gate_token(float* scratch, const float* bias, co
     int at = 0;
     auto own_best = [&]() {
         mine = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int e = lane; e < E; e += 32) {
-            const int g = group_of(e);
-            const uint32_t k = (kept >> g) & 1u ? key[e + g * pad] : 0u;
+            const uint32_t k = key[e];
             if (k > mine) {
                 mine = k;
                 at = e;
@@ -128,10 +134,13 @@ __device__ __forceinline__ void gate_token(float* scratch, const float* bias, co
     for (int k = 0; k < K; ++k) {
         const uint32_t best = __reduce_max_sync(kAll, mine);
         if (best == 0u) break;
-        const int e = (int)__reduce_min_sync(kAll, mine == best ? (uint32_t)at : 0xffffffffu);
+        // one lane has it, or more (equal values): the lowest index among them
+        const uint32_t with = __ballot_sync(kAll, mine == best);
+        const int e = with & (with - 1u) ? (int)__reduce_min_sync(kAll, mine == best ? (uint32_t)at : 0xffffffffu)
+                                         : __shfl_sync(kAll, at, __ffs(with) - 1);
         if (lane == k) my_id = e;
         if (lane == (e & 31)) {
-            key[e + group_of(e) * pad] = 0u;
+            key[e] = 0u;
             own_best();
         }
         __syncwarp();

@@ -19,8 +19,8 @@
 //      arrival and its latencies have the time of eight stages; the warps' sums of an item meet in shared memory, where two
 //      epilogue warps add them up. SwiGLU of them goes to the workspace in fp32 with the row's largest magnitude. A counter per
 //      expert says when its rows are complete.
-//   4. second product: items of 32 hidden columns (BF16: 128) of one expert, ordered by columns first and dealt in equal
-//      runs, so that a CTA adds up the experts of its columns itself, in order, in shared memory. Columns whose experts are
+//   4. second product: items of 32 hidden columns (BF16: 128) of one expert, ordered by columns first and dealt in runs of
+//      stages, so that a CTA adds up the experts of its columns itself, in order, in shared memory. Columns whose stages are
 //      split between CTAs meet in the workspace: the last CTA to arrive adds the parts in order. No atomics on values:
 //      results do not depend on timing.
 //
@@ -91,7 +91,7 @@ constexpr int kMaxBars = 48;
 
 struct Tables {
     uint64_t bars[kMaxBars];
-    int n_active, last, abort, unused;
+    int n_active, last, abort, mine;
     int count[kMaxE];
     int16_t expert[kMaxE];                // active experts
     int16_t start[kMaxE + 2];             // where their rows begin in row[]
@@ -324,7 +324,10 @@ __device__ void round_x(const Args& p, int t, uint32_t* scratch) {
 __device__ __forceinline__ void select_token(const Args& p, int t, float* scratch, int lane, int32_t* ids, float* weights) {
 #pragma unroll 8
     for (int e = lane; e < p.E; e += 32) scratch[e] = __ldcg(p.logits + (int64_t)t * p.E + e);
-    gate_token(scratch, p.bias, p.gate, p.E, p.K, lane, ids, weights);
+    if (p.bias)
+#pragma unroll 8
+        for (int e = lane; e < p.E; e += 32) scratch[p.E + e] = __ldg(p.bias + e);
+    gate_token(scratch, p.bias != nullptr, p.gate, p.E, p.K, lane, ids, weights);
 }
 
 // ids and weights (of the routed slots) -> the experts with rows, in order, and their rows. distinct: a token's ids are (as
@@ -417,30 +420,46 @@ __device__ void list_experts(const Args& p, Tables& tb, const int32_t* ids, cons
 // phases 3 and 4
 // ---------------------------------------------------------------------------------------
 
-// The items of a CTA in order: those of the first product (dealt in turn), then its run of the second.
+// The work of a CTA in order: its items of the first product (dealt in turn), then its run of the second product's stages. Those
+// are numbered column group by column group, expert by expert, and a run may begin and end inside an item: sums of parts of K
+// meet like sums of different experts do. Runs are cut so that every CTA has the same number of stages in all.
 template <int kFmt>
 struct Work {
-    int per1, n1;       // items of the first product per expert, in all
-    int n_active;
-    int lo2, hi2;       // this CTA's run of the second product: item = column group * n_active + expert
+    int per1, n1;          // items of the first product per expert, in all
+    int n_active, steps2;  // experts with rows; stages of an item of the second product
+    int steps1, grid;
+    int total2;            // all stages of the second product (below 2^30 at the limits of the sizes)
+    int lo2, hi2;          // this CTA's run
     __device__ Work(const Args& p, int active) {
-        per1 = p.I / Geo<kFmt>::kOut1;
+        using G = Geo<kFmt>;
+        per1 = p.I / G::kOut1;
         n_active = active;
         n1 = per1 * active;
-        lo2 = first(p, active, blockIdx.x);
-        hi2 = first(p, active, blockIdx.x + 1);
+        steps1 = (p.H + G::kStepK - 1) / G::kStepK;
+        steps2 = (p.I + G::kStepK - 1) / G::kStepK;
+        grid = (int)gridDim.x;
+        total2 = p.H / G::kRows * active * steps2;
+        lo2 = first(blockIdx.x);
+        hi2 = first(blockIdx.x + 1);
     }
-    static __device__ int first(const Args& p, int active, int cta) {
-        return (int)((int64_t)(p.H / Geo<kFmt>::kRows) * active * cta / (int)gridDim.x);
+    // the first stage of CTA c's run
+    __device__ int first(int c) const {
+        const int each = n1 / grid, more = n1 % grid;  // the first `more` CTAs have one item more
+        const int64_t all = (int64_t)n1 * steps1 + total2;
+        if (all < (int64_t)(each + (more > 0)) * steps1 * grid) return (int)((int64_t)total2 * c / grid);  // cannot be made even
+        return (int)(all * c / grid - (int64_t)steps1 * ((int64_t)each * c + min(c, more)));
     }
-    // the CTA whose run holds item i
-    static __device__ int owner(const Args& p, int active, int i) {
-        const int64_t n = (int64_t)(p.H / Geo<kFmt>::kRows) * active;
-        int c = (int)((int64_t)i * (int)gridDim.x / n);
-        while (first(p, active, c + 1) <= i) ++c;
-        while (first(p, active, c) > i) --c;
-        return c;
+    // the CTA whose run holds stage i
+    __device__ int owner(int i) const {
+        int lo = 0, hi = grid - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first(mid) <= i) lo = mid; else hi = mid - 1;
+        }
+        return lo;
     }
+    // stages of a column group
+    __device__ int group() const { return n_active * steps2; }
 };
 
 template <int kFmt>
@@ -465,28 +484,29 @@ __device__ __forceinline__ void produce(const Args& p, const CUtensorMap* map1, 
     using G = Geo<kFmt>;
     static_assert(G::kStages % kProducers == 0, "a slot of the ring is always the same lane's");
     constexpr uint32_t kLanes = (1u << kProducers) - 1u;
-    const int steps1 = (p.H + G::kStepK - 1) / G::kStepK, steps2 = (p.I + G::kStepK - 1) / G::kStepK;
     int it = lane, st = lane;             // this lane's stage: of the sequence, and of item i
     int i = blockIdx.x, phase = 0;        // phase 0: first product, 1: second, 2: past the end
+    const int end2 = wk.hi2 / wk.steps2, end2_st = wk.hi2 % wk.steps2;
     int last = -1;                        // the last stage this lane issued
     for (;; it += kProducers, st += kProducers) {
         while (phase < 2) {
             if (phase == 0) {
                 if (i >= wk.n1) {
                     phase = 1;
-                    i = wk.lo2;
+                    i = wk.lo2 / wk.steps2;
+                    st += wk.lo2 % wk.steps2;
                     continue;
                 }
-                if (st < steps1) break;
-                st -= steps1;
+                if (st < wk.steps1) break;
+                st -= wk.steps1;
                 i += gridDim.x;
             } else {
-                if (i >= wk.hi2) {
+                if (i > end2 || (i == end2 && st >= end2_st)) {
                     phase = 2;
                     continue;
                 }
-                if (st < steps2) break;
-                st -= steps2;
+                if (st < wk.steps2) break;
+                st -= wk.steps2;
                 ++i;
             }
         }
@@ -697,21 +717,20 @@ __device__ __forceinline__ void multiply_slice(const Args& p, uint32_t stage, in
     }
 }
 
-// One item by a consumer warp: its group's stages (i % kGroups of the CTA's sequence) times the expert's rows, then its sums to
+// Stages [st0, st1) of one item by a consumer warp: its group's (i % kGroups of the CTA's sequence) times the expert's rows, then its sums to
 // the epilogue, one set a column tile. Groups without a stage of the item only sign for their part of the set.
 template <int kFmt, bool kSecond, int NT>
-__device__ __forceinline__ void consume(const Args& p, const Ring<kFmt>& ring, float* reds, const Tables& tb, int a, int r0, int set,
-                                        int warp, int lane, volatile int* abort_flag) {
+__device__ __forceinline__ void consume(const Args& p, const Ring<kFmt>& ring, float* reds, const Tables& tb, int a, int r0, int st0, int st1,
+                                        int set, int warp, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
     using Cols = Columns<kFmt, kSecond>;
     // so many slices' columns of the first tile are on their way at a time, as far as registers go
     constexpr int kSums = G::kMt * 4 * NT;
     constexpr int kAhead = 4 * Cols::kWords + kSums <= 80 ? 4 : 2 * Cols::kWords + kSums <= 80 ? 2 : 1;
     const int K = kSecond ? p.I : p.H;
-    const int steps = (K + G::kStepK - 1) / G::kStepK;
     const int group = warp / G::kGroupWarps;
-    int st = (group - ring.it % G::kGroups + G::kGroups) % G::kGroups;  // this group's first stage of the item
-    const bool part = st < steps;
+    int st = st0 + (group - ring.it % G::kGroups + G::kGroups) % G::kGroups;  // this group's first stage of the item
+    const bool part = st < st1;
     const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, tiles = (n_rows + 7) / 8;
     float acc[G::kMt][NT][4], ainv[NT];
     if (part) {
@@ -739,8 +758,8 @@ __device__ __forceinline__ void consume(const Args& p, const Ring<kFmt>& ring, f
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-        for (; st < steps; st += G::kGroups) {
-            const int it = ring.it + st, s = it % G::kStages, k = st * G::kStepK;
+        for (; st < st1; st += G::kGroups) {
+            const int it = ring.it + st - st0, s = it % G::kStages, k = st * G::kStepK;
             const int slices = min(G::kSlices, (K - k) / G::kSliceK);
             Cols cols[kAhead];
             Scales<kFmt, kSecond> sc[G::kSlices];
@@ -791,10 +810,24 @@ __device__ __forceinline__ void consume(const Args& p, const Ring<kFmt>& ring, f
 
 template <int kFmt, bool kSecond, int NT>
 __device__ __forceinline__ void consume_item(const Args& p, Ring<kFmt>& ring, int& set, float* reds, const Tables& tb, int a, int r0,
-                                             int warp, int lane, volatile int* abort_flag) {
-    consume<kFmt, kSecond, NT>(p, ring, reds, tb, a, r0, set, warp, lane, abort_flag);
+                                             int st0, int st1, int warp, int lane, volatile int* abort_flag) {
+    consume<kFmt, kSecond, NT>(p, ring, reds, tb, a, r0, st0, st1, set, warp, lane, abort_flag);
     set += (tb.start[a + 1] - tb.start[a] + 7) / 8;
-    ring.it += ((kSecond ? p.I : p.H) + Geo<kFmt>::kStepK - 1) / Geo<kFmt>::kStepK;
+    ring.it += st1 - st0;
+}
+
+// Waits for the rows of active experts, those of the next items looked at together: `known` items from the run's start on have
+// theirs (both epilogue warps of every item of the first product count).
+__device__ __forceinline__ void wait_rows(const Args& p, int i, int first_item, int n_active, int target, int& known, int lane,
+                                          volatile int* abort_flag) {
+    const int n = i - first_item;
+    if (n < known || n >= n_active) return;  // after n_active items every expert has been looked at
+    const bool on = n + lane < n_active;
+    const uint32_t there = __ballot_sync(0xffffffffu, !on || ld_acquire_gpu(p.dep + (i + lane) % n_active) >= target);
+    const int ready = there == 0xffffffffu ? 32 : __ffs(~there) - 1;
+    known = n + max(ready, 1);
+    if (ready == 0 && lane == 0) wait_count(p.dep + i % n_active, target, p.hdr, abort_flag);
+    __syncwarp();  // the lanes' acquires order what the warp reads from here on
 }
 
 // The sum of the groups' parts of one value of a set; the item's stages begin at `it` and are `steps` many.
@@ -861,10 +894,10 @@ __device__ __forceinline__ void finish_first(const Args& p, Ring<kFmt>& ring, in
 // Epilogue warp w of an item of the second product: half of its hidden columns, added to the CTA's sums of these columns.
 template <int kFmt>
 __device__ __forceinline__ void finish_second(const Args& p, Ring<kFmt>& ring, int& set, const float* reds, const Tables& tb, float* y,
-                                              int a, int w, int lane, volatile int* abort_flag) {
+                                              int a, int steps, int w, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
     const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, Kt = p.K + p.S;
-    const int steps = (p.I + G::kStepK - 1) / G::kStepK, tiles = (n_rows + 7) / 8;
+    const int tiles = (n_rows + 7) / 8;
     for (int n = 0; n < tiles; ++n, ++set) {
         const int q = set % G::kReds;
         const float* red = reds + q * G::kRed;
@@ -902,9 +935,9 @@ template <int kFmt>
 __device__ void finish_columns(const Args& p, Tables& tb, float* y, const Work<kFmt>& wk, int g, int tid) {
     using G = Geo<kFmt>;
     constexpr int R = G::kRows;
-    const int first = g * wk.n_active, last = first + wk.n_active - 1, n = p.T * R;
+    const int first = g * wk.group(), end = first + wk.group(), n = p.T * R;
     epilogue_sync();  // both warps' sums are in place
-    if (wk.lo2 <= first && wk.hi2 > last) {
+    if (wk.lo2 <= first && wk.hi2 >= end) {
         for (int i = tid; i < n; i += 32 * kEpiWarps) {
             p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(y[i]);
             y[i] = 0.0f;
@@ -915,21 +948,19 @@ __device__ void finish_columns(const Args& p, Tables& tb, float* y, const Work<k
     // the CTAs with experts of these columns, in order (with fewer items than CTAs, some in between have none)
     if (tid == 0) {
         int parts = 0;
-        for (int i = first; i <= last; ++parts) {
-            const int c = Work<kFmt>::owner(p, wk.n_active, i);
-            tb.count[parts] = c;
-            i = Work<kFmt>::first(p, wk.n_active, c + 1);
+        for (int i = first; i < end; ++parts) {
+            const int c = wk.owner(i);
+            // a CTA's first column group goes to its first buffer, its last to the second
+            tb.count[parts] = 2 * c + (wk.first(c) / wk.group() == g ? 0 : 1);
+            if (c == (int)blockIdx.x) tb.mine = tb.count[parts];
+            i = wk.first(c + 1);
         }
         tb.last = parts;
     }
     epilogue_sync();
     const int parts = tb.last;
-    // a CTA's first column group goes to its first buffer, its last to the second
-    auto buffer = [&](int cta) {
-        const int at = Work<kFmt>::first(p, wk.n_active, cta);
-        return p.part + ((int64_t)cta * 2 + (at / wk.n_active == g ? 0 : 1)) * kMaxT * R;
-    };
-    float* mine = buffer(blockIdx.x);
+    auto buffer = [&](int b) { return p.part + (int64_t)b * kMaxT * R; };
+    float* mine = buffer(tb.mine);
     for (int i = tid; i < n; i += 32 * kEpiWarps) {
         mine[i] = y[i];
         y[i] = 0.0f;
@@ -1028,23 +1059,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             int set = 0;
             for (int i = blockIdx.x; i < wk.n1; i += gridDim.x)
                 finish_first<kFmt>(p, ring, set, reds, tb, i / wk.per1, i % wk.per1 * G::kOut1, w, lane, abort_flag);
-            for (int i = wk.lo2; i < wk.hi2; ++i) {
-                finish_second<kFmt>(p, ring, set, reds, tb, y, i % wk.n_active, w, lane, abort_flag);
-                if (i + 1 == wk.hi2 || (i + 1) % wk.n_active == 0) finish_columns<kFmt>(p, tb, y, wk, i / wk.n_active, w * 32 + lane);
+            for (int at = wk.lo2; at < wk.hi2;) {
+                const int i = at / wk.steps2, to = min(wk.hi2, (i + 1) * wk.steps2);
+                finish_second<kFmt>(p, ring, set, reds, tb, y, i % wk.n_active, to - at, w, lane, abort_flag);
+                at = to;
+                if (at == wk.hi2 || at % wk.group() == 0) finish_columns<kFmt>(p, tb, y, wk, i / wk.n_active, w * 32 + lane);
             }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         int set = 0;
         for (int i = blockIdx.x; i < wk.n1; i += gridDim.x)
-            consume_item<kFmt, false, NT>(p, ring, set, reds, tb, i / wk.per1, i % wk.per1 * G::kOut1, warp, lane, abort_flag);
-        for (int i = wk.lo2; i < wk.hi2; ++i) {
-            const int a = i % wk.n_active;
-            if (i - wk.lo2 < wk.n_active) {  // the run's first item of this expert: wait for its rows (both epilogue warps count)
-                if (lane == 0) wait_count(p.dep + a, kEpiWarps * wk.per1, p.hdr, abort_flag);
-                __syncwarp();
-            }
-            consume_item<kFmt, true, NT>(p, ring, set, reds, tb, a, i / wk.n_active * G::kRows, warp, lane, abort_flag);
+            consume_item<kFmt, false, NT>(p, ring, set, reds, tb, i / wk.per1, i % wk.per1 * G::kOut1, 0, wk.steps1, warp, lane, abort_flag);
+        const int first_item = wk.lo2 / wk.steps2;
+        int known = 0;
+        for (int at = wk.lo2; at < wk.hi2;) {
+            const int i = at / wk.steps2, a = i % wk.n_active;
+            const int begin = i * wk.steps2, to = min(wk.hi2, begin + wk.steps2);
+            wait_rows(p, i, first_item, wk.n_active, kEpiWarps * wk.per1, known, lane, abort_flag);
+            consume_item<kFmt, true, NT>(p, ring, set, reds, tb, a, i / wk.n_active * G::kRows, at - begin, to - begin,
+                                         warp, lane, abort_flag);
+            at = to;
         }
     }
     if (wk.n_active == 0)
