@@ -326,42 +326,62 @@ def moe_plan_noalloc(topk_ids, d: MoeDims, counts, offsets, row_src, stream=None
 # ---------------------------------------------------------------------------------------
 
 
-def _float_type(t, what):
-    if t.dtype == torch.bfloat16:
-        return MOE_TYPE_BF16
-    if t.dtype == torch.float32:
-        return MOE_TYPE_F32
-    raise TypeError(f"{what} must be bfloat16 or float32")
+_FLOAT_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
+_FP8_CODES = (torch.float8_e4m3fn, torch.uint8)
+# the current stream's handle without a Stream object around it (a third of a small call's host time otherwise)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _typed(t, what, *dtypes):
-    if t is not None and t.dtype not in dtypes:
-        raise TypeError(f"{what} must be " + " or ".join(str(d).replace("torch.", "") for d in dtypes))
-    return _ptr(t, what)
+def _handle(stream, t):
+    """Handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or t.device.type != "cuda":
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(t.get_device())
 
 
-def _shaped(t, what, *shape):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
-
-
-def _rows(t, what, rows=None, cols=None):
-    """Address and row stride of a matrix whose rows are contiguous (a column slice of a wider one is)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a torch.Tensor")
+def _vec(t, what, dtype, shape):
+    """Address of a contiguous device tensor of that type and shape."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be in device memory")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not ({rows}, {cols})")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _float_type(t, what):
+    try:
+        return _FLOAT_TYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what} must be bfloat16 or float32") from None
+
+
+def _rows(t, what, shape):
+    """Row stride of a device matrix of that shape whose rows are contiguous (a column slice of a wider one is)."""
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be in device memory")
+    stride, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {what} must be contiguous")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    return (t.data_ptr() if t.numel() else None), stride
+    return stride if shape[0] > 1 else shape[1]
+
+
+def _space(workspace):
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous device memory")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def moe_ops_workspace_init(workspace, stream=None):
-    ws, nb = _ws(workspace)
-    _check(LIB.moe_ops_workspace_init(ws, nb, _stream(stream)), "moe_ops_workspace_init")
+    ws, nb = _space(workspace)
+    _check(LIB.moe_ops_workspace_init(ws, nb, _handle(stream, workspace)), "moe_ops_workspace_init")
 
 
 def gate_options(score="softmax", groups=1, topk_groups=1, group_top=1, normalize=True, route_scale=1.0) -> MoeGateOptions:
@@ -373,26 +393,24 @@ def gate_options(score="softmax", groups=1, topk_groups=1, group_top=1, normaliz
 def moe_gate(logits, d: MoeDims, topk_ids, topk_weights, bias=None, options=None, stream=None):
     """topk_ids (int32 [T,K]) and topk_weights (fp32 [T,K]) from logits (bf16 or fp32 [T,E], rows may be strided)."""
     T, E, K = d.num_tokens, d.num_experts, d.topk
-    ptr, stride = _rows(logits, "logits", T, E)
-    for t, what in ((topk_ids, "topk_ids"), (topk_weights, "topk_weights")):
-        _shaped(t, what, T, K)
-    _shaped(bias, "bias", E)
-    _check(LIB.moe_gate(ptr, _float_type(logits, "logits"), stride, _typed(bias, "bias", torch.float32),
-                        None if options is None else ctypes.byref(options), ctypes.byref(d),
-                        _typed(topk_ids, "topk_ids", torch.int32), _typed(topk_weights, "topk_weights", torch.float32),
-                        _stream(stream)), "moe_gate")
+    status = LIB.moe_gate(logits.data_ptr(), _float_type(logits, "logits"), _rows(logits, "logits", (T, E)),
+                          None if bias is None else _vec(bias, "bias", torch.float32, (E,)), options, d,
+                          _vec(topk_ids, "topk_ids", torch.int32, (T, K)),
+                          _vec(topk_weights, "topk_weights", torch.float32, (T, K)), _handle(stream, logits))
+    if status:
+        raise MoeError(status, "moe_gate")
 
 
 def moe_fp8_quantize(x, q, scale, pow2=False, stream=None):
     """Rows of x (bf16 or fp32 [M,K]) into q (e4m3 [M,K]) and scale (fp32 [M, ceil(K/128)]); rows of x and q may be strided."""
-    M, K = x.shape
-    xp, xs = _rows(x, "x")
-    if q.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    M, K = shape = x.shape
+    if q.dtype not in _FP8_CODES:
         raise TypeError("q must be float8_e4m3fn or uint8")
-    qp, qs = _rows(q, "q", M, K)
-    _shaped(scale, "scale", M, -(-K // 128))
-    _check(LIB.moe_fp8_quantize(xp, _float_type(x, "x"), M, K, xs, qp, qs, _typed(scale, "scale", torch.float32),
-                                MOE_QUANT_POW2 if pow2 else 0, _stream(stream)), "moe_fp8_quantize")
+    status = LIB.moe_fp8_quantize(x.data_ptr(), _float_type(x, "x"), M, K, _rows(x, "x", shape), q.data_ptr(), _rows(q, "q", shape),
+                                  _vec(scale, "scale", torch.float32, (M, (K + 127) // 128)), MOE_QUANT_POW2 if pow2 else 0,
+                                  _handle(stream, x))
+    if status:
+        raise MoeError(status, "moe_fp8_quantize")
 
 
 def moe_fp8_matmul_workspace_bytes(M: int, N: int, K: int, groups: int = 1) -> int:
@@ -403,28 +421,34 @@ def moe_fp8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream=
     """out[m,n] = sum over blocks of a_scale * b_scale * (a . b^T): a e4m3 [M,K], a_scale fp32 [M, ceil(K/128)], b e4m3
     [groups,N,K] (or [N,K]), b_scale fp32 [groups, ceil(N/128), ceil(K/128)], out bf16 or fp32 [M,N]. With `offsets`
     (int32 [groups+1]) rows [offsets[g], offsets[g+1]) are multiplied by b[g]. Rows of a, b and out may be strided."""
-    codes = (torch.float8_e4m3fn, torch.uint8)
-    if a.dtype not in codes or b.dtype not in codes:
+    if a.dtype not in _FP8_CODES or b.dtype not in _FP8_CODES:
         raise TypeError("a and b must be float8_e4m3fn (or uint8 codes)")
-    if b.dim() == 2:
-        b = b.unsqueeze(0)
-    if b_scale.dim() == 2:
-        b_scale = b_scale.unsqueeze(0)
-    (M, K), (G, N) = a.shape, b.shape[:2]
-    nb, kb = -(-N // 128), -(-K // 128)
-    if G > 1 and b.stride(0) != N * b.stride(1):
-        raise ValueError("the groups of b must follow each other")
-    ap, a_stride = _rows(a, "a")
-    bp, b_stride = _rows(b.flatten(0, 1), "b", G * N, K)
-    op, out_stride = _rows(out, "out", M, N)
-    _shaped(a_scale, "a_scale", M, kb)
-    _shaped(b_scale, "b_scale", G, nb, kb)
-    _shaped(offsets, "offsets", G + 1)
-    args = MoeFp8MatmulArgs(ap, _typed(a_scale, "a_scale", torch.float32), bp, _typed(b_scale, "b_scale", torch.float32),
-                            _typed(offsets, "offsets", torch.int32), op, M, N, K, a_stride, b_stride, out_stride, G,
-                            _float_type(out, "out"))
-    ws, nbytes = _ws(workspace)
-    _check(LIB.moe_fp8_matmul(ctypes.byref(args), ws, nbytes, _stream(stream)), "moe_fp8_matmul")
+    shape = a.shape
+    M, K = shape
+    kb = (K + 127) // 128
+    if b.dim() == 3:
+        G, N, k2 = b.shape
+        between, b_stride, one = b.stride()
+        if G > 1 and between != N * b_stride:
+            raise ValueError("the groups of b must follow each other")
+        b_scale_shape = (G, (N + 127) // 128, kb)
+        if b_scale.dim() == 2 and G == 1:
+            b_scale_shape = b_scale_shape[1:]
+    else:
+        G, (N, k2), (b_stride, one) = 1, b.shape, b.stride()
+        b_scale_shape = ((N + 127) // 128, kb) if b_scale.dim() == 2 else (1, (N + 127) // 128, kb)
+    if k2 != K or not b.is_cuda or one != 1:
+        raise ValueError(f"b must be device memory of {K} contiguous columns")
+    if G * N == 1:
+        b_stride = K
+    ws, nbytes = _space(workspace)
+    args = MoeFp8MatmulArgs(a.data_ptr(), _vec(a_scale, "a_scale", torch.float32, (M, kb)), b.data_ptr(),
+                            _vec(b_scale, "b_scale", torch.float32, b_scale_shape),
+                            None if offsets is None else _vec(offsets, "offsets", torch.int32, (G + 1,)), out.data_ptr(), M, N, K,
+                            _rows(a, "a", shape), b_stride, _rows(out, "out", (M, N)), G, _float_type(out, "out"))
+    status = LIB.moe_fp8_matmul(args, ws, nbytes, _handle(stream, a))
+    if status:
+        raise MoeError(status, "moe_fp8_matmul")
 
 
 def moe_layer_workspace_bytes(d: MoeDims, weights) -> int:
@@ -437,17 +461,25 @@ def moe_layer(x, router, w1, w1_scale, w2, w2_scale, y, d: MoeDims, weights, wor
     weights: "bf16", "fp8_block" or "fp4_mx". Without a router, topk_ids and topk_weights are inputs; with one they are
     optional outputs."""
     T, H, E, K = d.num_tokens, d.hidden, d.num_experts, d.topk
-    _shaped(x, "x", T, H)
-    _shaped(y, "y", T, H)
-    _shaped(router, "router", E, H)
-    _shaped(bias, "bias", E)
-    _shaped(topk_ids, "topk_ids", T, K)
-    _shaped(topk_weights, "topk_weights", T, K)
-    args = MoeLayerArgs(_typed(x, "x", torch.bfloat16), _ptr(router, "router"), _operand(w1, w1_scale, "w1"),
-                        _operand(w2, w2_scale, "w2"), None if options is None else ctypes.pointer(options),
-                        _typed(bias, "bias", torch.float32), _typed(topk_ids, "topk_ids", torch.int32),
-                        _typed(topk_weights, "topk_weights", torch.float32), _typed(y, "y", torch.bfloat16),
-                        MOE_TYPE_BF16 if router is None else _float_type(router, "router"), LAYER_WEIGHTS[weights],
-                        0 if activation_clamp is None else 1, 0.0 if activation_clamp is None else float(activation_clamp))
-    ws, nb = _ws(workspace)
-    _check(LIB.moe_layer(ctypes.byref(args), ctypes.byref(d), ws, nb, _stream(stream)), "moe_layer")
+    args = MoeLayerArgs()
+    args.x = _vec(x, "x", torch.bfloat16, (T, H))
+    args.y = _vec(y, "y", torch.bfloat16, (T, H))
+    args.w1, args.w2 = _operand(w1, w1_scale, "w1"), _operand(w2, w2_scale, "w2")
+    args.weights = LAYER_WEIGHTS[weights]
+    if router is not None:
+        args.router_type = _float_type(router, "router")
+        args.router = _vec(router, "router", router.dtype, (E, H))
+    if options is not None:
+        args.gate = ctypes.pointer(options)
+    if bias is not None:
+        args.gate_bias = _vec(bias, "bias", torch.float32, (E,))
+    if topk_ids is not None:
+        args.topk_ids = _vec(topk_ids, "topk_ids", torch.int32, (T, K))
+    if topk_weights is not None:
+        args.topk_weights = _vec(topk_weights, "topk_weights", torch.float32, (T, K))
+    if activation_clamp is not None:
+        args.has_activation_clamp, args.activation_clamp = 1, float(activation_clamp)
+    ws, nb = _space(workspace)
+    status = LIB.moe_layer(args, d, ws, nb, _handle(stream, x))
+    if status:
+        raise MoeError(status, "moe_layer")
