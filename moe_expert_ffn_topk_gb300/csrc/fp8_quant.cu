@@ -1,7 +1,10 @@
 // Rows of x in e4m3 with an fp32 scale for each 128 columns (moe_fp8_quantize in moe_ops.h).
 //
 // One pass: 8 lanes hold a block of 128 columns, 16 values each, so the block's amax is three shuffles and x is read
-// once. Bound by HBM: 2 (bf16) or 4 (fp32) bytes read and 1 written an element.
+// once. Bound by HBM: 2 (bf16) or 4 (fp32) bytes read and 1 written an element. That takes the division out of the way: by a
+// power of two it is an exact product, and by other scales it is Markstein's: with r = 1/s rounded to nearest, q = x r and
+// q + r (x - q s) with fused multiply-adds is x / s rounded to nearest, wherever nothing over- or underflows (scales outside
+// 2^-60 .. 2^60 take the division itself).
 #include "common.cuh"
 #include "ops.h"
 
@@ -19,29 +22,37 @@ __device__ __forceinline__ float to_f32(T v) {
     else return v;
 }
 
-// kVec: rows of x are 16-byte aligned and of q too, so every full lane loads and stores 16 bytes at a time
-template <typename T, bool kPow2, bool kVec>
+// two e4m3 codes, the first in the low byte
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t pair;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(hi), "f"(lo));
+    return pair;
+}
+
+// kVec: rows of x are 16-byte aligned and of q too, so every full lane loads and stores 16 bytes at a time. Index: of a unit of
+// four blocks (a warp's), 32 bits wide where they suffice.
+template <typename T, bool kPow2, bool kVec, typename Index>
 __global__ void __launch_bounds__(kThreads)
-    quantize_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t x_stride, uint8_t* __restrict__ q,
-                    int64_t q_stride, float* __restrict__ scale, int64_t blocks) {
-    const int64_t total = rows * blocks;
+    quantize_kernel(const T* __restrict__ x, int64_t cols, int64_t x_stride, uint8_t* __restrict__ q, int64_t q_stride,
+                    float* __restrict__ scale, Index blocks, Index units_per_row, Index units) {
     const int sub = threadIdx.x % kLanes;
-    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;; i += (int64_t)gridDim.x * kThreads / kLanes) {
-        const bool on = i < total;
-        if (!__any_sync(0xffffffffu, on)) break;  // whole warps leave together
-        const int64_t r = on ? i / blocks : 0, b = on ? i % blocks : 0;
-        const int64_t c0 = b * 128 + sub * kPer;
-        const int n = on ? (int)max((int64_t)0, min((int64_t)kPer, cols - c0)) : 0;
-        const T* src = x + r * x_stride + c0;
+    const Index first = (Index)blockIdx.x * (kThreads / 32) + threadIdx.x / 32, step = (Index)gridDim.x * (kThreads / 32);
+    for (Index u = first; u < units; u += step) {
+        const Index r = u / units_per_row, b = (u - r * units_per_row) * 4 + (threadIdx.x & 31) / kLanes;
+        const int64_t c0 = (int64_t)b * 128 + sub * kPer;
+        const int n = (int)max((int64_t)0, min((int64_t)kPer, cols - c0));
+        const T* src = x + (int64_t)r * x_stride + c0;
         float v[kPer];
         if (kVec && n == kPer) {
             constexpr int kW = 16 / sizeof(T);
+            uint4 w[kPer / kW];
+#pragma unroll
+            for (int j = 0; j < kPer / kW; ++j) w[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
 #pragma unroll
             for (int j = 0; j < kPer / kW; ++j) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + j);
-                const T* p = reinterpret_cast<const T*>(&w);
+                const T* e = reinterpret_cast<const T*>(&w[j]);
 #pragma unroll
-                for (int k = 0; k < kW; ++k) v[j * kW + k] = to_f32(p[k]);
+                for (int k = 0; k < kW; ++k) v[j * kW + k] = to_f32(e[k]);
             }
         } else {
 #pragma unroll
@@ -57,17 +68,23 @@ __global__ void __launch_bounds__(kThreads)
         // the next power of two: any fraction bit carries into the exponent (not of an infinity or NaN)
         if (kPow2 && top < 0x7f800000u) s = __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u);
         if (s == 0.0f) s = 1.0f;
-        if (!on) continue;
-        if (sub == 0) scale[r * blocks + b] = s;
-        uint8_t* dst = q + r * q_stride + c0;
+        if (n == 0) continue;
+        if (sub == 0) scale[(int64_t)r * blocks + b] = s;
+        const bool plain = s > 8.6736174e-19f && s < 1.1529215e18f;  // 2^-60, 2^60
+        const float inv = __fdiv_rn(1.0f, s);
         uint32_t word[kPer / 4];
 #pragma unroll
         for (int j = 0; j < kPer; j += 4) {
-            uint32_t w = 0;
+            float d[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w |= (uint32_t)float_to_e4m3_satfinite(__fdiv_rn(v[j + k], s)) << (8 * k);
-            word[j / 4] = w;
+            for (int k = 0; k < 4; ++k) {
+                const float y = __fmul_rn(v[j + k], inv);
+                d[k] = kPow2 ? y : __fmaf_rn(__fmaf_rn(-y, s, v[j + k]), inv, y);
+                if (!plain) d[k] = __fdiv_rn(v[j + k], s);
+            }
+            word[j / 4] = e4m3x2(d[0], d[1]) | (e4m3x2(d[2], d[3]) << 16);
         }
+        uint8_t* dst = q + (int64_t)r * q_stride + c0;
         if (kVec && n == kPer) {
             *reinterpret_cast<uint4*>(dst) = make_uint4(word[0], word[1], word[2], word[3]);
         } else {
@@ -81,14 +98,22 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, bool kPow2>
 cudaError_t launch(const void* x, int64_t rows, int64_t cols, int64_t x_stride, uint8_t* q, int64_t q_stride, float* scale,
                    cudaStream_t s) {
-    const int64_t blocks = (cols + 127) / 128;
-    const int64_t ctas = (rows * blocks * kLanes + kThreads - 1) / kThreads;
+    const int64_t blocks = (cols + 127) / 128, per_row = (blocks + 3) / 4, units = rows * per_row;
+    const int64_t ctas = (units + kThreads / 32 - 1) / (kThreads / 32);
     const int grid = (int)(ctas < (1 << 20) ? ctas : (1 << 20));
     const bool vec = !((reinterpret_cast<uintptr_t>(x) | (uint64_t)(x_stride * (int64_t)sizeof(T)) |
                         reinterpret_cast<uintptr_t>(q) | (uint64_t)q_stride) & 15);
     const T* xt = static_cast<const T*>(x);
-    if (vec) quantize_kernel<T, kPow2, true><<<grid, kThreads, 0, s>>>(xt, rows, cols, x_stride, q, q_stride, scale, blocks);
-    else quantize_kernel<T, kPow2, false><<<grid, kThreads, 0, s>>>(xt, rows, cols, x_stride, q, q_stride, scale, blocks);
+    // 32-bit unit numbers, the step past the last one included; sizes beyond them are odd enough for the slower rows
+    if (units < (int64_t(1) << 31) && vec)
+        quantize_kernel<T, kPow2, true, uint32_t><<<grid, kThreads, 0, s>>>(xt, cols, x_stride, q, q_stride, scale, (uint32_t)blocks,
+                                                                            (uint32_t)per_row, (uint32_t)units);
+    else if (vec)
+        quantize_kernel<T, kPow2, true, uint64_t><<<grid, kThreads, 0, s>>>(xt, cols, x_stride, q, q_stride, scale, (uint64_t)blocks,
+                                                                            (uint64_t)per_row, (uint64_t)units);
+    else
+        quantize_kernel<T, kPow2, false, uint64_t><<<grid, kThreads, 0, s>>>(xt, cols, x_stride, q, q_stride, scale, (uint64_t)blocks,
+                                                                             (uint64_t)per_row, (uint64_t)units);
     return cudaGetLastError();
 }
 

@@ -81,7 +81,7 @@ struct Geo {
     static constexpr int kRedCol = kRows + 4;       // floats of a column of partial sums (two columns apart: 8 banks)
     static constexpr int kRedGroup = 8 * kRedCol;
     static constexpr int kRed = kGroups * kRedGroup + 8;  // and the inverse scale of each column's activations
-    static constexpr int kReds = kBf16 ? 2 : 3;     // sets of partial sums on their way to the epilogue
+    static constexpr int kReds = kBf16 ? 2 : 4;     // sets of partial sums on their way to the epilogue
     // shared memory: ring | sets of partial sums | tables | y sums
     static constexpr int kRedOff = kStages * kStageBytes;
     static constexpr int kTabOff = kRedOff + kReds * 4 * kRed;
@@ -96,6 +96,8 @@ struct Tables {
     int16_t expert[kMaxE];                // active experts
     int16_t start[kMaxE + 2];             // where their rows begin in row[]
     uint16_t row[kMaxSlots];              // slot = token * (K + S) + k
+    uint8_t token[kMaxSlots];             // by slot
+    int first[kMaxSms + 1];               // where the CTAs' runs of the second product begin
     float weight[kMaxSlots];              // by slot
     int16_t id[kMaxSlots];                // by slot, -1: none
 };
@@ -149,10 +151,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
-// two e4m3 codes -> two f16 (exact)
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+// the two e4m3 codes of half i of a word -> two f16 (exact)
+template <int i>
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t word) {
     uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+    asm("{\n\t.reg .b16 h0, h1;\n\tmov.b32 {h0, h1}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h%2;\n\t}" : "=r"(r) : "r"(word), "n"(i));
     return r;
 }
 // the two e2m1 codes of byte i -> two f16 (exact), low nibble first
@@ -361,6 +364,7 @@ __device__ void list_experts(const Args& p, Tables& tb, const int32_t* ids, cons
             }
         }
         tb.id[s] = (int16_t)e;
+        tb.token[s] = (uint8_t)t;
         tb.weight[s] = w;
         if (e >= 0) atomicAdd(&tb.count[e], 1);
     }
@@ -449,17 +453,50 @@ struct Work {
         if (all < (int64_t)(each + (more > 0)) * steps1 * grid) return (int)((int64_t)total2 * c / grid);  // cannot be made even
         return (int)(all * c / grid - (int64_t)steps1 * ((int64_t)each * c + min(c, more)));
     }
-    // the CTA whose run holds stage i
-    __device__ int owner(int i) const {
-        int lo = 0, hi = grid - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (first(mid) <= i) lo = mid; else hi = mid - 1;
-        }
-        return lo;
-    }
     // stages of a column group
     __device__ int group() const { return n_active * steps2; }
+};
+
+// The items of a CTA's phase in order, stepped without divisions.
+template <int kFmt, bool kSecond>
+struct Items {
+    int a, group;  // active expert, group of rows (kOut1 outputs or kRows hidden columns) in it
+    int n = 0;     // items before this one
+    int st0, left; // first stage; second product: stages of the run from this item on
+    __device__ __forceinline__ explicit Items(const Work<kFmt>& wk) {
+        if constexpr (kSecond) {
+            const int per = wk.group();
+            group = per > 0 ? wk.lo2 / per : 0;
+            const int in = wk.lo2 - group * per;
+            a = in / wk.steps2;
+            st0 = in - a * wk.steps2;
+            left = wk.hi2 - wk.lo2;
+        } else {
+            a = (int)blockIdx.x / wk.per1;
+            group = (int)blockIdx.x - a * wk.per1;
+            st0 = left = 0;
+        }
+    }
+    __device__ __forceinline__ bool valid(const Work<kFmt>& wk) const { return kSecond ? left > 0 : a < wk.n_active; }
+    __device__ __forceinline__ int st1(const Work<kFmt>& wk) const { return kSecond ? min(wk.steps2, st0 + left) : wk.steps1; }
+    __device__ __forceinline__ int r0() const { return group * (kSecond ? Geo<kFmt>::kRows : Geo<kFmt>::kOut1); }
+    __device__ __forceinline__ void next(const Work<kFmt>& wk) {
+        ++n;
+        if constexpr (kSecond) {
+            left -= st1(wk) - st0;
+            st0 = 0;
+            if (++a == wk.n_active) {
+                a = 0;
+                ++group;
+            }
+        } else {
+            group += wk.grid;
+            while (group >= wk.per1) {
+                group -= wk.per1;
+                ++a;
+            }
+        }
+    }
 };
 
 template <int kFmt>
@@ -484,49 +521,48 @@ __device__ __forceinline__ void produce(const Args& p, const CUtensorMap* map1, 
     using G = Geo<kFmt>;
     static_assert(G::kStages % kProducers == 0, "a slot of the ring is always the same lane's");
     constexpr uint32_t kLanes = (1u << kProducers) - 1u;
-    int it = lane, st = lane;             // this lane's stage: of the sequence, and of item i
-    int i = blockIdx.x, phase = 0;        // phase 0: first product, 1: second, 2: past the end
-    const int end2 = wk.hi2 / wk.steps2, end2_st = wk.hi2 % wk.steps2;
+    int it = lane, st = lane;             // this lane's stage: of the sequence, and of the item past its first stage
+    int phase = 0;                        // 0: first product, 1: second, 2: past the end
     int last = -1;                        // the last stage this lane issued
+    Items<kFmt, false> i1(wk);
+    Items<kFmt, true> i2(wk);
     for (;; it += kProducers, st += kProducers) {
-        while (phase < 2) {
-            if (phase == 0) {
-                if (i >= wk.n1) {
-                    phase = 1;
-                    i = wk.lo2 / wk.steps2;
-                    st += wk.lo2 % wk.steps2;
-                    continue;
-                }
+        while (phase == 0) {
+            if (!i1.valid(wk)) {
+                phase = 1;
+            } else {
                 if (st < wk.steps1) break;
                 st -= wk.steps1;
-                i += gridDim.x;
+                i1.next(wk);
+            }
+        }
+        while (phase == 1) {
+            if (!i2.valid(wk)) {
+                phase = 2;
             } else {
-                if (i > end2 || (i == end2 && st >= end2_st)) {
-                    phase = 2;
-                    continue;
-                }
-                if (st < wk.steps2) break;
-                st -= wk.steps2;
-                ++i;
+                const int n = i2.st1(wk) - i2.st0;
+                if (st < n) break;
+                st -= n;
+                i2.next(wk);
             }
         }
         if (__all_sync(kLanes, phase == 2)) break;
         if (phase < 2) {
             const bool second = phase == 1;
-            const int a = second ? i % wk.n_active : i / wk.per1;
-            const int expert = tb.expert[a], r0 = second ? i / wk.n_active * G::kRows : (i - a * wk.per1) * G::kOut1;
+            const int expert = tb.expert[second ? i2.a : i1.a], r0 = second ? i2.r0() : i1.r0();
+            const int sti = second ? i2.st0 + st : st;
             const int s = it % G::kStages;
             const uint32_t dst = ring.base + (uint32_t)(s * G::kStageBytes), bar = ring.full(s);
             const CUtensorMap* map = second ? map2 : map1;
             if (mbar_wait(ring.empty(s), ((uint32_t)(it / G::kStages) & 1u) ^ 1u, p.hdr, abort_flag)) {
                 if constexpr (G::kBf16) {
                     mbar_arrive_expect_tx(bar, 16384);
-                    const int y = expert * (second ? p.I : p.H) + st * 64;
+                    const int y = expert * (second ? p.I : p.H) + sti * 64;
                     tma_load_2d(dst, map, r0, y, bar);
                     tma_load_2d(dst + 8192, map, second ? r0 + 64 : p.I + r0, y, bar);
                 } else {
                     const int row_bytes = (second ? p.I : p.H) / (G::kFp4 ? 2 : 1);
-                    const int row = expert * (second ? p.H : 2 * p.I) + r0, x = st * 256;
+                    const int row = expert * (second ? p.H : 2 * p.I) + r0, x = sti * 256;
                     const bool two = x + 128 < row_bytes;  // a box that ends inside a row is filled up with zeros
                     mbar_arrive_expect_tx(bar, two ? 8192u : 4096u);
                     // first product: 16 gate rows, then the up rows of the same outputs (the map's third coordinate)
@@ -553,63 +589,68 @@ __device__ __forceinline__ void produce(const Args& p, const CUtensorMap* map1, 
 // bytes of a row, and the rows of two neighbouring g, four apart, lie in different halves of the swizzled lines.
 __device__ __forceinline__ int perm(int g) { return (g >> 1) | ((g & 1) << 2); }
 
-// One column tile's values for a warp's part of a stage: B words as they are in memory (fp32 activations: two to a word of B).
+// One column tile's values for a slice: B words as they are in memory (fp32 activations: two to a word of B).
 template <int kFmt, bool kSecond>
 struct Columns {
     using G = Geo<kFmt>;
     static constexpr int kB = G::kBf16 ? 2 : G::kFp4 ? 16 : 8;  // 16-bit pairs of the tile
     static constexpr int kWords = kSecond ? 2 * kB : kB;
+    static constexpr int kBytes = kSecond ? 4 : 2;              // of a value in memory
     uint32_t w[kWords];
 
-    // r: the x row (a token) or activation row (a slot) of this lane's column, -1: none
-    __device__ __forceinline__ void load(const Args& p, int r, int k, int lane) {
-        const bool row = r >= 0;
+    // The x row or activation row `row` (-1: none), from this lane's first value of a slice on.
+    static __device__ __forceinline__ const uint8_t* base(const Args& p, int row, int lane) {
+        if (row < 0) return nullptr;
+        const uint8_t* q = kSecond ? reinterpret_cast<const uint8_t*>(p.act + (int64_t)row * p.I)
+                                   : reinterpret_cast<const uint8_t*>((G::kBf16 ? p.x : p.x16) + (int64_t)row * p.H);
+        return q + kBytes * (lane & 3) * (G::kBf16 ? 2 : G::kFp4 ? 32 : 16);
+    }
+    __device__ __forceinline__ void load(const uint8_t* q, int k) {
+        const bool on = q != nullptr;
+        q += kBytes * k;
         if constexpr (G::kBf16) {
-            const int at = k + 2 * (lane & 3);
             if constexpr (kSecond) {
-                const float* q = p.act + (int64_t)r * p.I + at;
-                const float2 u = row ? *reinterpret_cast<const float2*>(q) : make_float2(0.0f, 0.0f);
-                const float2 v = row ? *reinterpret_cast<const float2*>(q + 8) : make_float2(0.0f, 0.0f);
-                w[0] = __float_as_uint(u.x), w[1] = __float_as_uint(u.y);
-                w[2] = __float_as_uint(v.x), w[3] = __float_as_uint(v.y);
+                const uint2 u = on ? *reinterpret_cast<const uint2*>(q) : make_uint2(0, 0);
+                const uint2 v = on ? *reinterpret_cast<const uint2*>(q + 32) : make_uint2(0, 0);
+                w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
             } else {
-                const uint16_t* q = p.x + (int64_t)r * p.H + at;
-                w[0] = row ? *reinterpret_cast<const uint32_t*>(q) : 0u;
-                w[1] = row ? *reinterpret_cast<const uint32_t*>(q + 8) : 0u;
+                w[0] = on ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+                w[1] = on ? *reinterpret_cast<const uint32_t*>(q + 16) : 0u;
             }
         } else {
-            const int at = k + (G::kFp4 ? 32 : 16) * (lane & 3);
-            const uint4* q = kSecond ? reinterpret_cast<const uint4*>(p.act + (int64_t)r * p.I + at)
-                                     : reinterpret_cast<const uint4*>(p.x16 + (int64_t)r * p.H + at);
 #pragma unroll
             for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 v = row ? q[i] : make_uint4(0, 0, 0, 0);
+                const uint4 v = on ? reinterpret_cast<const uint4*>(q)[i] : make_uint4(0, 0, 0, 0);
                 w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
             }
         }
     }
 };
 
-// The weight scales of a warp's part of a stage. FP8: of the item's two 128-row blocks (gate, up). FP4: four bytes, one for
-// each 32 of K, of the rows g and g + 8 of both 16-row tiles.
+// The weight scales of a slice. FP8: of the item's two 128-row blocks (gate, up). FP4: four bytes, one for each 32 of K, of the
+// rows g and g + 8 of both 16-row tiles.
 template <int kFmt, bool kSecond>
 struct Scales {
     using G = Geo<kFmt>;
     uint32_t s[G::kFp4 ? 4 : 2];
-    __device__ __forceinline__ void load(const Args& p, int k, int K, int expert, int r0, int lane) {
-        const int N = kSecond ? p.H : 2 * p.I;
+    static __device__ __forceinline__ const uint8_t* base(const Args& p, int expert, int r0, int lane) {
+        const int K = kSecond ? p.I : p.H, N = kSecond ? p.H : 2 * p.I;
+        const uint8_t* q = static_cast<const uint8_t*>(kSecond ? p.s2 : p.s1);
+        if constexpr (G::kFp4) return q + ((int64_t)expert * N + r0 + perm(lane >> 2)) * (K / 32);
+        else if constexpr (!G::kBf16) return q + 4 * ((int64_t)expert * (N / 128) + r0 / 128) * (K / 128);
+        else return nullptr;
+    }
+    __device__ __forceinline__ void load(const Args& p, const uint8_t* q, int k) {
+        const int K = kSecond ? p.I : p.H;
         if constexpr (G::kFp4) {
-            const uint8_t* q = static_cast<const uint8_t*>(kSecond ? p.s2 : p.s1);
+            q += k / 32;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // i = 2 m: the tile's row g, 2 m + 1: its row g + 8
-                const int row = r0 + (i >> 1) * 8 + perm(lane >> 2) + ((i & 1) ? (kSecond ? 16 : p.I) : 0);
-                s[i] = __ldg(reinterpret_cast<const uint32_t*>(q + ((int64_t)expert * N + row) * (K / 32) + k / 32));
-            }
+            for (int i = 0; i < 4; ++i)  // i = 2 m: tile m's row g, 2 m + 1: its row g + 8
+                s[i] = __ldg(reinterpret_cast<const uint32_t*>(q + (int64_t)((i >> 1) * 8 + ((i & 1) ? (kSecond ? 16 : p.I) : 0)) * (K / 32)));
         } else if constexpr (!G::kBf16) {
-            const float* q = static_cast<const float*>(kSecond ? p.s2 : p.s1) + (int64_t)expert * (N / 128) * (K / 128) + k / 128;
-            s[0] = __float_as_uint(__ldg(q + (int64_t)(r0 / 128) * (K / 128)));
-            s[1] = kSecond ? s[0] : __float_as_uint(__ldg(q + (int64_t)((p.I + r0) / 128) * (K / 128)));
+            q += 4 * (k / 128);
+            s[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+            s[1] = kSecond ? s[0] : __ldg(reinterpret_cast<const uint32_t*>(q + (int64_t)4 * (p.I / 128) * (K / 128)));
         }
     }
 };
@@ -661,10 +702,10 @@ __device__ __forceinline__ void multiply_slice(const Args& p, uint32_t stage, in
                 f1[m] = __uint_as_float(sc.s[1]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    a[m][q][0] = e4m3x2_f16x2(ug[q]);
-                    a[m][q][1] = e4m3x2_f16x2(vg[q]);
-                    a[m][q][2] = e4m3x2_f16x2(ug[q] >> 16);
-                    a[m][q][3] = e4m3x2_f16x2(vg[q] >> 16);
+                    a[m][q][0] = e4m3x2_f16x2<0>(ug[q]);
+                    a[m][q][1] = e4m3x2_f16x2<0>(vg[q]);
+                    a[m][q][2] = e4m3x2_f16x2<1>(ug[q]);
+                    a[m][q][3] = e4m3x2_f16x2<1>(vg[q]);
                 }
             }
         }
@@ -674,7 +715,7 @@ __device__ __forceinline__ void multiply_slice(const Args& p, uint32_t stage, in
         if (n >= tiles) break;
         Cols c;
         if (n == 0) c = first;
-        else c.load(p, rows[n], k, lane);
+        else c.load(Cols::base(p, rows[n], lane), k);
         if constexpr (G::kBf16) {
             uint32_t hi[2], lo[2];
 #pragma unroll
@@ -717,117 +758,115 @@ __device__ __forceinline__ void multiply_slice(const Args& p, uint32_t stage, in
     }
 }
 
-// Stages [st0, st1) of one item by a consumer warp: its group's (i % kGroups of the CTA's sequence) times the expert's rows, then its sums to
-// the epilogue, one set a column tile. Groups without a stage of the item only sign for their part of the set.
-template <int kFmt, bool kSecond, int NT>
-__device__ __forceinline__ void consume(const Args& p, const Ring<kFmt>& ring, float* reds, const Tables& tb, int a, int r0, int st0, int st1,
-                                        int set, int warp, int lane, volatile int* abort_flag) {
-    using G = Geo<kFmt>;
-    using Cols = Columns<kFmt, kSecond>;
-    // so many slices' columns of the first tile are on their way at a time, as far as registers go
-    constexpr int kSums = G::kMt * 4 * NT;
-    constexpr int kAhead = 4 * Cols::kWords + kSums <= 80 ? 4 : 2 * Cols::kWords + kSums <= 80 ? 2 : 1;
-    const int K = kSecond ? p.I : p.H;
-    const int group = warp / G::kGroupWarps;
-    int st = st0 + (group - ring.it % G::kGroups + G::kGroups) % G::kGroups;  // this group's first stage of the item
-    const bool part = st < st1;
-    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, tiles = (n_rows + 7) / 8;
-    float acc[G::kMt][NT][4], ainv[NT];
-    if (part) {
-        const int Kt = p.K + p.S, expert = tb.expert[a];
-        int rows[NT];  // of this lane's column of each tile; -1 past the expert's rows
-        float ascale[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int c = n * 8 + (lane >> 2);
-            rows[n] = -1;
-            ascale[n] = ainv[n] = 1.0f;
-            if (c < n_rows) {
-                const int slot = tb.row[begin + c];
-                if constexpr (kSecond) {
-                    rows[n] = slot;
-                    if constexpr (!G::kBf16) ascale[n] = row_scale(__ldcg(p.amax + slot), &ainv[n]);
-                } else {
-                    rows[n] = slot / Kt;
-                }
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < G::kMt; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-        for (; st < st1; st += G::kGroups) {
-            const int it = ring.it + st - st0, s = it % G::kStages, k = st * G::kStepK;
-            const int slices = min(G::kSlices, (K - k) / G::kSliceK);
-            Cols cols[kAhead];
-            Scales<kFmt, kSecond> sc[G::kSlices];
-#pragma unroll
-            for (int i = 0; i < G::kSlices; ++i)
-                if (i < slices) {
-                    sc[i].load(p, k + i * G::kSliceK, K, expert, r0, lane);
-                    if (i < kAhead) cols[i].load(p, rows[0], k + i * G::kSliceK, lane);
-                }
-            // a wait that ran out skips the stage: the set is still signed for
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(ring.full(s), (uint32_t)(it / G::kStages) & 1u, p.hdr, abort_flag));
-            const uint32_t stage = ring.base + (uint32_t)(s * G::kStageBytes);
-            if (ok)
-#pragma unroll
-                for (int i = 0; i < G::kSlices; ++i)
-                    if (i < slices) {
-                        multiply_slice<kFmt, kSecond, NT>(p, stage, i, k + i * G::kSliceK, cols[i % kAhead], sc[i], rows, ascale,
-                                                          tiles, warp, lane, acc);
-                        if (i + kAhead < slices) cols[i % kAhead].load(p, rows[0], k + (i + kAhead) * G::kSliceK, lane);
-                    }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ring.empty(s));
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n, ++set) {
-        if (n >= tiles) break;
-        const int q = set % G::kReds;
-        mbar_wait(ring.red_empty(q), ((uint32_t)(set / G::kReds) & 1u) ^ 1u, p.hdr, abort_flag);
-        if (part) {
-            float* dst = reds + q * G::kRed + group * G::kRedGroup + (G::kBf16 ? (warp & 1) * 64 : 0);
-            const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-            for (int m = 0; m < G::kMt; ++m) {
-                const int r = G::kBf16 ? m * 16 + g : m * 8 + perm(g), r8 = G::kBf16 ? r + 8 : r + 16;
-                dst[(2 * t) * G::kRedCol + r] = acc[m][n][0];
-                dst[(2 * t + 1) * G::kRedCol + r] = acc[m][n][1];
-                dst[(2 * t) * G::kRedCol + r8] = acc[m][n][2];
-                dst[(2 * t + 1) * G::kRedCol + r8] = acc[m][n][3];
-            }
-            // once per set: by the group that holds the item's first stage
-            if (kSecond && !G::kBf16 && ring.it % G::kGroups == group && t == 0) reds[(q + 1) * G::kRed - 8 + g] = ainv[n];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ring.red_full(q));
-    }
-}
-
-template <int kFmt, bool kSecond, int NT>
-__device__ __forceinline__ void consume_item(const Args& p, Ring<kFmt>& ring, int& set, float* reds, const Tables& tb, int a, int r0,
-                                             int st0, int st1, int warp, int lane, volatile int* abort_flag) {
-    consume<kFmt, kSecond, NT>(p, ring, reds, tb, a, r0, st0, st1, set, warp, lane, abort_flag);
-    set += (tb.start[a + 1] - tb.start[a] + 7) / 8;
-    ring.it += st1 - st0;
-}
-
-// Waits for the rows of active experts, those of the next items looked at together: `known` items from the run's start on have
-// theirs (both epilogue warps of every item of the first product count).
-__device__ __forceinline__ void wait_rows(const Args& p, int i, int first_item, int n_active, int target, int& known, int lane,
+// Waits for the rows of the active expert a of the run's n-th item, those of the next items looked at together: `known` items
+// from the run's start on have theirs (both epilogue warps of every item of the first product count).
+__device__ __forceinline__ void wait_rows(const Args& p, int n, int a, int n_active, int target, int& known, int lane,
                                           volatile int* abort_flag) {
-    const int n = i - first_item;
     if (n < known || n >= n_active) return;  // after n_active items every expert has been looked at
     const bool on = n + lane < n_active;
-    const uint32_t there = __ballot_sync(0xffffffffu, !on || ld_acquire_gpu(p.dep + (i + lane) % n_active) >= target);
+    const int e = a + lane;
+    const uint32_t there = __ballot_sync(0xffffffffu, !on || ld_acquire_gpu(p.dep + (e >= n_active ? e - n_active : e)) >= target);
     const int ready = there == 0xffffffffu ? 32 : __ffs(~there) - 1;
     known = n + max(ready, 1);
-    if (ready == 0 && lane == 0) wait_count(p.dep + i % n_active, target, p.hdr, abort_flag);
+    if (ready == 0 && lane == 0) wait_count(p.dep + a, target, p.hdr, abort_flag);
     __syncwarp();  // the lanes' acquires order what the warp reads from here on
+}
+
+// The items of one phase by a consumer warp: of each item its group's stages (i % kGroups of the CTA's sequence) times the
+// expert's rows, then its sums to the epilogue, one set a column tile. Groups without a stage of an item only sign for their part
+// of the sets. A stage's scales and first columns are asked for before the wait for the stage (asking for those of the next
+// stage or item while a slice is multiplied was measured slower: 1494 us instead of 1182 for 32 tokens and 256 experts).
+template <int kFmt, bool kSecond, int NT>
+__device__ __forceinline__ void consume(const Args& p, Ring<kFmt>& ring, int& set, float* reds, const Tables& tb, const Work<kFmt>& wk,
+                                        int warp, int lane, volatile int* abort_flag) {
+    using G = Geo<kFmt>;
+    using Cols = Columns<kFmt, kSecond>;
+    using Sc = Scales<kFmt, kSecond>;
+    constexpr int kSlices = G::kSlices;
+    // so many slices of the first tile's values are held, as far as registers go
+    constexpr int kSums = G::kMt * 4 * NT;
+    constexpr int kAhead = 4 * Cols::kWords + kSums <= 80 ? 4 : 2 * Cols::kWords + kSums <= 80 ? 2 : 1;
+    const int K = kSecond ? p.I : p.H, group = warp / G::kGroupWarps;
+    Items<kFmt, kSecond> item(wk);
+    int seq = ring.it, known = 0;  // number of the item's first stage in the CTA's sequence
+
+    Cols cols[kAhead];
+    Sc sc[kSlices];
+    for (; item.valid(wk); item.next(wk)) {
+        const int a = item.a, r0 = item.r0(), st0 = item.st0, st1 = item.st1(wk);
+        int st = st0 + (group - seq % G::kGroups + G::kGroups) % G::kGroups;  // the group's first stage of the item
+        const bool part = st < st1;
+        if (kSecond) wait_rows(p, item.n, a, wk.n_active, kEpiWarps * wk.per1, known, lane, abort_flag);
+        const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, tiles = (n_rows + 7) / 8;
+        float acc[G::kMt][NT][4], ainv[NT];
+        if (part) {
+            int rows[NT];  // of this lane's column of each tile; -1 past the expert's rows
+            float ascale[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int c = n * 8 + (lane >> 2);
+                rows[n] = -1;
+                ascale[n] = ainv[n] = 1.0f;
+                if (c < n_rows) {
+                    const int slot = tb.row[begin + c];
+                    rows[n] = kSecond ? slot : (int)tb.token[slot];
+                    if constexpr (kSecond && !G::kBf16) ascale[n] = row_scale(__ldcg(p.amax + slot), &ainv[n]);
+                }
+            }
+            const uint8_t *col = Cols::base(p, rows[0], lane), *scale = Sc::base(p, tb.expert[a], r0, lane);
+#pragma unroll
+            for (int m = 0; m < G::kMt; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.0f;
+            for (; st < st1; st += G::kGroups) {
+                const int it = seq + st - st0, s = it % G::kStages, k0 = st * G::kStepK;
+#pragma unroll
+                for (int j = 0; j < kSlices; ++j)
+                    if (k0 + j * G::kSliceK < K) {
+                        sc[j].load(p, scale, k0 + j * G::kSliceK);
+                        if (j < kAhead) cols[j].load(col, k0 + j * G::kSliceK);
+                    }
+                // a wait that ran out skips the stage: the set is still signed for
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(ring.full(s), (uint32_t)(it / G::kStages) & 1u, p.hdr, abort_flag));
+                const uint32_t stage = ring.base + (uint32_t)(s * G::kStageBytes);
+#pragma unroll
+                for (int j = 0; j < kSlices; ++j) {
+                    if (ok && k0 + j * G::kSliceK < K)
+                        multiply_slice<kFmt, kSecond, NT>(p, stage, j, k0 + j * G::kSliceK, cols[j % kAhead], sc[j], rows, ascale, tiles,
+                                                          warp, lane, acc);
+                    if (j + kAhead < kSlices && k0 + (j + kAhead) * G::kSliceK < K) cols[j % kAhead].load(col, k0 + (j + kAhead) * G::kSliceK);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ring.empty(s));
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n, ++set) {
+            if (n >= tiles) break;
+            const int q = set % G::kReds;
+            mbar_wait(ring.red_empty(q), ((uint32_t)(set / G::kReds) & 1u) ^ 1u, p.hdr, abort_flag);
+            if (part) {
+                float* dst = reds + q * G::kRed + group * G::kRedGroup + (G::kBf16 ? (warp & 1) * 64 : 0);
+                const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+                for (int m = 0; m < G::kMt; ++m) {
+                    const int r = G::kBf16 ? m * 16 + g : m * 8 + perm(g), r8 = G::kBf16 ? r + 8 : r + 16;
+                    dst[(2 * t) * G::kRedCol + r] = acc[m][n][0];
+                    dst[(2 * t + 1) * G::kRedCol + r] = acc[m][n][1];
+                    dst[(2 * t) * G::kRedCol + r8] = acc[m][n][2];
+                    dst[(2 * t + 1) * G::kRedCol + r8] = acc[m][n][3];
+                }
+                // once per set: by the group that holds the item's first stage
+                if (kSecond && !G::kBf16 && seq % G::kGroups == group && t == 0) reds[(q + 1) * G::kRed - 8 + g] = ainv[n];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ring.red_full(q));
+        }
+        seq += st1 - st0;
+    }
+    ring.it = seq;
 }
 
 // The sum of the groups' parts of one value of a set; the item's stages begin at `it` and are `steps` many.
@@ -849,7 +888,7 @@ template <int kFmt>
 __device__ __forceinline__ void finish_first(const Args& p, Ring<kFmt>& ring, int& set, const float* reds, const Tables& tb, int a,
                                              int r0, int w, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
-    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, Kt = p.K + p.S;
+    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin;
     const int steps = (p.H + G::kStepK - 1) / G::kStepK, tiles = (n_rows + 7) / 8;
     for (int n = 0; n < tiles; ++n, ++set) {
         const int q = set % G::kReds;
@@ -861,7 +900,7 @@ __device__ __forceinline__ void finish_first(const Args& p, Ring<kFmt>& ring, in
 #pragma unroll
         for (int i = 0; i < 8 / kCols; ++i) {
             const int c = n * 8 + i * kCols + (G::kBf16 ? 0 : lane >> 3);
-            inv[i] = !G::kBf16 && c < n_rows ? __ldcg(p.xinv + tb.row[begin + c] / Kt) : 1.0f;
+            inv[i] = !G::kBf16 && c < n_rows ? __ldcg(p.xinv + tb.token[tb.row[begin + c]]) : 1.0f;
         }
         mbar_wait(ring.red_full(q), (uint32_t)(set / G::kReds) & 1u, p.hdr, abort_flag);
 #pragma unroll
@@ -896,8 +935,7 @@ template <int kFmt>
 __device__ __forceinline__ void finish_second(const Args& p, Ring<kFmt>& ring, int& set, const float* reds, const Tables& tb, float* y,
                                               int a, int steps, int w, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
-    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, Kt = p.K + p.S;
-    const int tiles = (n_rows + 7) / 8;
+    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, tiles = (n_rows + 7) / 8;
     for (int n = 0; n < tiles; ++n, ++set) {
         const int q = set % G::kReds;
         const float* red = reds + q * G::kRed;
@@ -918,7 +956,7 @@ __device__ __forceinline__ void finish_second(const Args& p, Ring<kFmt>& ring, i
 #pragma unroll
                 for (int h = 0; h < (G::kBf16 ? 2 : 1); ++h) {
                     const int r = G::kBf16 ? w * 64 + h * 32 + lane : w * 16 + (lane & 15);
-                    float* dst = y + slot[i] / Kt * G::kRows + r;
+                    float* dst = y + tb.token[slot[i]] * G::kRows + r;
                     *dst = fmaf(red_sum<kFmt>(red, ring.it, steps, cc, r) * f, weight, *dst);
                 }
             }
@@ -945,17 +983,22 @@ __device__ void finish_columns(const Args& p, Tables& tb, float* y, const Work<k
         epilogue_sync();
         return;
     }
-    // the CTAs with experts of these columns, in order (with fewer items than CTAs, some in between have none)
-    if (tid == 0) {
+    // the CTAs with stages of these columns, in order; a CTA's first column group goes to its first buffer, its last to the second
+    if (tid < 32) {
         int parts = 0;
-        for (int i = first; i < end; ++parts) {
-            const int c = wk.owner(i);
-            // a CTA's first column group goes to its first buffer, its last to the second
-            tb.count[parts] = 2 * c + (wk.first(c) / wk.group() == g ? 0 : 1);
-            if (c == (int)blockIdx.x) tb.mine = tb.count[parts];
-            i = wk.first(c + 1);
+        for (int b = 0; b < wk.grid; b += 32) {
+            const int c = b + tid;
+            const int lo = c < wk.grid ? tb.first[c] : 0, hi = c < wk.grid ? tb.first[c + 1] : 0;
+            const bool in = max(lo, first) < min(hi, end);
+            const uint32_t all = __ballot_sync(0xffffffffu, in);
+            if (in) {
+                const int at = parts + __popc(all & ((1u << tid) - 1u)), buffer = 2 * c + (lo >= first ? 0 : 1);
+                tb.count[at] = buffer;
+                if (c == (int)blockIdx.x) tb.mine = buffer;
+            }
+            parts += __popc(all);
         }
-        tb.last = parts;
+        if (tid == 0) tb.last = parts;
     }
     epilogue_sync();
     const int parts = tb.last;
@@ -1048,6 +1091,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_smem();
     __syncthreads();
     const Work<kFmt> wk(p, tb.n_active);
+    for (int c = threadIdx.x; c <= (int)gridDim.x; c += kThreads) tb.first[c] = wk.first(c);
+    __syncthreads();
 
     // ---- phases 3 and 4
     if (warp >= kWarps) {
@@ -1057,30 +1102,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp <= kWarps + kEpiWarps) {
             const int w = warp - kWarps - 1;
             int set = 0;
-            for (int i = blockIdx.x; i < wk.n1; i += gridDim.x)
-                finish_first<kFmt>(p, ring, set, reds, tb, i / wk.per1, i % wk.per1 * G::kOut1, w, lane, abort_flag);
-            for (int at = wk.lo2; at < wk.hi2;) {
-                const int i = at / wk.steps2, to = min(wk.hi2, (i + 1) * wk.steps2);
-                finish_second<kFmt>(p, ring, set, reds, tb, y, i % wk.n_active, to - at, w, lane, abort_flag);
-                at = to;
-                if (at == wk.hi2 || at % wk.group() == 0) finish_columns<kFmt>(p, tb, y, wk, i / wk.n_active, w * 32 + lane);
+            for (Items<kFmt, false> item(wk); item.valid(wk); item.next(wk))
+                finish_first<kFmt>(p, ring, set, reds, tb, item.a, item.r0(), w, lane, abort_flag);
+            for (Items<kFmt, true> item(wk); item.valid(wk);) {
+                finish_second<kFmt>(p, ring, set, reds, tb, y, item.a, item.st1(wk) - item.st0, w, lane, abort_flag);
+                const int g = item.group;
+                item.next(wk);
+                if (item.group != g || !item.valid(wk)) finish_columns<kFmt>(p, tb, y, wk, g, w * 32 + lane);
             }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         int set = 0;
-        for (int i = blockIdx.x; i < wk.n1; i += gridDim.x)
-            consume_item<kFmt, false, NT>(p, ring, set, reds, tb, i / wk.per1, i % wk.per1 * G::kOut1, 0, wk.steps1, warp, lane, abort_flag);
-        const int first_item = wk.lo2 / wk.steps2;
-        int known = 0;
-        for (int at = wk.lo2; at < wk.hi2;) {
-            const int i = at / wk.steps2, a = i % wk.n_active;
-            const int begin = i * wk.steps2, to = min(wk.hi2, begin + wk.steps2);
-            wait_rows(p, i, first_item, wk.n_active, kEpiWarps * wk.per1, known, lane, abort_flag);
-            consume_item<kFmt, true, NT>(p, ring, set, reds, tb, a, i / wk.n_active * G::kRows, at - begin, to - begin,
-                                         warp, lane, abort_flag);
-            at = to;
-        }
+        consume<kFmt, false, NT>(p, ring, set, reds, tb, wk, warp, lane, abort_flag);
+        consume<kFmt, true, NT>(p, ring, set, reds, tb, wk, warp, lane, abort_flag);
     }
     if (wk.n_active == 0)
         for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (int64_t)p.T * p.H; i += (int64_t)gridDim.x * kThreads)
