@@ -6,7 +6,7 @@
 // weights once. The kernel is a stream of weights through shared memory: one CTA per SM, a producer warp that keeps a ring
 // of stages of 16 KB full by TMA, and eight warps that multiply each stage by the tokens' rows with mma.sync
 // (16 weight rows x 8 tokens x 16 of K), which at this shape is far from the tensor pipe's bound. The weight addresses
-// depend on the routes alone, so the producer runs ahead across items, experts and from the first product into the
+// depend on the routes alone, so the producer runs ahead across units, experts and from the first product into the
 // second, while the consumers wait for activations.
 //
 // Phases:
@@ -14,15 +14,16 @@
 //      selection compares these sums); one CTA per token also rounds x to the f16 operand of the FP8 and FP4 formats. Grid barrier.
 //   2. selection: each CTA selects for all tokens itself (up to 8 tokens), or for its share of them and a second barrier.
 //      Each CTA then lists the experts with rows and their rows in shared memory.
-//   3. first product: items of 16 outputs (16 gate and 16 up rows of W1; BF16: 64 and 64) of one expert, dealt to the CTAs in
-//      turn. Each warp (BF16: pair of warps) takes every eighth (fourth) stage whole, so that a stage costs one wait and one
-//      arrival and its latencies have the time of eight stages; the warps' sums of an item meet in shared memory, where two
-//      epilogue warps add them up. SwiGLU of them goes to the workspace in fp32 with the row's largest magnitude. A counter per
-//      expert says when its rows are complete.
-//   4. second product: items of 32 hidden columns (BF16: 128) of one expert, ordered by columns first and dealt in runs of
-//      stages, so that a CTA adds up the experts of its columns itself, in order, in shared memory. Columns whose stages are
-//      split between CTAs meet in the workspace: the last CTA to arrive adds the parts in order. No atomics on values:
-//      results do not depend on timing.
+//   3. first product: units of 16 outputs (16 gate and 16 up rows of W1; BF16: 64 and 64) of one expert. Each warp (BF16: pair
+//      of warps) takes every eighth (fourth) stage whole, so that a stage costs one wait and one arrival and its latencies have the
+//      time of eight stages; the warps' sums of a unit meet in shared memory, where one of two epilogue warps adds them up. SwiGLU of
+//      them goes to the workspace in fp32 with the row's largest magnitude. A counter per expert says when its rows are complete.
+//   4. second product: units of 32 hidden columns (BF16: 128) of one expert, expert by expert, over all of K or a part of it. The
+//      slots' sums go to the workspace; the epilogue warp that brings the last ones of a column group adds its tokens' slots up
+//      in order.
+// Units are handed out one by one from a counter, a few ahead of the producer: equal shares of the bytes left the SMs up to a sixth
+// apart at the end. What a unit computes does not depend on who computes it, and there are no atomics on values: results do not
+// depend on timing.
 //
 // Operands. BF16: x as it is; the activations as two bf16 (hi + lo, 16 bits of them) and two MMAs. FP8 and FP4: the weights are
 // exact in f16, x and the activations are scaled by a power of two of their row to below 2^15 and rounded once to f16 (11 bits;
@@ -50,14 +51,14 @@ namespace {
 using namespace tc;
 
 constexpr int kWarps = 8;                       // consumers
-constexpr int kAllWarps = 12;                   // warp 8 is the producer, 9 and 10 the epilogue, 11 only helps in the first phases
+constexpr int kAllWarps = 12;                   // warp 8 is the producer, 9 and 10 the epilogue, 11 fetches units
 constexpr int kThreads = 32 * kAllWarps;
 // registers of warps 8-11 and of the consumers from phase 3 on: 128 * 104 + 256 * 200 = 384 * 168, what the launch holds
 constexpr int kLaunchRegs = 168, kFewRegs = 104, kManyRegs = 200;
 static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kMaxT = MOE_LAYER_MAX_TOKENS;
 constexpr int kMaxSlots = kMaxT * 32;
-constexpr int kEpiWarps = 2;                    // warps 9 and 10 take the sums of an item further
+constexpr int kEpiWarps = 2;                    // warps 9 and 10 take the sums of a unit further
 constexpr int kMaxE = 1024;
 
 // Stage geometry. K-contiguous formats: two boxes of 32 rows x 128 bytes. BF16: 64 of K x two boxes of 64 columns. All boxes
@@ -66,8 +67,8 @@ template <int kFmt>
 struct Geo {
     static constexpr bool kBf16 = kFmt == MOE_LAYER_BF16;
     static constexpr bool kFp4 = kFmt == MOE_LAYER_FP4_MX;
-    static constexpr int kRows = kBf16 ? 128 : 32;  // weight rows of an item
-    static constexpr int kOut1 = kRows / 2;         // outputs of an item of the first product
+    static constexpr int kRows = kBf16 ? 128 : 32;  // weight rows of a unit
+    static constexpr int kOut1 = kRows / 2;         // outputs of a unit of the first product
     static constexpr int kStepK = kBf16 ? 64 : kFp4 ? 512 : 256;
     static constexpr int kSlices = 4, kSliceK = kStepK / kSlices;
     static constexpr int kStageBytes = kBf16 ? 16384 : 8192;
@@ -82,22 +83,26 @@ struct Geo {
     static constexpr int kRedGroup = 8 * kRedCol;
     static constexpr int kRed = kGroups * kRedGroup + 8;  // and the inverse scale of each column's activations
     static constexpr int kReds = kBf16 ? 2 : 4;     // sets of partial sums on their way to the epilogue
-    // shared memory: ring | sets of partial sums | tables | y sums
+    static_assert(kReds % kEpiWarps == 0, "likewise for the sets and the epilogue's warps, which take them in turn");
+    // shared memory: ring | sets of partial sums | tables
     static constexpr int kRedOff = kStages * kStageBytes;
     static constexpr int kTabOff = kRedOff + kReds * 4 * kRed;
 };
 
 constexpr int kMaxBars = 48;
+constexpr int kQueue = 64;                      // units between the fetching warp and the slowest reader: at most some 24
+constexpr uint32_t kNoUnit = 0xffffffffu;
 
 struct Tables {
     uint64_t bars[kMaxBars];
-    int n_active, last, abort, mine;
+    volatile uint64_t queue[kQueue];      // the CTA's units: (k + 1) << 32 | unit of the k-th
+    volatile int begun;                   // units the producer has begun
+    int n_active, last, abort;
     int count[kMaxE];
     int16_t expert[kMaxE];                // active experts
     int16_t start[kMaxE + 2];             // where their rows begin in row[]
     uint16_t row[kMaxSlots];              // slot = token * (K + S) + k
     uint8_t token[kMaxSlots];             // by slot
-    int first[kMaxSms + 1];               // where the CTAs' runs of the second product begin
     float weight[kMaxSlots];              // by slot
     int16_t id[kMaxSlots];                // by slot, -1: none
 };
@@ -115,9 +120,10 @@ struct Args {
     int router_bf16;
     int T, H, I, E, K, S;
     float clamp;
-    int32_t* hdr;      // [0] error word, [1] barrier, [2] CTAs finished
-    int32_t* dep;      // per active expert: finished items of the first product
-    int32_t* cols;     // per column group: parts that have arrived
+    int splits;        // parts of K that a column group of an expert is cut into in the second product
+    int32_t* hdr;      // [0] error word, [1] barrier, [2] CTAs finished, [3] units handed out
+    int32_t* dep;      // per active expert: finished column tiles of its units of the first product
+    int32_t* cols;     // per column group: finished column tiles of the second product
     uint32_t* amax;    // per slot: largest |activation| so far, as bits
     float* logits;     // [T][E]
     int32_t* ids;      // [T][K]
@@ -125,7 +131,7 @@ struct Args {
     uint16_t* x16;     // f16 [T][H]
     float* xinv;       // [T]
     float* act;        // [slots][I]
-    float* part;       // [CTA][2][T][rows of an item]
+    float* comb;       // [splits][slots][H]
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -193,7 +199,6 @@ __device__ __forceinline__ float row_scale(uint32_t top, float* inverse) {
     *inverse = __uint_as_float((uint32_t)(e - 14) << 23);     // 2^(e - 141)
     return __uint_as_float((uint32_t)(268 - e) << 23);        // 2^(141 - e)
 }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 64;" ::: "memory"); }
 
 // All CTAs have arrived n times (n counts the barriers of this launch); one thread waits, bounded.
 __device__ __forceinline__ void grid_barrier(const Args& p, int n, volatile int* abort_flag) {
@@ -424,80 +429,85 @@ __device__ void list_experts(const Args& p, Tables& tb, const int32_t* ids, cons
 // phases 3 and 4
 // ---------------------------------------------------------------------------------------
 
-// The work of a CTA in order: its items of the first product (dealt in turn), then its run of the second product's stages. Those
-// are numbered column group by column group, expert by expert, and a run may begin and end inside an item: sums of parts of K
-// meet like sums of different experts do. Runs are cut so that every CTA has the same number of stages in all.
+// The launch's work in units, handed out one by one: first those of the first product, expert by expert, then those of the second.
+// A unit of the first is kOut1 outputs of an expert; of the second it is kRows hidden columns of an expert, over all of K or one
+// of `splits` parts of it.
 template <int kFmt>
 struct Work {
-    int per1, n1;          // items of the first product per expert, in all
-    int n_active, steps2;  // experts with rows; stages of an item of the second product
-    int steps1, grid;
-    int total2;            // all stages of the second product (below 2^30 at the limits of the sizes)
-    int lo2, hi2;          // this CTA's run
+    uint32_t per1, per2, n1, total;  // units per expert, of the first product, in all
+    int steps1, steps2, split_steps;
+    uint32_t splits;
     __device__ Work(const Args& p, int active) {
         using G = Geo<kFmt>;
+        splits = p.splits;
         per1 = p.I / G::kOut1;
-        n_active = active;
+        per2 = p.H / G::kRows * splits;
         n1 = per1 * active;
+        total = n1 + per2 * active;
         steps1 = (p.H + G::kStepK - 1) / G::kStepK;
         steps2 = (p.I + G::kStepK - 1) / G::kStepK;
-        grid = (int)gridDim.x;
-        total2 = p.H / G::kRows * active * steps2;
-        lo2 = first(blockIdx.x);
-        hi2 = first(blockIdx.x + 1);
+        split_steps = (steps2 + p.splits - 1) / p.splits;
     }
-    // the first stage of CTA c's run
-    __device__ int first(int c) const {
-        const int each = n1 / grid, more = n1 % grid;  // the first `more` CTAs have one item more
-        const int64_t all = (int64_t)n1 * steps1 + total2;
-        if (all < (int64_t)(each + (more > 0)) * steps1 * grid) return (int)((int64_t)total2 * c / grid);  // cannot be made even
-        return (int)(all * c / grid - (int64_t)steps1 * ((int64_t)each * c + min(c, more)));
-    }
-    // stages of a column group
-    __device__ int group() const { return n_active * steps2; }
 };
 
-// The items of a CTA's phase in order, stepped without divisions.
-template <int kFmt, bool kSecond>
-struct Items {
-    int a, group;  // active expert, group of rows (kOut1 outputs or kRows hidden columns) in it
-    int n = 0;     // items before this one
-    int st0, left; // first stage; second product: stages of the run from this item on
-    __device__ __forceinline__ explicit Items(const Work<kFmt>& wk) {
-        if constexpr (kSecond) {
-            const int per = wk.group();
-            group = per > 0 ? wk.lo2 / per : 0;
-            const int in = wk.lo2 - group * per;
-            a = in / wk.steps2;
-            st0 = in - a * wk.steps2;
-            left = wk.hi2 - wk.lo2;
-        } else {
-            a = (int)blockIdx.x / wk.per1;
-            group = (int)blockIdx.x - a * wk.per1;
-            st0 = left = 0;
-        }
-    }
-    __device__ __forceinline__ bool valid(const Work<kFmt>& wk) const { return kSecond ? left > 0 : a < wk.n_active; }
-    __device__ __forceinline__ int st1(const Work<kFmt>& wk) const { return kSecond ? min(wk.steps2, st0 + left) : wk.steps1; }
-    __device__ __forceinline__ int r0() const { return group * (kSecond ? Geo<kFmt>::kRows : Geo<kFmt>::kOut1); }
-    __device__ __forceinline__ void next(const Work<kFmt>& wk) {
-        ++n;
-        if constexpr (kSecond) {
-            left -= st1(wk) - st0;
-            st0 = 0;
-            if (++a == wk.n_active) {
-                a = 0;
-                ++group;
-            }
-        } else {
-            group += wk.grid;
-            while (group >= wk.per1) {
-                group -= wk.per1;
-                ++a;
-            }
-        }
-    }
+struct Unit {
+    int a, group, split, st0, st1;  // active expert; group of rows (or of hidden columns); part of K; stages [st0, st1)
 };
+template <int kFmt>
+__device__ __forceinline__ Unit unit_first(const Work<kFmt>& wk, uint32_t u) {
+    const uint32_t a = u / wk.per1;
+    return {(int)a, (int)(u - a * wk.per1), 0, 0, wk.steps1};
+}
+template <int kFmt>
+__device__ __forceinline__ Unit unit_second(const Work<kFmt>& wk, uint32_t u) {
+    u -= wk.n1;
+    const uint32_t a = u / wk.per2, r = u - a * wk.per2, g = r / wk.splits, q = r - g * wk.splits;
+    // (parts of whole stages: the last ones may be empty)
+    const int st0 = min(wk.steps2, (int)q * wk.split_steps);
+    return {(int)a, (int)g, (int)q, st0, min(wk.steps2, st0 + wk.split_steps)};
+}
+
+// The CTA's k-th unit, kNoUnit after the last one (or when the wait ran out).
+__device__ __forceinline__ uint32_t take(const Tables& tb, int k, int32_t* hdr, volatile int* abort_flag) {
+    const volatile uint64_t* q = tb.queue + k % kQueue;
+    uint64_t v = *q;
+    if ((uint32_t)(v >> 32) == (uint32_t)k + 1u) return (uint32_t)v;
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 1;; ++i) {
+        v = *q;
+        if ((uint32_t)(v >> 32) == (uint32_t)k + 1u) return (uint32_t)v;
+        if (*abort_flag) return kNoUnit;
+        if (i % 256 == 0 && globaltimer_ns() - t0 > kWaitTimeoutNs) {
+            record_error(hdr, MOE_ERR_TIMEOUT);
+            *abort_flag = 1;
+            return kNoUnit;
+        }
+    }
+}
+
+// One lane: gets the CTA's units from the launch's counter, a few ahead of the producer, until they run out.
+template <int kFmt>
+__device__ __forceinline__ void fetch(const Args& p, Tables& tb, const Work<kFmt>& wk, volatile int* abort_flag) {
+    constexpr int kLead = 3;
+    uint32_t u = blockIdx.x;  // the first one is given
+    for (int k = 0;; ++k) {
+        if (k > 0) {
+            const uint64_t t0 = globaltimer_ns();
+            while (tb.begun + kLead < k) {
+                if (*abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs) {
+                    if (!*abort_flag) record_error(p.hdr, MOE_ERR_TIMEOUT);
+                    *abort_flag = 1;
+                    return;
+                }
+                __nanosleep(32);
+            }
+            u = gridDim.x + (uint32_t)atomicAdd(p.hdr + 3, 1);
+        }
+        const bool end = u >= wk.total;
+        tb.queue[k % kQueue] = ((uint64_t)(k + 1) << 32) | (end ? kNoUnit : u);
+        if (end) return;
+    }
+}
 
 template <int kFmt>
 struct Ring {
@@ -517,40 +527,27 @@ constexpr int kProducers = 4;
 
 template <int kFmt>
 __device__ __forceinline__ void produce(const Args& p, const CUtensorMap* map1, const CUtensorMap* map2, const Ring<kFmt>& ring,
-                                        const Tables& tb, const Work<kFmt>& wk, int lane, volatile int* abort_flag) {
+                                        Tables& tb, const Work<kFmt>& wk, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
     static_assert(G::kStages % kProducers == 0, "a slot of the ring is always the same lane's");
     constexpr uint32_t kLanes = (1u << kProducers) - 1u;
-    int it = lane, st = lane;             // this lane's stage: of the sequence, and of the item past its first stage
-    int phase = 0;                        // 0: first product, 1: second, 2: past the end
-    int last = -1;                        // the last stage this lane issued
-    Items<kFmt, false> i1(wk);
-    Items<kFmt, true> i2(wk);
+    int k = 0, last = -1;                 // units taken; the last stage this lane issued
+    uint32_t u = take(tb, k, p.hdr, abort_flag);
+    bool second = u >= wk.n1;
+    Unit un = {};
+    if (u != kNoUnit) un = second ? unit_second(wk, u) : unit_first(wk, u);
+    int it = lane, st = lane;             // this lane's stage: of the sequence, and of the unit past its first stage
     for (;; it += kProducers, st += kProducers) {
-        while (phase == 0) {
-            if (!i1.valid(wk)) {
-                phase = 1;
-            } else {
-                if (st < wk.steps1) break;
-                st -= wk.steps1;
-                i1.next(wk);
-            }
+        while (u != kNoUnit && st >= un.st1 - un.st0) {
+            st -= un.st1 - un.st0;
+            u = take(tb, ++k, p.hdr, abort_flag);
+            if (lane == 0) tb.begun = k;
+            second = u >= wk.n1;
+            if (u != kNoUnit) un = second ? unit_second(wk, u) : unit_first(wk, u);
         }
-        while (phase == 1) {
-            if (!i2.valid(wk)) {
-                phase = 2;
-            } else {
-                const int n = i2.st1(wk) - i2.st0;
-                if (st < n) break;
-                st -= n;
-                i2.next(wk);
-            }
-        }
-        if (__all_sync(kLanes, phase == 2)) break;
-        if (phase < 2) {
-            const bool second = phase == 1;
-            const int expert = tb.expert[second ? i2.a : i1.a], r0 = second ? i2.r0() : i1.r0();
-            const int sti = second ? i2.st0 + st : st;
+        if (__all_sync(kLanes, u == kNoUnit)) break;
+        if (u != kNoUnit) {
+            const int expert = tb.expert[un.a], r0 = un.group * (second ? G::kRows : G::kOut1), sti = un.st0 + st;
             const int s = it % G::kStages;
             const uint32_t dst = ring.base + (uint32_t)(s * G::kStageBytes), bar = ring.full(s);
             const CUtensorMap* map = second ? map2 : map1;
@@ -575,7 +572,7 @@ __device__ __forceinline__ void produce(const Args& p, const CUtensorMap* map1, 
                 }
                 last = it;
             } else {
-                phase = 2;  // gave up: what is in flight is waited for below
+                u = kNoUnit;  // gave up: what is in flight is waited for below
             }
         }
         __syncwarp(kLanes);
@@ -627,7 +624,7 @@ struct Columns {
     }
 };
 
-// The weight scales of a slice. FP8: of the item's two 128-row blocks (gate, up). FP4: four bytes, one for each 32 of K, of the
+// The weight scales of a slice. FP8: of the unit's two 128-row blocks (gate, up). FP4: four bytes, one for each 32 of K, of the
 // rows g and g + 8 of both 16-row tiles.
 template <int kFmt, bool kSecond>
 struct Scales {
@@ -758,27 +755,28 @@ __device__ __forceinline__ void multiply_slice(const Args& p, uint32_t stage, in
     }
 }
 
-// Waits for the rows of the active expert a of the run's n-th item, those of the next items looked at together: `known` items
-// from the run's start on have theirs (both epilogue warps of every item of the first product count).
-__device__ __forceinline__ void wait_rows(const Args& p, int n, int a, int n_active, int target, int& known, int lane,
+// Waits for the rows of active expert a, those of the next ones looked at together: experts below `known` have theirs
+// (units come expert by expert).
+__device__ __forceinline__ void wait_rows(const Args& p, const Tables& tb, int a, int per1, int& known, int lane,
                                           volatile int* abort_flag) {
-    if (n < known || n >= n_active) return;  // after n_active items every expert has been looked at
-    const bool on = n + lane < n_active;
-    const int e = a + lane;
-    const uint32_t there = __ballot_sync(0xffffffffu, !on || ld_acquire_gpu(p.dep + (e >= n_active ? e - n_active : e)) >= target);
+    if (a < known) return;
+    // a unit counts its column tiles
+    auto target = [&](int e) { return per1 * ((tb.start[e + 1] - tb.start[e] + 7) / 8); };
+    const bool on = a + lane < tb.n_active;
+    const uint32_t there = __ballot_sync(0xffffffffu, on && ld_acquire_gpu(p.dep + a + lane) >= target(on ? a + lane : a));
     const int ready = there == 0xffffffffu ? 32 : __ffs(~there) - 1;
-    known = n + max(ready, 1);
-    if (ready == 0 && lane == 0) wait_count(p.dep + a, target, p.hdr, abort_flag);
+    known = a + max(ready, 1);
+    if (ready == 0 && lane == 0) wait_count(p.dep + a, target(a), p.hdr, abort_flag);
     __syncwarp();  // the lanes' acquires order what the warp reads from here on
 }
 
-// The items of one phase by a consumer warp: of each item its group's stages (i % kGroups of the CTA's sequence) times the
-// expert's rows, then its sums to the epilogue, one set a column tile. Groups without a stage of an item only sign for their part
-// of the sets. A stage's scales and first columns are asked for before the wait for the stage (asking for those of the next
-// stage or item while a slice is multiplied was measured slower: 1494 us instead of 1182 for 32 tokens and 256 experts).
+// The units of one product by a consumer warp, from the CTA's k-th (u) on: of each its group's stages (i % kGroups of the CTA's
+// sequence) times the expert's rows, then its sums to the epilogue, one set a column tile. Groups without a stage of a unit only
+// sign for their part of the sets. A stage's scales and first columns are asked for before the wait for the stage (asking for those of the next
+// stage or unit while a slice is multiplied was measured slower: 1494 us instead of 1182 for 32 tokens and 256 experts).
 template <int kFmt, bool kSecond, int NT>
-__device__ __forceinline__ void consume(const Args& p, Ring<kFmt>& ring, int& set, float* reds, const Tables& tb, const Work<kFmt>& wk,
-                                        int warp, int lane, volatile int* abort_flag) {
+__device__ __forceinline__ void consume(const Args& p, Ring<kFmt>& ring, int& set, int& k, uint32_t& u, float* reds,
+                                        const Tables& tb, const Work<kFmt>& wk, int warp, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
     using Cols = Columns<kFmt, kSecond>;
     using Sc = Scales<kFmt, kSecond>;
@@ -787,16 +785,16 @@ __device__ __forceinline__ void consume(const Args& p, Ring<kFmt>& ring, int& se
     constexpr int kSums = G::kMt * 4 * NT;
     constexpr int kAhead = 4 * Cols::kWords + kSums <= 80 ? 4 : 2 * Cols::kWords + kSums <= 80 ? 2 : 1;
     const int K = kSecond ? p.I : p.H, group = warp / G::kGroupWarps;
-    Items<kFmt, kSecond> item(wk);
-    int seq = ring.it, known = 0;  // number of the item's first stage in the CTA's sequence
+    int seq = ring.it, known = 0;  // number of the unit's first stage in the CTA's sequence; see wait_rows
 
     Cols cols[kAhead];
     Sc sc[kSlices];
-    for (; item.valid(wk); item.next(wk)) {
-        const int a = item.a, r0 = item.r0(), st0 = item.st0, st1 = item.st1(wk);
-        int st = st0 + (group - seq % G::kGroups + G::kGroups) % G::kGroups;  // the group's first stage of the item
+    for (; u != kNoUnit && (kSecond || u < wk.n1); u = take(tb, ++k, p.hdr, abort_flag)) {
+        const Unit un = kSecond ? unit_second(wk, u) : unit_first(wk, u);
+        const int a = un.a, r0 = un.group * (kSecond ? G::kRows : G::kOut1), st0 = un.st0, st1 = un.st1;
+        int st = st0 + (group - seq % G::kGroups + G::kGroups) % G::kGroups;  // the group's first stage of the unit
         const bool part = st < st1;
-        if (kSecond) wait_rows(p, item.n, a, wk.n_active, kEpiWarps * wk.per1, known, lane, abort_flag);
+        if (kSecond) wait_rows(p, tb, a, (int)wk.per1, known, lane, abort_flag);
         const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, tiles = (n_rows + 7) / 8;
         float acc[G::kMt][NT][4], ainv[NT];
         if (part) {
@@ -858,7 +856,7 @@ __device__ __forceinline__ void consume(const Args& p, Ring<kFmt>& ring, int& se
                     dst[(2 * t) * G::kRedCol + r8] = acc[m][n][2];
                     dst[(2 * t + 1) * G::kRedCol + r8] = acc[m][n][3];
                 }
-                // once per set: by the group that holds the item's first stage
+                // once per set: by the group that holds the unit's first stage
                 if (kSecond && !G::kBf16 && seq % G::kGroups == group && t == 0) reds[(q + 1) * G::kRed - 8 + g] = ainv[n];
             }
             __syncwarp();
@@ -869,160 +867,150 @@ __device__ __forceinline__ void consume(const Args& p, Ring<kFmt>& ring, int& se
     ring.it = seq;
 }
 
-// The sum of the groups' parts of one value of a set; the item's stages begin at `it` and are `steps` many.
+// The sum of the groups' parts of one value of a set; the unit's stages begin at `it` and are `steps` many. In the order of the
+// stages, whichever groups they fell to: the sum does not depend on what the CTA did before.
 template <int kFmt>
 __device__ __forceinline__ float red_sum(const float* red, int it, int steps, int col, int row) {
     using G = Geo<kFmt>;
+    const float* q = red + col * G::kRedCol + row;
     float s = 0.0f;
     if (steps >= G::kGroups) {
 #pragma unroll
-        for (int i = 0; i < G::kGroups; ++i) s += red[i * G::kRedGroup + col * G::kRedCol + row];
+        for (int i = 0; i < G::kGroups; ++i) s += q[(it + i) % G::kGroups * G::kRedGroup];
     } else {
-        for (int i = 0; i < steps; ++i) s += red[(it + i) % G::kGroups * G::kRedGroup + col * G::kRedCol + row];
+        for (int i = 0; i < steps; ++i) s += q[(it + i) % G::kGroups * G::kRedGroup];
     }
     return s;
 }
 
-// Epilogue warp w (0 or 1) of an item of the first product: half of its outputs, SwiGLU and the row's largest magnitude.
+// A unit of the first product by epilogue warp w, which takes every second set: SwiGLU of its outputs and the rows' largest
+// magnitudes.
 template <int kFmt>
 __device__ __forceinline__ void finish_first(const Args& p, Ring<kFmt>& ring, int& set, const float* reds, const Tables& tb, int a,
                                              int r0, int w, int lane, volatile int* abort_flag) {
     using G = Geo<kFmt>;
     const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin;
     const int steps = (p.H + G::kStepK - 1) / G::kStepK, tiles = (n_rows + 7) / 8;
+    int mine = 0;
     for (int n = 0; n < tiles; ++n, ++set) {
+        if (set % kEpiWarps != w) continue;
+        ++mine;
         const int q = set % G::kReds;
         const float* red = reds + q * G::kRed;
-        // FP8, FP4: 8 outputs of four columns at a time; BF16: 32 outputs of one column
-        constexpr int kCols = G::kBf16 ? 1 : 4;
-        const int j = G::kBf16 ? w * 32 + lane : w * 8 + (lane & 7);
+        // FP8, FP4: 16 outputs of two columns at a time; BF16: 64 of one, two a lane
+        constexpr int kCols = G::kBf16 ? 1 : 2, kEach = G::kBf16 ? 2 : 1;
         float inv[8 / kCols];
 #pragma unroll
         for (int i = 0; i < 8 / kCols; ++i) {
-            const int c = n * 8 + i * kCols + (G::kBf16 ? 0 : lane >> 3);
+            const int c = n * 8 + i * kCols + (G::kBf16 ? 0 : lane >> 4);
             inv[i] = !G::kBf16 && c < n_rows ? __ldcg(p.xinv + tb.token[tb.row[begin + c]]) : 1.0f;
         }
         mbar_wait(ring.red_full(q), (uint32_t)(set / G::kReds) & 1u, p.hdr, abort_flag);
 #pragma unroll
         for (int i = 0; i < 8 / kCols; ++i) {
-            const int cc = i * kCols + (G::kBf16 ? 0 : lane >> 3), c = n * 8 + cc;
-            const float g = red_sum<kFmt>(red, ring.it, steps, cc, j) * inv[i];
-            const float u = red_sum<kFmt>(red, ring.it, steps, cc, G::kOut1 + j) * inv[i];
-            const float v = swiglu1(g, u, p.clamp);
+            const int cc = i * kCols + (G::kBf16 ? 0 : lane >> 4), c = n * 8 + cc;
             if (c < n_rows) {
                 const int slot = tb.row[begin + c];
-                p.act[(int64_t)slot * p.I + r0 + j] = v;
-                if constexpr (!G::kBf16) {
-                    uint32_t top = __float_as_uint(v) & 0x7fffffffu;
-                    const uint32_t eight = 0xffu << (lane & 24);
-                    top = __reduce_max_sync(eight, top);
-                    if ((lane & 7) == 0) atomicMax(p.amax + slot, top);
+#pragma unroll
+                for (int h = 0; h < kEach; ++h) {
+                    const int j = G::kBf16 ? h * 32 + lane : lane & 15;
+                    const float g = red_sum<kFmt>(red, ring.it, steps, cc, j) * inv[i];
+                    const float u = red_sum<kFmt>(red, ring.it, steps, cc, G::kOut1 + j) * inv[i];
+                    const float v = swiglu1(g, u, p.clamp);
+                    p.act[(int64_t)slot * p.I + r0 + j] = v;
+                    if constexpr (!G::kBf16) {
+                        const uint32_t top = __reduce_max_sync(0xffffu << (lane & 16), __float_as_uint(v) & 0x7fffffffu);
+                        if ((lane & 15) == 0) atomicMax(p.amax + slot, top);
+                    }
                 }
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(ring.red_empty(q));
     }
-    if (lane == 0) {
+    if (mine && lane == 0) {
         __threadfence();
-        atomicAdd(p.dep + a, 1);
+        atomicAdd(p.dep + a, mine);
     }
     ring.it += steps;
 }
 
-// Epilogue warp w of an item of the second product: half of its hidden columns, added to the CTA's sums of these columns.
+// The tokens' sums over their slots of one column group (a warp): weights times the parts of K, in order, to bf16. Eight loads in
+// flight: this is what the last units of a launch wait for.
 template <int kFmt>
-__device__ __forceinline__ void finish_second(const Args& p, Ring<kFmt>& ring, int& set, const float* reds, const Tables& tb, float* y,
-                                              int a, int steps, int w, int lane, volatile int* abort_flag) {
+__device__ __forceinline__ void combine(const Args& p, const Tables& tb, int group, int lane) {
     using G = Geo<kFmt>;
-    const int begin = tb.start[a], n_rows = tb.start[a + 1] - begin, tiles = (n_rows + 7) / 8;
+    constexpr int kPerToken = G::kRows / 4, kBatch = 8;  // lanes of a token: four columns each
+    const int Kt = p.K + p.S, n = Kt * p.splits;
+    const int64_t part = (int64_t)p.T * Kt * p.H;
+    for (int t = lane / kPerToken; t < p.T; t += 32 / kPerToken) {
+        const int64_t at = (int64_t)group * G::kRows + lane % kPerToken * 4;
+        const float* row = p.comb + (int64_t)t * Kt * p.H + at;
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        int k = 0, q = 0;  // slot and part of the next load
+        for (int j = 0; j < n; j += kBatch) {
+            float4 v[kBatch];
+            float w[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int slot = t * Kt + k;
+                const bool on = j + i < n && tb.id[min(slot, kMaxSlots - 1)] >= 0;
+                w[i] = on ? tb.weight[slot] : 0.0f;
+                v[i] = on ? __ldcg(reinterpret_cast<const float4*>(row + (int64_t)k * p.H + q * part)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (++q == p.splits) {
+                    q = 0;
+                    ++k;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                y.x = fmaf(w[i], v[i].x, y.x), y.y = fmaf(w[i], v[i].y, y.y), y.z = fmaf(w[i], v[i].z, y.z), y.w = fmaf(w[i], v[i].w, y.w);
+        }
+        *reinterpret_cast<uint2*>(p.y + (int64_t)t * p.H + at) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    }
+}
+
+// A unit of the second product by epilogue warp w: the sums of its sets to the slots' rows in the workspace. The warp with the last
+// of a column group's `total` sets (all experts, all parts) adds the tokens' rows up.
+template <int kFmt>
+__device__ __forceinline__ void finish_second(const Args& p, Ring<kFmt>& ring, int& set, const float* reds, const Tables& tb,
+                                              const Unit& un, int total, int w, int lane, volatile int* abort_flag) {
+    using G = Geo<kFmt>;
+    const int begin = tb.start[un.a], n_rows = tb.start[un.a + 1] - begin, tiles = (n_rows + 7) / 8, steps = un.st1 - un.st0;
+    const int slots = p.T * (p.K + p.S);
+    float* out = p.comb + (int64_t)un.split * slots * p.H + (int64_t)un.group * G::kRows;
+    int mine = 0;
     for (int n = 0; n < tiles; ++n, ++set) {
+        if (set % kEpiWarps != w) continue;
+        ++mine;
         const int q = set % G::kReds;
         const float* red = reds + q * G::kRed;
-        // FP8, FP4: 16 hidden columns of two rows at a time; BF16: 64 of one row, two a lane
-        constexpr int kCols = G::kBf16 ? 1 : 2;
-        int slot[8 / kCols];
-#pragma unroll
-        for (int i = 0; i < 8 / kCols; ++i) {
-            const int c = n * 8 + i * kCols + (G::kBf16 ? 0 : lane >> 4);
-            slot[i] = c < n_rows ? tb.row[begin + c] : -1;
-        }
         mbar_wait(ring.red_full(q), (uint32_t)(set / G::kReds) & 1u, p.hdr, abort_flag);
 #pragma unroll
-        for (int i = 0; i < 8 / kCols; ++i) {
-            const int cc = i * kCols + (G::kBf16 ? 0 : lane >> 4);
-            if (slot[i] >= 0) {
-                const float weight = tb.weight[slot[i]], f = G::kBf16 ? 1.0f : red[G::kRed - 8 + cc];
+        for (int cc = 0; cc < 8; ++cc) {
+            const int c = n * 8 + cc;
+            if (c >= n_rows) break;
+            const float f = G::kBf16 || steps == 0 ? 1.0f : red[G::kRed - 8 + cc];
+            float* dst = out + (int64_t)tb.row[begin + c] * p.H;
 #pragma unroll
-                for (int h = 0; h < (G::kBf16 ? 2 : 1); ++h) {
-                    const int r = G::kBf16 ? w * 64 + h * 32 + lane : w * 16 + (lane & 15);
-                    float* dst = y + tb.token[slot[i]] * G::kRows + r;
-                    *dst = fmaf(red_sum<kFmt>(red, ring.it, steps, cc, r) * f, weight, *dst);
-                }
-            }
+            for (int h = 0; h < G::kRows / 32; ++h) dst[h * 32 + lane] = red_sum<kFmt>(red, ring.it, steps, cc, h * 32 + lane) * f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(ring.red_empty(q));
     }
     ring.it += steps;
-}
-
-// The CTA's sums of column group g are complete as far as its run goes (both epilogue warps): to y, or to the workspace where
-// other CTAs have experts of these columns too.
-template <int kFmt>
-__device__ void finish_columns(const Args& p, Tables& tb, float* y, const Work<kFmt>& wk, int g, int tid) {
-    using G = Geo<kFmt>;
-    constexpr int R = G::kRows;
-    const int first = g * wk.group(), end = first + wk.group(), n = p.T * R;
-    epilogue_sync();  // both warps' sums are in place
-    if (wk.lo2 <= first && wk.hi2 >= end) {
-        for (int i = tid; i < n; i += 32 * kEpiWarps) {
-            p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(y[i]);
-            y[i] = 0.0f;
-        }
-        epilogue_sync();
-        return;
-    }
-    // the CTAs with stages of these columns, in order; a CTA's first column group goes to its first buffer, its last to the second
-    if (tid < 32) {
-        int parts = 0;
-        for (int b = 0; b < wk.grid; b += 32) {
-            const int c = b + tid;
-            const int lo = c < wk.grid ? tb.first[c] : 0, hi = c < wk.grid ? tb.first[c + 1] : 0;
-            const bool in = max(lo, first) < min(hi, end);
-            const uint32_t all = __ballot_sync(0xffffffffu, in);
-            if (in) {
-                const int at = parts + __popc(all & ((1u << tid) - 1u)), buffer = 2 * c + (lo >= first ? 0 : 1);
-                tb.count[at] = buffer;
-                if (c == (int)blockIdx.x) tb.mine = buffer;
-            }
-            parts += __popc(all);
-        }
-        if (tid == 0) tb.last = parts;
-    }
-    epilogue_sync();
-    const int parts = tb.last;
-    auto buffer = [&](int b) { return p.part + (int64_t)b * kMaxT * R; };
-    float* mine = buffer(tb.mine);
-    for (int i = tid; i < n; i += 32 * kEpiWarps) {
-        mine[i] = y[i];
-        y[i] = 0.0f;
-    }
-    epilogue_sync();
-    if (tid == 0) {
+    if (!mine) return;
+    int done = 0;
+    if (lane == 0) {
         __threadfence();
-        // counts up to the last part and is zero again then
-        tb.last = atomicInc(reinterpret_cast<unsigned*>(p.cols) + g, (unsigned)(parts - 1)) == (unsigned)(parts - 1);
-        __threadfence();
+        done = atomicAdd(p.cols + un.group, mine) + mine;
     }
-    epilogue_sync();
-    if (tb.last)
-        for (int i = tid; i < n; i += 32 * kEpiWarps) {
-            float s = 0.0f;
-            for (int c = 0; c < parts; ++c) s += __ldcg(buffer(tb.count[c]) + i);
-            p.y[(int64_t)(i / R) * p.H + g * R + i % R] = float_to_bf16_bits(s);
-        }
-    epilogue_sync();
+    done = __shfl_sync(0xffffffffu, done, 0);
+    if (done == total) {
+        __threadfence();
+        combine<kFmt>(p, tb, un.group, lane);
+        if (lane == 0) p.cols[un.group] = 0;
+    }
 }
 
 // NT: column tiles that an expert can have (T <= 8 NT).
@@ -1037,7 +1025,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = smem_raw + (base - raw);
     Tables& tb = *reinterpret_cast<Tables*>(smem + G::kTabOff);
     float* reds = reinterpret_cast<float*>(smem + G::kRedOff);
-    float* y = reinterpret_cast<float*>(smem + G::kTabOff + ((sizeof(Tables) + 15) & ~size_t(15)));
     volatile int* abort_flag = &tb.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Ring<kFmt> ring;
@@ -1050,12 +1037,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < G::kReds; ++s) {
             mbar_init(ring.red_full(s), kWarps);
-            mbar_init(ring.red_empty(s), kEpiWarps);
+            mbar_init(ring.red_empty(s), 1);
         }
         tb.abort = 0;
+        tb.begun = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int i = threadIdx.x; i < p.T * G::kRows; i += kThreads) y[i] = 0.0f;
+    if (threadIdx.x < kQueue) tb.queue[threadIdx.x] = 0;
     __syncthreads();
 
     // ---- phase 1
@@ -1091,8 +1079,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_smem();
     __syncthreads();
     const Work<kFmt> wk(p, tb.n_active);
-    for (int c = threadIdx.x; c <= (int)gridDim.x; c += kThreads) tb.first[c] = wk.first(c);
-    __syncthreads();
 
     // ---- phases 3 and 4
     if (warp >= kWarps) {
@@ -1100,24 +1086,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kWarps) {
             if (lane < kProducers) produce<kFmt>(p, &map1, &map2, ring, tb, wk, lane, abort_flag);
         } else if (warp <= kWarps + kEpiWarps) {
+            // the sets alternate between the two warps: each has the time of two for a unit's fence and counter
             const int w = warp - kWarps - 1;
-            int set = 0;
-            for (Items<kFmt, false> item(wk); item.valid(wk); item.next(wk))
-                finish_first<kFmt>(p, ring, set, reds, tb, item.a, item.r0(), w, lane, abort_flag);
-            for (Items<kFmt, true> item(wk); item.valid(wk);) {
-                finish_second<kFmt>(p, ring, set, reds, tb, y, item.a, item.st1(wk) - item.st0, w, lane, abort_flag);
-                const int g = item.group;
-                item.next(wk);
-                if (item.group != g || !item.valid(wk)) finish_columns<kFmt>(p, tb, y, wk, g, w * 32 + lane);
+            int total = 0;  // sets of a column group of the second product
+            for (int a = lane; a < tb.n_active; a += 32) total += (tb.start[a + 1] - tb.start[a] + 7) / 8;
+            total = (int)__reduce_add_sync(0xffffffffu, (uint32_t)total) * p.splits;
+            int set = 0, k = 0;
+            uint32_t u = take(tb, 0, p.hdr, abort_flag);
+            for (; u < wk.n1; u = take(tb, ++k, p.hdr, abort_flag)) {
+                const Unit un = unit_first(wk, u);
+                finish_first<kFmt>(p, ring, set, reds, tb, un.a, un.group * G::kOut1, w, lane, abort_flag);
             }
+            for (; u != kNoUnit; u = take(tb, ++k, p.hdr, abort_flag))
+                finish_second<kFmt>(p, ring, set, reds, tb, unit_second(wk, u), total, w, lane, abort_flag);
+        } else if (lane == 0) {
+            fetch<kFmt>(p, tb, wk, abort_flag);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
-        int set = 0;
-        consume<kFmt, false, NT>(p, ring, set, reds, tb, wk, warp, lane, abort_flag);
-        consume<kFmt, true, NT>(p, ring, set, reds, tb, wk, warp, lane, abort_flag);
+        int set = 0, k = 0;
+        uint32_t u = take(tb, 0, p.hdr, abort_flag);
+        consume<kFmt, false, NT>(p, ring, set, k, u, reds, tb, wk, warp, lane, abort_flag);
+        consume<kFmt, true, NT>(p, ring, set, k, u, reds, tb, wk, warp, lane, abort_flag);
     }
-    if (wk.n_active == 0)
+    if (tb.n_active == 0)
         for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (int64_t)p.T * p.H; i += (int64_t)gridDim.x * kThreads)
             p.y[i] = 0;
 
@@ -1131,24 +1123,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tb.last) {
         for (int i = threadIdx.x; i < tb.n_active; i += kThreads) p.dep[i] = 0;
         for (int i = threadIdx.x; i < p.T * (p.K + p.S); i += kThreads) p.amax[i] = 0u;
-        if (threadIdx.x == 0) p.hdr[1] = 0;
+        if (threadIdx.x == 0) p.hdr[1] = p.hdr[3] = 0;
     }
 }
 
 size_t align_up(size_t v) { return (v + 255) & ~size_t(255); }
 
 template <int kFmt>
-constexpr size_t smem_bytes(int T) {
-    return 1024 + (size_t)Geo<kFmt>::kTabOff + ((sizeof(Tables) + 15) & ~size_t(15)) + (size_t)T * Geo<kFmt>::kRows * 4;
+constexpr size_t smem_bytes() {
+    return 1024 + (size_t)Geo<kFmt>::kTabOff + sizeof(Tables);
 }
 
 template <int kFmt, int NT>
 cudaError_t launch_tiles(const Args& p, cudaStream_t s) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
-    static_assert(smem_bytes<kFmt>(kMaxT) <= 232448, "shared memory");
+    static_assert(smem_bytes<kFmt>() <= 232448, "shared memory");
     std::call_once(once, [] {
-        err = cudaFuncSetAttribute(layer_kernel<kFmt, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<kFmt>(kMaxT));
+        err = cudaFuncSetAttribute(layer_kernel<kFmt, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<kFmt>());
         if (err == cudaSuccess) err = check_register_split(reinterpret_cast<const void*>(layer_kernel<kFmt, NT>), kLaunchRegs);
     });
     if (err != cudaSuccess) return err;
@@ -1175,7 +1167,7 @@ cudaError_t launch_tiles(const Args& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tc_num_sms());
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<kFmt>(p.T);
+    cfg.dynamicSmemBytes = smem_bytes<kFmt>();
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another: all of them are resident
@@ -1195,9 +1187,18 @@ cudaError_t launch_fmt(const Args& p, cudaStream_t s) {
 
 }  // namespace
 
+// Parts of K of the second product's units: as many as give every SM a dozen units where few experts have rows (they are handed
+// out one by one, so a unit is what the SMs can be apart at the end), of at least four stages each.
+static int layer_splits(const moe_dims& d, int weights) {
+    const int64_t columns = d.hidden / (weights == MOE_LAYER_BF16 ? 128 : 32);
+    const int64_t experts = std::min<int64_t>(d.num_experts, (int64_t)d.num_tokens * d.topk) + d.num_shared_experts;
+    const int64_t step = weights == MOE_LAYER_BF16 ? 64 : weights == MOE_LAYER_FP8_BLOCK ? 256 : 512;
+    const int64_t want = (12 * 152 + columns * experts - 1) / (columns * experts), most = std::max<int64_t>(1, d.intermediate / step / 4);
+    return (int)std::min<int64_t>(std::min(want, most), 16);
+}
+
 LayerLayout layer_layout(const moe_dims& d, int weights) {
     const size_t T = d.num_tokens, R = T * (d.topk + d.num_shared_experts);
-    const size_t rows = weights == MOE_LAYER_BF16 ? 128 : 32;
     LayerLayout L = {};
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -1216,7 +1217,7 @@ LayerLayout layer_layout(const moe_dims& d, int weights) {
     L.x16 = take(2 * T * d.hidden);
     L.xinv = take(sizeof(float) * T);
     L.act = take(sizeof(float) * R * d.intermediate);
-    L.part = take(sizeof(float) * 2 * kMaxT * rows * kMaxSms);
+    L.comb = take(sizeof(float) * R * d.hidden * (T ? layer_splits(d, weights) : 1));
     L.total = off;
     return L;
 }
@@ -1224,8 +1225,6 @@ LayerLayout layer_layout(const moe_dims& d, int weights) {
 cudaError_t launch_layer(const moe_layer_args& a, const moe_gate_options& gate, const moe_dims& d, void* workspace,
                          cudaStream_t s) {
     if (d.num_tokens == 0) return cudaSuccess;
-    const int sms = tc_num_sms();
-    if (sms > kMaxSms) return cudaErrorInvalidValue;
     const LayerLayout L = layer_layout(d, a.weights);
     uint8_t* b = static_cast<uint8_t*>(workspace);
     Args p = {};
@@ -1258,7 +1257,8 @@ cudaError_t launch_layer(const moe_layer_args& a, const moe_gate_options& gate, 
     p.x16 = reinterpret_cast<uint16_t*>(b + L.x16);
     p.xinv = reinterpret_cast<float*>(b + L.xinv);
     p.act = reinterpret_cast<float*>(b + L.act);
-    p.part = reinterpret_cast<float*>(b + L.part);
+    p.comb = reinterpret_cast<float*>(b + L.comb);
+    p.splits = layer_splits(d, a.weights);
     switch (a.weights) {
         case MOE_LAYER_BF16: return launch_fmt<MOE_LAYER_BF16>(p, s);
         case MOE_LAYER_FP8_BLOCK: return launch_fmt<MOE_LAYER_FP8_BLOCK>(p, s);

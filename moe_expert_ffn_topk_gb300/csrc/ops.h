@@ -40,10 +40,9 @@ cudaError_t launch_fp8_quantize(const void* x, int type, int64_t rows, int64_t c
 size_t fp8_matmul_workspace(int64_t M, int64_t N, int64_t K, int groups);
 cudaError_t launch_fp8_matmul(const moe_fp8_matmul_args& a, void* workspace, cudaStream_t s);
 
-// Byte offsets of moe_layer's workspace; kMaxSms bounds the CTAs of its launch.
-constexpr int kMaxSms = 192;
+// Byte offsets of moe_layer's workspace.
 struct LayerLayout {
-    size_t header, dep, cols, amax, logits, ids, weights, x16, xinv, act, part, total;
+    size_t header, dep, cols, amax, logits, ids, weights, x16, xinv, act, comb, total;
 };
 LayerLayout layer_layout(const moe_dims& d, int weights);
 cudaError_t launch_layer(const moe_layer_args& a, const moe_gate_options& gate, const moe_dims& d, void* workspace,
