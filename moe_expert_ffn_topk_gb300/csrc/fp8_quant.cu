@@ -5,8 +5,11 @@
 // power of two it is an exact product, and by other scales it is Markstein's: with r = 1/s rounded to nearest, q = x r and
 // q + r (x - q s) with fused multiply-adds is x / s rounded to nearest, wherever nothing over- or underflows (scales outside
 // 2^-60 .. 2^60 take the division itself).
+#include <algorithm>
+
 #include "common.cuh"
 #include "ops.h"
+#include "tc_common.cuh"
 
 namespace moe {
 
@@ -37,17 +40,32 @@ __global__ void __launch_bounds__(kThreads)
                     float* __restrict__ scale, Index blocks, Index units_per_row, Index units) {
     const int sub = threadIdx.x % kLanes;
     const Index first = (Index)blockIdx.x * (kThreads / 32) + threadIdx.x / 32, step = (Index)gridDim.x * (kThreads / 32);
-    for (Index u = first; u < units; u += step) {
-        const Index r = u / units_per_row, b = (u - r * units_per_row) * 4 + (threadIdx.x & 31) / kLanes;
-        const int64_t c0 = (int64_t)b * 128 + sub * kPer;
-        const int n = (int)max((int64_t)0, min((int64_t)kPer, cols - c0));
-        const T* src = x + (int64_t)r * x_stride + c0;
-        float v[kPer];
-        if (kVec && n == kPer) {
-            constexpr int kW = 16 / sizeof(T);
-            uint4 w[kPer / kW];
+    constexpr int kW = 16 / sizeof(T);
+    // where unit u's lane begins, and how many values it has there
+    Index r, b;
+    int64_t c0;
+    int n;
+    auto place = [&](Index u) {
+        r = u / units_per_row;
+        b = (u - r * units_per_row) * 4 + (threadIdx.x & 31) / kLanes;
+        c0 = (int64_t)b * 128 + sub * kPer;
+        n = u < units ? (int)max((int64_t)0, min((int64_t)kPer, cols - c0)) : 0;
+    };
+    uint4 w[kPer / kW];  // of a full lane: the next unit's values are on their way while one is worked on
+    auto load = [&]() {
+        const uint4* src = reinterpret_cast<const uint4*>(x + (int64_t)r * x_stride + c0);
 #pragma unroll
-            for (int j = 0; j < kPer / kW; ++j) w[j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
+        for (int j = 0; j < kPer / kW; ++j) w[j] = __ldg(src + j);
+    };
+    place(first);
+    if (kVec && n == kPer) load();
+    for (Index u = first; u < units; u += step) {
+        place(u);
+        const Index row = r, block = b;
+        const int64_t col = c0;
+        const int have = n;
+        float v[kPer];
+        if (kVec && have == kPer) {
 #pragma unroll
             for (int j = 0; j < kPer / kW; ++j) {
                 const T* e = reinterpret_cast<const T*>(&w[j]);
@@ -56,8 +74,10 @@ __global__ void __launch_bounds__(kThreads)
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] = j < n ? to_f32(src[j]) : 0.0f;
+            for (int j = 0; j < kPer; ++j) v[j] = j < have ? to_f32(x[(int64_t)row * x_stride + col + j]) : 0.0f;
         }
+        place(u + step);
+        if (kVec && n == kPer) load();
         // the largest magnitude as an integer: infinities and NaNs are above every number and survive
         uint32_t top = 0;
 #pragma unroll
@@ -68,29 +88,35 @@ __global__ void __launch_bounds__(kThreads)
         // the next power of two: any fraction bit carries into the exponent (not of an infinity or NaN)
         if (kPow2 && top < 0x7f800000u) s = __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u);
         if (s == 0.0f) s = 1.0f;
-        if (n == 0) continue;
-        if (sub == 0) scale[(int64_t)r * blocks + b] = s;
-        const bool plain = s > 8.6736174e-19f && s < 1.1529215e18f;  // 2^-60, 2^60
-        const float inv = __fdiv_rn(1.0f, s);
+        if (have == 0) continue;
+        if (sub == 0) scale[(int64_t)row * blocks + block] = s;
         uint32_t word[kPer / 4];
+        auto code = [&](auto quotient) {
 #pragma unroll
-        for (int j = 0; j < kPer; j += 4) {
-            float d[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float y = __fmul_rn(v[j + k], inv);
-                d[k] = kPow2 ? y : __fmaf_rn(__fmaf_rn(-y, s, v[j + k]), inv, y);
-                if (!plain) d[k] = __fdiv_rn(v[j + k], s);
+            for (int j = 0; j < kPer; j += 4)
+                word[j / 4] = e4m3x2(quotient(v[j]), quotient(v[j + 1])) | (e4m3x2(quotient(v[j + 2]), quotient(v[j + 3])) << 16);
+        };
+        if (s > 8.6736174e-19f && s < 1.1529215e18f) {  // 2^-60, 2^60
+            // (of a power of two: the exponent turned round)
+            const float inv = kPow2 ? __uint_as_float(0x7f000000u - __float_as_uint(s)) : __fdiv_rn(1.0f, s);
+            if constexpr (kPow2) {
+                code([&](float x) { return __fmul_rn(x, inv); });
+            } else {
+                code([&](float x) {
+                    const float y = __fmul_rn(x, inv);
+                    return __fmaf_rn(__fmaf_rn(-y, s, x), inv, y);
+                });
             }
-            word[j / 4] = e4m3x2(d[0], d[1]) | (e4m3x2(d[2], d[3]) << 16);
+        } else {
+            code([&](float x) { return __fdiv_rn(x, s); });
         }
-        uint8_t* dst = q + (int64_t)r * q_stride + c0;
-        if (kVec && n == kPer) {
+        uint8_t* dst = q + (int64_t)row * q_stride + col;
+        if (kVec && have == kPer) {
             *reinterpret_cast<uint4*>(dst) = make_uint4(word[0], word[1], word[2], word[3]);
         } else {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
-                if (j < n) dst[j] = (uint8_t)(word[j / 4] >> (8 * (j % 4)));
+                if (j < have) dst[j] = (uint8_t)(word[j / 4] >> (8 * (j % 4)));
         }
     }
 }
@@ -100,7 +126,7 @@ cudaError_t launch(const void* x, int64_t rows, int64_t cols, int64_t x_stride, 
                    cudaStream_t s) {
     const int64_t blocks = (cols + 127) / 128, per_row = (blocks + 3) / 4, units = rows * per_row;
     const int64_t ctas = (units + kThreads / 32 - 1) / (kThreads / 32);
-    const int grid = (int)(ctas < (1 << 20) ? ctas : (1 << 20));
+    const int grid = (int)std::min<int64_t>(ctas, (int64_t)tc_num_sms() * 5);  // what the SMs hold at a time
     const bool vec = !((reinterpret_cast<uintptr_t>(x) | (uint64_t)(x_stride * (int64_t)sizeof(T)) |
                         reinterpret_cast<uintptr_t>(q) | (uint64_t)q_stride) & 15);
     const T* xt = static_cast<const T*>(x);
