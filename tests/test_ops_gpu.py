@@ -579,3 +579,15 @@ def test_gate_feeds_the_routed_layer(moe):
     ref, bound = layer_reference(x, ids, weights, w1[2], w2[2], E, S)
     assert (y.double() - ref).abs().max() <= 2e-2 * ref.abs().max()
     assert ((ours.double() - ref).abs() <= bound).all()
+
+
+def test_example_runs_both_ways(moe):
+    """The example's decode and prefill ways agree up to the prefill way's FP8 rounding: x and the activations each lose
+    2^-4 a value at most, 2^-4/sqrt(3) in the mean of uniform errors: together below 2^-4 * sqrt(2/3) = 0.051."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "fp8_block_layer.py")
+    spec = importlib.util.spec_from_file_location("fp8_block_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.compare(example.Layer(1024, 512, 32, 4), 150) < 0.051
