@@ -16,12 +16,23 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-// s = 1 / (1 + e^-l) in fp32 with IEEE operations (the selection compares these values, so the fast exp and
-// divide of the activations are not used here)
-__device__ __forceinline__ float gate_sigmoid(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
+// s = 1 / (1 + e^-l) in fp32, rounded to nearest in the last step (the selection compares these values, so the fast exp and divide
+// of the activations are not used here). The reciprocal is an estimate and two Newton steps with fused multiply-adds, without the
+// branch of a division: a lane's scores then overlap (8 of them: 2450 cycles with divisions, one after another). Above 2^120 the
+// divisor is taken down by 2^64 and the result with it, as the steps would leave the range.
+__device__ __forceinline__ float gate_sigmoid(float l) {
+    const float x = __fadd_rn(1.0f, expf(-l));
+    const float scale = x >= 1.329228e36f ? 5.4210109e-20f : 1.0f, d = x * scale;  // 2^120, 2^-64
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    r = __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r);
+    r = __fmaf_rn(__fmaf_rn(-d, r, 1.0f), r, r);
+    return x <= 3.4028235e38f ? r * scale : x == x ? 0.0f : x;
+}
 
-// Floats of shared memory that gate_token works in, per warp: logits, bias, choice keys (a few words apart per group, see there).
-__host__ __device__ inline int gate_scratch(int E) { return 3 * E + 32; }
+// Floats of shared memory that gate_token works in, per warp: logits, bias, choice keys (a few words apart per group,
+// see there), selected ids.
+__host__ __device__ inline int gate_scratch(int E) { return 3 * E + 64; }
 
 // One token, by one warp. scratch: gate_scratch(E) words of shared memory of this warp, the first E holding the logits, the
 // next E the bias where there is one (this function separates its reads from their writes). Selected experts go to ids[0..K) and weights[0..K).
@@ -33,7 +44,7 @@ __device__ __forceinline__ void gate_token(float* scratch, bool has_bias, const 
     constexpr uint32_t kAll = 0xffffffffu;
     const float *logit = scratch, *bias = scratch + E;
     uint32_t* key = reinterpret_cast<uint32_t*>(scratch + 2 * E);
-    uint32_t* bias_key = reinterpret_cast<uint32_t*>(scratch + E);  // the bias is not needed once the keys are there
+    int* chosen = reinterpret_cast<int*>(scratch + 3 * E + 32);
     const bool softmax = o.score == MOE_SCORE_SOFTMAX;
     const bool groups = o.num_groups > 1;
     // group of expert e: (e + 0.5) / size truncated, exact for e < 1024; `per` lanes scan a group, and keys of a group are `per`
@@ -68,16 +79,29 @@ __device__ __forceinline__ void gate_token(float* scratch, bool has_bias, const 
     }
     auto score = [&](float l) { return softmax ? __fdiv_rn(exp_of(l), total) : gate_sigmoid(l); };
 
-    // choice keys: 0 = not available
-#pragma unroll 2
-    for (int e = lane; e < E; e += 32) {
-        float c = logit[e];
-        const bool on = c > -INFINITY;  // false for a NaN too
-        if (has_bias || !softmax) c = score(c);
-        if (has_bias) c += bias[e];
-        key[e + group_of(e) * pad] = on && c == c ? order_key(c) : 0u;
-    }
+    // choice keys: 0 = not available. A loop for each kind of score, four experts at a time and read before the first is
+    // written: their chains of some 250 cycles overlap.
+    auto make_keys = [&](auto value) {
+        for (int e = lane; e < E; e += 128) {
+            float l[4], c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                l[j] = e + 32 * j < E ? logit[e + 32 * j] : -INFINITY;
+                c[j] = has_bias && e + 32 * j < E ? bias[e + 32 * j] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] += value(l[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (e + 32 * j < E)  // not for a NaN either
+                    key[e + 32 * j + group_of(e + 32 * j) * pad] = l[j] > -INFINITY && c[j] == c[j] ? order_key(c[j]) : 0u;
+        }
+    };
+    if (!softmax) make_keys([](float l) { return gate_sigmoid(l); });
+    else if (has_bias) make_keys(score);
+    else make_keys([](float l) { return l; });
 
+    uint32_t kept = ~0u;  // bit g: the experts of group g are eligible
     if (groups) {
         __syncwarp();
         const int g = lane / per, sub = lane & (per - 1);
@@ -98,53 +122,57 @@ __device__ __forceinline__ void gate_token(float* scratch, bool has_bias, const 
         }
         // of a fully masked group too: -inf is a rank
         uint32_t rank = g < o.num_groups && sub == 0 ? order_key(o.group_top == 1 || size == 1 ? a : a + b) : 0u;
-        uint32_t kept = 0u;  // bit g: the experts of group g stay eligible
+        kept = 0u;
         for (int k = 0; k < o.topk_groups; ++k) {
             const uint32_t best = __reduce_max_sync(kAll, rank);
             const int win = __ffs(__ballot_sync(kAll, rank == best)) - 1;  // the lowest lane: the lowest group
             kept |= 1u << __shfl_sync(kAll, g, win);
             if (lane == win) rank = 0u;
         }
-        // the keys of the groups that stay, packed (a lane's own experts again; every lane is past its scan)
-#pragma unroll 4
-        for (int e = lane; e < E; e += 32) {
-            const int h = group_of(e);
-            const uint32_t k = key[e + h * pad];
-            bias_key[e] = (kept >> h) & 1u ? k : 0u;
-        }
-        key = bias_key;
     }
 
-    // K rounds of "largest key, lowest index"; lane k keeps the k-th. Each lane knows the best of its own experts.
-    uint32_t mine = 0;
-    int at = 0;
+    // K rounds of "largest key, lowest index"; lane k keeps the k-th. Each lane knows the best two of its own experts that are
+    // left, and looks for them again only when both have been taken.
+    uint32_t best1, best2;
+    int at1, at2;
     auto own_best = [&]() {
-        mine = 0;
-#pragma unroll 8
+        best1 = best2 = 0u;
+        at1 = at2 = 0;
+#pragma unroll 4
         for (int e = lane; e < E; e += 32) {
-            const uint32_t k = key[e];
-            if (k > mine) {
-                mine = k;
-                at = e;
+            const int h = groups ? group_of(e) : 0;
+            const uint32_t c = key[e + h * pad], k = (kept >> h) & 1u ? c : 0u;
+            if (k > best1) {
+                best2 = best1, at2 = at1;
+                best1 = k, at1 = e;
+            } else if (k > best2) {
+                best2 = k, at2 = e;
             }
         }
     };
     own_best();
-    int my_id = -1;
-    for (int k = 0; k < K; ++k) {
-        const uint32_t best = __reduce_max_sync(kAll, mine);
+    bool two = true;  // the second one is known
+    int found = 0;
+    for (; found < K; ++found) {
+        const uint32_t best = __reduce_max_sync(kAll, best1);
         if (best == 0u) break;
-        // one lane has it, or more (equal values): the lowest index among them
-        const uint32_t with = __ballot_sync(kAll, mine == best);
-        const int e = with & (with - 1u) ? (int)__reduce_min_sync(kAll, mine == best ? (uint32_t)at : 0xffffffffu)
-                                         : __shfl_sync(kAll, at, __ffs(with) - 1);
-        if (lane == k) my_id = e;
-        if (lane == (e & 31)) {
-            key[e] = 0u;
-            own_best();
+        // one lane has it, or more (equal values): the one with the lowest index
+        const uint32_t with = __ballot_sync(kAll, best1 == best);
+        bool mine = best1 == best;
+        if (with & (with - 1u)) mine = __reduce_min_sync(kAll, mine ? (uint32_t)at1 : 0xffffffffu) == (uint32_t)at1 && mine;
+        if (mine) {
+            chosen[found] = at1;
+            key[at1 + (groups ? group_of(at1) : 0) * pad] = 0u;
+            if (two) {
+                best1 = best2, at1 = at2;
+            } else {
+                own_best();
+            }
+            two = !two;
         }
         __syncwarp();
     }
+    const int my_id = lane < found ? chosen[lane] : -1;
     float w = my_id >= 0 ? score(logit[my_id]) : 0.0f;
     if (o.normalize) {
         float sum = w;
