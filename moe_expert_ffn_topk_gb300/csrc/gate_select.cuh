@@ -38,7 +38,8 @@ __host__ __device__ inline int gate_scratch(int E) { return 3 * E + 64; }
 // next E the bias where there is one (this function separates its reads from their writes). Selected experts go to ids[0..K) and weights[0..K).
 //
 // Rows stay in shared memory, not in registers, and every loop is kept rolled: few tokens run this once, and then what counts
-// is how much code has to be fetched (with the row in registers and everything unrolled: twice the time for 7 tokens).
+// is how much code has to be fetched (7 tokens, 256 experts, on the device: 6.9 us with the row in registers and everything
+// unrolled, 6.3 when first rolled, 5.1 now).
 __device__ __forceinline__ void gate_token(float* scratch, bool has_bias, const moe_gate_options& o, int E, int K, int lane,
                                            int32_t* ids, float* weights) {
     constexpr uint32_t kAll = 0xffffffffu;

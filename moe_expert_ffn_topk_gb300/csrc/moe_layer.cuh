@@ -32,10 +32,12 @@
 // FP8 weight scale multiplies the fp32 sum over each 64 of K; the UE8M0 scales of FP4 multiply the f16 codes relative to the
 // largest of the four blocks that a stage's sum covers (exact while they lie within 2^20 of it) and that one the fp32 sum.
 //
-// Bound by HBM where the experts' weights are many: 32 tokens, top-8 of 256 experts and a shared one, hidden 7168, intermediate
-// 2048, FP8: 7.24 GB in 1.10 ms, 0.99 of the measured copy rate. 3 tokens, top-2 of 8 experts, 4096 / 14336, BF16: 1.63 GB in 278 us,
-// 0.88. One token of the first: 400 MB in 84 us, 0.72 (13 us are the router and the selection, whose barriers and latencies no
-// weights hide). 5 tokens, top-6 of 64, 2048 / 768, FP4: 63 MB in 55 us, latency all over.
+// Bound by HBM where a call reads much of few experts. Fractions are of the measured copy rate and count the weights of the experts
+// that the routes in fact touched. 3 tokens, top-2 of 8 experts, 4096 / 14336, BF16: 1.41 GB (4 experts) in 228 us, 0.93; 1.76 GB (5)
+// in 274, 0.96; 2.11 GB (6) in 320, 0.99. 32 tokens, top-8 of 256 experts in the best 4 of 8 groups and a shared one, hidden 7168,
+// intermediate 2048, FP8: 6.08 GB (138 experts) in 1.11-1.12 ms, 0.81. One token of the same: 397 MB (9) in 82 us, 0.72 (13 us are
+// the router and the selection, whose barriers and latencies no weights hide). 5 tokens, top-6 of 64, 2048 / 768, FP4: 58 MB (23) in
+// 53-54 us, latency all over.
 //
 // Every wait is bounded (2 s): MOE_ERR_TIMEOUT; from then on the CTA skips its waits and its work, and still passes its barriers.
 #pragma once
