@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "layer_parts.h"
 #include "moe_layer.cuh"
 
 namespace moe {
@@ -18,16 +19,6 @@ namespace {
 size_t align_up(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace
-
-// Parts of K of the second product's units: as many as give every SM a dozen units where few experts have rows (they are handed
-// out one by one, so a unit is what the SMs can be apart at the end), of at least four stages each.
-static int layer_splits(const moe_dims& d, int weights) {
-    const int64_t columns = d.hidden / (weights == MOE_LAYER_BF16 ? 128 : 32);
-    const int64_t experts = std::min<int64_t>(d.num_experts, (int64_t)d.num_tokens * d.topk) + d.num_shared_experts;
-    const int64_t step = weights == MOE_LAYER_BF16 ? 64 : weights == MOE_LAYER_FP8_BLOCK ? 256 : 512;
-    const int64_t want = (12 * 152 + columns * experts - 1) / (columns * experts), most = std::max<int64_t>(1, d.intermediate / step / 4);
-    return (int)std::min<int64_t>(std::min(want, most), 16);
-}
 
 LayerLayout layer_layout(const moe_dims& d, int weights) {
     const size_t T = d.num_tokens, R = T * (d.topk + d.num_shared_experts);
@@ -49,7 +40,7 @@ LayerLayout layer_layout(const moe_dims& d, int weights) {
     L.x16 = take(2 * T * d.hidden);
     L.xinv = take(sizeof(float) * T);
     L.act = take(sizeof(float) * R * d.intermediate);
-    L.comb = take(sizeof(float) * R * d.hidden * (T ? layer_splits(d, weights) : 1));
+    L.comb = take(sizeof(float) * R * d.hidden * layer_parts(d, weights));
     L.total = off;
     return L;
 }
@@ -90,7 +81,7 @@ cudaError_t launch_layer(const moe_layer_args& a, const moe_gate_options& gate, 
     p.xinv = reinterpret_cast<float*>(b + L.xinv);
     p.act = reinterpret_cast<float*>(b + L.act);
     p.comb = reinterpret_cast<float*>(b + L.comb);
-    p.splits = layer_splits(d, a.weights);
+    p.splits = layer_parts(d, a.weights);
     switch (a.weights) {
         case MOE_LAYER_BF16: return layer::launch_fmt<MOE_LAYER_BF16>(p, s);
         case MOE_LAYER_FP8_BLOCK: return layer::launch_fmt<MOE_LAYER_FP8_BLOCK>(p, s);

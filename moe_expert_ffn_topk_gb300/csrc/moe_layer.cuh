@@ -51,6 +51,7 @@
 
 #include "common.cuh"
 #include "gate_select.cuh"
+#include "layer_parts.h"
 #include "ops.h"
 #include "tc_common.cuh"
 
@@ -100,7 +101,15 @@ struct Geo {
 };
 
 constexpr int kMaxBars = 48;
-constexpr int kQueue = 64;                      // units between the fetching warp and the slowest reader: at most some 24
+constexpr int kProducers = 4;                   // producer lanes, each on every fourth stage of the CTA's sequence
+// Units are published up to kLead past the one that the producer's first lane is in. Its lanes go on together, from one stage each to
+// the next, and a unit has at least one stage: the last lane needs the unit kProducers - 1 further at most, which is there without
+// the first lane's help (with units of no stage it would wait for the first lane, and that for it).
+constexpr int kLead = 3;
+static_assert(kLead >= kProducers - 1, "units in reach of every producer lane");
+// Units between the fetching warp and the slowest reader: kLead, one a stage of the ring (16) and one a set of partial sums (4, a unit
+// has at least one) at most, and the ones being worked on.
+constexpr int kQueue = 64;
 constexpr uint32_t kNoUnit = 0xffffffffu;
 
 struct Tables {
@@ -130,7 +139,7 @@ struct Args {
     int router_bf16;
     int T, H, I, E, K, S;
     float clamp;
-    int splits;        // parts of K that a column group of an expert is cut into in the second product
+    int splits;        // parts of K that a column group of an expert is cut into in the second product (layer_parts)
     int32_t* hdr;      // [0] error word, [1] barrier, [2] CTAs finished, [3] units handed out
     int32_t* dep;      // per active expert: finished column tiles of its units of the first product
     int32_t* cols;     // per column group: finished column tiles of the second product
@@ -456,7 +465,7 @@ struct Work {
         total = n1 + per2 * active;
         steps1 = (p.H + G::kStepK - 1) / G::kStepK;
         steps2 = (p.I + G::kStepK - 1) / G::kStepK;
-        split_steps = (steps2 + p.splits - 1) / p.splits;
+        split_steps = part_steps(steps2, p.splits);
     }
 };
 
@@ -472,8 +481,7 @@ template <int kFmt>
 __device__ __forceinline__ Unit unit_second(const Work<kFmt>& wk, uint32_t u) {
     u -= wk.n1;
     const uint32_t a = u / wk.per2, r = u - a * wk.per2, g = r / wk.splits, q = r - g * wk.splits;
-    // (parts of whole stages: the last ones may be empty)
-    const int st0 = min(wk.steps2, (int)q * wk.split_steps);
+    const int st0 = (int)q * wk.split_steps;
     return {(int)a, (int)g, (int)q, st0, min(wk.steps2, st0 + wk.split_steps)};
 }
 
@@ -498,7 +506,6 @@ __device__ __forceinline__ uint32_t take(const Tables& tb, int k, int32_t* hdr, 
 // One lane: gets the CTA's units from the launch's counter, a few ahead of the producer, until they run out.
 template <int kFmt>
 __device__ __forceinline__ void fetch(const Args& p, Tables& tb, const Work<kFmt>& wk, volatile int* abort_flag) {
-    constexpr int kLead = 3;
     uint32_t u = blockIdx.x;  // the first one is given
     for (int k = 0;; ++k) {
         if (k > 0) {
@@ -533,8 +540,6 @@ struct Ring {
 
 // The producer warp: four lanes take every fourth stage of the CTA's sequence each, so that the latencies of a stage's wait and
 // of its barrier's byte count (some 150 cycles each) are those of four stages.
-constexpr int kProducers = 4;
-
 template <int kFmt>
 __device__ __forceinline__ void produce(const Args& p, const CUtensorMap* map1, const CUtensorMap* map2, const Ring<kFmt>& ring,
                                         Tables& tb, const Work<kFmt>& wk, int lane, volatile int* abort_flag) {
@@ -1000,7 +1005,7 @@ __device__ __forceinline__ void finish_second(const Args& p, Ring<kFmt>& ring, i
         for (int cc = 0; cc < 8; ++cc) {
             const int c = n * 8 + cc;
             if (c >= n_rows) break;
-            const float f = G::kBf16 || steps == 0 ? 1.0f : red[G::kRed - 8 + cc];
+            const float f = G::kBf16 ? 1.0f : red[G::kRed - 8 + cc];
             float* dst = out + (int64_t)tb.row[begin + c] * p.H;
 #pragma unroll
             for (int h = 0; h < G::kRows / 32; ++h) dst[h * 32 + lane] = red_sum<kFmt>(red, ring.it, steps, cc, h * 32 + lane) * f;
