@@ -39,7 +39,8 @@
 // the router and the selection, whose barriers and latencies no weights hide). 5 tokens, top-6 of 64, 2048 / 768, FP4: 58 MB (23) in
 // 53-54 us, latency all over.
 //
-// Every wait is bounded (2 s): MOE_ERR_TIMEOUT; from then on the CTA skips its waits and its work, and still passes its barriers.
+// Every wait is bounded (2 s): MOE_ERR_TIMEOUT. From then on the CTA's waits end at once, no slot of the ring is handed back for
+// another copy, its queue of units ends, and it passes the barriers that are left.
 #pragma once
 
 #include <cuda.h>
@@ -485,7 +486,9 @@ __device__ __forceinline__ Unit unit_second(const Work<kFmt>& wk, uint32_t u) {
     return {(int)a, (int)g, (int)q, st0, min(wk.steps2, st0 + wk.split_steps)};
 }
 
-// The CTA's k-th unit, kNoUnit after the last one (or when the wait ran out).
+// The CTA's k-th unit, kNoUnit after the last one. Every lane of every warp gets the same answer, also when the CTA gives up: an
+// entry is written once, and fetch ends the sequence within its own limit, so this one, four times as long, is not reached. (Looking
+// at the abort flag here let lanes part that have to stay together; a vote on the answer took 0.4 to 0.8 % of the layer's time.)
 __device__ __forceinline__ uint32_t take(const Tables& tb, int k, int32_t* hdr, volatile int* abort_flag) {
     const volatile uint64_t* q = tb.queue + k % kQueue;
     uint64_t v = *q;
@@ -494,8 +497,7 @@ __device__ __forceinline__ uint32_t take(const Tables& tb, int k, int32_t* hdr, 
     for (int i = 1;; ++i) {
         v = *q;
         if ((uint32_t)(v >> 32) == (uint32_t)k + 1u) return (uint32_t)v;
-        if (*abort_flag) return kNoUnit;
-        if (i % 256 == 0 && globaltimer_ns() - t0 > kWaitTimeoutNs) {
+        if (i % 256 == 0 && globaltimer_ns() - t0 > 4 * kWaitTimeoutNs) {
             record_error(hdr, MOE_ERR_TIMEOUT);
             *abort_flag = 1;
             return kNoUnit;
@@ -503,24 +505,29 @@ __device__ __forceinline__ uint32_t take(const Tables& tb, int k, int32_t* hdr, 
     }
 }
 
-// One lane: gets the CTA's units from the launch's counter, a few ahead of the producer, until they run out.
+// One lane: gets the CTA's units from the launch's counter, a few ahead of the producer, until they run out or the CTA gives up.
+// Either way the last entry says so.
 template <int kFmt>
 __device__ __forceinline__ void fetch(const Args& p, Tables& tb, const Work<kFmt>& wk, volatile int* abort_flag) {
     uint32_t u = blockIdx.x;  // the first one is given
     for (int k = 0;; ++k) {
+        bool end = u >= wk.total;
         if (k > 0) {
             const uint64_t t0 = globaltimer_ns();
             while (tb.begun + kLead < k) {
                 if (*abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs) {
                     if (!*abort_flag) record_error(p.hdr, MOE_ERR_TIMEOUT);
                     *abort_flag = 1;
-                    return;
+                    end = true;
+                    break;
                 }
                 __nanosleep(32);
             }
-            u = gridDim.x + (uint32_t)atomicAdd(p.hdr + 3, 1);
+            if (!end) {
+                u = gridDim.x + (uint32_t)atomicAdd(p.hdr + 3, 1);
+                end = u >= wk.total;
+            }
         }
-        const bool end = u >= wk.total;
         tb.queue[k % kQueue] = ((uint64_t)(k + 1) << 32) | (end ? kNoUnit : u);
         if (end) return;
     }
@@ -841,12 +848,15 @@ __device__ __forceinline__ void consume(const Args& p, Ring<kFmt>& ring, int& se
                         sc[j].load(p, scale, k0 + j * G::kSliceK);
                         if (j < kAhead) cols[j].load(col, k0 + j * G::kSliceK);
                     }
-                // a wait that ran out skips the stage: the set is still signed for
-                const bool ok = __all_sync(0xffffffffu, mbar_wait(ring.full(s), (uint32_t)(it / G::kStages) & 1u, p.hdr, abort_flag));
+                // a wait that ran out is the warp's last: the slot is not handed back, as the copy into it may still be under way
+                if (!__all_sync(0xffffffffu, mbar_wait(ring.full(s), (uint32_t)(it / G::kStages) & 1u, p.hdr, abort_flag))) {
+                    u = kNoUnit;
+                    return;
+                }
                 const uint32_t stage = ring.base + (uint32_t)(s * G::kStageBytes);
 #pragma unroll
                 for (int j = 0; j < kSlices; ++j) {
-                    if (ok && k0 + j * G::kSliceK < K)
+                    if (k0 + j * G::kSliceK < K)
                         multiply_slice<kFmt, kSecond, NT>(p, stage, j, k0 + j * G::kSliceK, cols[j % kAhead], sc[j], rows, ascale, tiles,
                                                           warp, lane, acc);
                     if (j + kAhead < kSlices && k0 + (j + kAhead) * G::kSliceK < K) cols[j % kAhead].load(col, k0 + (j + kAhead) * G::kSliceK);

@@ -33,3 +33,24 @@ def test_layer_whose_stages_do_not_divide_into_the_parts(moe, fmt, shape):
     for _ in range(40):
         again, status = run_layer(moe, x, router, w1, w2, d, fmt, ws)
         assert status == moe.MOE_OK and torch.equal(y, again)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8_block", "fp4_mx"])
+@pytest.mark.parametrize("T", [3, 12])
+def test_layer_that_gives_up_returns(moe, fmt, T):
+    """A grid barrier that never fills (its counter starts far below zero) runs into the wait's limit: the launch ends with
+    MOE_ERR_TIMEOUT, and the workspace serves again once it is zeroed."""
+    H, I, E, K, S = 512, 384, 8, 2, 1  # noqa: E741
+    g = gen(21)
+    d = moe.dims(T, H, I, E, K, S)
+    x, router = randn(g, T, H).to(torch.bfloat16), (randn(g, E, H) * H ** -0.5).to(torch.bfloat16)
+    w1, w2 = layer_weights(g, fmt, E + S, 2 * I, H), layer_weights(g, fmt, E + S, H, I)
+    want, status = run_layer(moe, x, router, w1, w2, d, fmt)
+    assert status == moe.MOE_OK
+    ws = moe.alloc_ops_workspace(moe.moe_layer_workspace_bytes(d, fmt))
+    ws[:256].view(torch.int32)[1] = -(1 << 24)  # CTAs at the barrier
+    _, status = run_layer(moe, x, router, w1, w2, d, fmt, ws)
+    assert status == moe.MOE_ERR_TIMEOUT
+    moe.moe_ops_workspace_init(ws)
+    y, status = run_layer(moe, x, router, w1, w2, d, fmt, ws)
+    assert status == moe.MOE_OK and torch.equal(y, want)
