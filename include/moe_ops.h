@@ -50,12 +50,15 @@ typedef struct {
  *   choice value   c[e] = s[e] + bias[e] with a bias, else l[e] for softmax scores (same order as s, undisturbed
  *                  by rounding) and s[e] for sigmoid ones.
  *   selection      the topk_groups groups of highest rank, then the K experts of highest c among theirs, highest
- *                  first; equal values (of groups and of experts) go to the lowest index.
+ *                  first; equal values (of groups and of experts) go to the lowest index. A group is ranked by the
+ *                  experts that are not masked: with fewer than group_top of them by their sum, with none below
+ *                  every other group.
  *   weight         s[id] of the chosen ones (without the bias), normalised and scaled as the options say.
- *   masked experts a logit of -inf, or a NaN, is never chosen. When fewer than K experts are left, the
- *                  remaining ids are -1 (moe_plan's masked route) and their weights 0. A finite logit, the
- *                  type's lowest value too, is a candidate like any other. A logit of +inf has s = 1 (softmax:
- *                  1 / the number of +inf logits of the row, and 0 for the finite ones).
+ *   masked experts a logit of -inf, or a NaN, is never chosen. When fewer than K experts are left in the groups that
+ *                  stay, the remaining ids are -1 (moe_plan's masked route) and their weights 0. A finite logit,
+ *                  the type's lowest value too, is a candidate like any other. A logit of +inf has s = 1 (softmax:
+ *                  1 / the number of +inf logits of the row, and 0 for the finite ones). A bias of NaN masks its
+ *                  expert too, one of -inf makes it the last candidate.
  *   logits         device [T,E] of `type`, row_stride >= E elements apart (T = d->num_tokens, E =
  *                  d->num_experts, K = d->topk; the other sizes in d are not read).
  *   bias           device fp32 [E] or NULL.      opt   NULL: softmax, one group, normalised, scale 1.

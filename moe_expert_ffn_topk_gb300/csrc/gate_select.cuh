@@ -106,24 +106,28 @@ __device__ __forceinline__ void gate_token(float* scratch, bool has_bias, const 
     if (groups) {
         __syncwarp();
         const int g = lane / per, sub = lane & (per - 1);
-        float a = -INFINITY, b = -INFINITY;  // the group's two largest, a >= b
+        uint32_t a = 0u, b = 0u;  // keys of the group's two largest, a >= b; 0: it has no such candidate
         if (g < o.num_groups) {
 #pragma unroll 4
             for (int j = sub; j < size; j += per) {
                 const uint32_t k = key[g * (size + pad) + j];
-                const float c = k ? key_value(k) : -INFINITY;
-                b = fmaxf(b, fminf(a, c));
-                a = fmaxf(a, c);
+                b = max(b, min(a, k));
+                a = max(a, k);
             }
         }
         for (int d = 1; d < per; d <<= 1) {
-            const float a2 = __shfl_xor_sync(kAll, a, d), b2 = __shfl_xor_sync(kAll, b, d);
-            b = fmaxf(fminf(a, a2), fmaxf(b, b2));
-            a = fmaxf(a, a2);
+            const uint32_t a2 = __shfl_xor_sync(kAll, a, d), b2 = __shfl_xor_sync(kAll, b, d);
+            b = max(min(a, a2), max(b, b2));
+            a = max(a, a2);
         }
-        // of a fully masked group too: -inf is a rank
-        uint32_t rank = g < o.num_groups && sub == 0 ? order_key(o.group_top == 1 || size == 1 ? a : a + b) : 0u;
-        kept = 0u;
+        // the sum over the candidates there are; 0, below the rank of any group with one, without (+inf is a rank of its own: what
+        // the second adds to it does not count)
+        uint32_t rank = 0u;
+        if (a != 0u && sub == 0) {
+            const float first = key_value(a);
+            rank = order_key(o.group_top == 2 && b != 0u && first < INFINITY ? first + key_value(b) : first);
+        }
+        kept = 0u;  // (a bit more does no harm where only groups without a candidate are left)
         for (int k = 0; k < o.topk_groups; ++k) {
             const uint32_t best = __reduce_max_sync(kAll, rank);
             const int win = __ffs(__ballot_sync(kAll, rank == best)) - 1;  // the lowest lane: the lowest group

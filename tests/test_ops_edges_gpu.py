@@ -54,3 +54,59 @@ def test_layer_that_gives_up_returns(moe, fmt, T):
     moe.moe_ops_workspace_init(ws)
     y, status = run_layer(moe, x, router, w1, w2, d, fmt, ws)
     assert status == moe.MOE_OK and torch.equal(y, want)
+
+
+def gate_by_definition(rows, K, groups, kept, top):
+    """ids from choice values (exact in 32 bits, sums of two as well; -inf and NaN: masked), the groups ranked by what is not masked
+    in them."""
+    ids = []
+    for row in rows:
+        on = [v == v and v != float("-inf") for v in row]
+        n = len(row) // groups
+        rank = []
+        for i in range(groups):
+            there = sorted(v for v, o in zip(row[i * n:(i + 1) * n], on[i * n:(i + 1) * n]) if o)
+            rank.append((bool(there), sum(there[-top:])))
+        stay = sorted(range(groups), key=lambda i: (-rank[i][0], -rank[i][1], i))[:kept]
+        got = sorted((i for i, o in enumerate(on) if o and i // n in stay), key=lambda i: (-row[i], i))[:K]
+        ids.append(got + [-1] * (K - len(got)))
+    return ids
+
+
+def gate_ids(moe, logits, K, **opt):
+    T, E = logits.shape
+    ids, w = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
+    moe.moe_gate(logits, moe.dims(T, 128, 128, E, K), ids, w, options=moe.gate_options(**opt))
+    return ids, w
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_ranks_a_group_by_the_experts_it_has(moe, score):
+    inf = float("inf")
+    # group 0 masked, one expert left in group 1
+    logits = torch.full((1, 8), -inf, device="cuda")
+    logits[0, 6] = -2.0
+    ids, w = gate_ids(moe, logits, 2, score=score, groups=2, topk_groups=1, group_top=2)
+    assert ids.tolist() == [[6, -1]] and w[0, 0] == 1.0 and w[0, 1] == 0.0
+    # a NaN masks as -inf does; the sum of one counts against the sum of two (softmax ranks by the logits, sigmoid by scores above 0)
+    logits = torch.tensor([[float("nan"), 4.0, -inf, -inf, 1.0, 2.0, -inf, float("nan")]], device="cuda")
+    ids, _ = gate_ids(moe, logits, 2, score=score, groups=4, topk_groups=1, group_top=2)
+    assert ids.tolist() == ([[1, -1]] if score == "softmax" else [[5, 4]])
+    # +inf alone is the highest rank, also beside a masked one
+    logits = torch.tensor([[3.0, 3.0, -inf, -inf, -inf, inf, 1.0, 1.0]], device="cuda")
+    if score == "softmax":
+        ids, _ = gate_ids(moe, logits, 2, score=score, groups=4, topk_groups=1, group_top=2)
+        assert ids.tolist() == [[5, -1]]
+
+
+@pytest.mark.parametrize("groups,kept,top", [(2, 1, 2), (4, 1, 2), (8, 4, 2), (8, 3, 1), (3, 2, 2), (32, 8, 2), (16, 16, 2)])
+@pytest.mark.parametrize("left", [0.02, 0.1, 0.5])
+def test_gate_groups_with_random_masks(moe, groups, kept, top, left):
+    g = gen(groups + kept)
+    E, K, T = groups * 8, 5, 60
+    logits = torch.randint(-64, 64, (T, E), generator=g, device="cuda") / 8.0
+    logits[torch.rand((T, E), generator=g, device="cuda") > left] = float("-inf")
+    logits[:, 3] = torch.where(torch.rand(T, generator=g, device="cuda") < 0.5, float("nan"), logits[:, 3])
+    ids, w = gate_ids(moe, logits, K, groups=groups, topk_groups=kept, group_top=top)
+    assert ids.tolist() == gate_by_definition(logits.tolist(), K, groups, kept, top)
+    assert ((ids < 0) == (w == 0)).all()
