@@ -3,7 +3,7 @@
 // One pass: 8 lanes hold a block of 128 columns, 16 values each, so the block's amax is three shuffles and x is read
 // once. Bound by HBM: 2 (bf16) or 4 (fp32) bytes read and 1 written an element. That takes the division out of the way: by a
 // power of two it is an exact product, and by other scales it is Markstein's: with r = 1/s rounded to nearest, q = x r and
-// q + r (x - q s) with fused multiply-adds is x / s rounded to nearest, wherever nothing over- or underflows (scales outside
+// q - r (q s - x) with fused multiply-adds is x / s rounded to nearest, wherever nothing over- or underflows (scales outside
 // 2^-60 .. 2^60 take the division itself). 8192 x 7168 bf16 to power-of-two scales: 31.8 us, 0.84 of the
 // copy rate (51 us with a division a value, 41 before the resident grid with the next unit's loads in flight).
 #include <algorithm>
@@ -103,9 +103,11 @@ __global__ void __launch_bounds__(kThreads)
             if constexpr (kPow2) {
                 code([&](float x) { return __fmul_rn(x, inv); });
             } else {
+                // the residual with the other sign: that of a zero x is +0, and -inv times it -0, which leaves y's own sign (with
+                // x - y s and inv, -0 came out as +0)
                 code([&](float x) {
                     const float y = __fmul_rn(x, inv);
-                    return __fmaf_rn(__fmaf_rn(-y, s, x), inv, y);
+                    return __fmaf_rn(__fmaf_rn(y, s, -x), -inv, y);
                 });
             }
         } else {

@@ -110,3 +110,24 @@ def test_gate_groups_with_random_masks(moe, groups, kept, top, left):
     ids, w = gate_ids(moe, logits, K, groups=groups, topk_groups=kept, group_top=top)
     assert ids.tolist() == gate_by_definition(logits.tolist(), K, groups, kept, top)
     assert ((ids < 0) == (w == 0)).all()
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [128, 200, 512])
+def test_quantize_keeps_the_sign_of_a_zero(moe, cols, dtype, pow2):
+    g = gen(cols)
+    x = randn(g, 9, cols)
+    x[:, ::3] = -0.0
+    x[:, 1::3] = 0.0
+    x[1] = -0.0                 # a block of zeros alone: scale 1
+    x[2] *= 1e25                # scales outside the range of the exact quotient's short way
+    x[3] *= 1e-25
+    x[4, 2] = 1e30              # the rest of the block far below a code's smallest value, either sign
+    x = x.to(dtype)
+    q, scale = torch.empty((9, cols), dtype=torch.uint8, device="cuda"), torch.empty((9, -(-cols // 128)), device="cuda")
+    moe.moe_fp8_quantize(x, q, scale, pow2=pow2)
+    # the host divides by each scale (IEEE), so -0 and quotients that round to nothing keep their sign
+    v = x.float().cpu() / scale.cpu().repeat_interleave(128, 1)[:, :cols]
+    assert torch.equal(q.cpu(), v.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8))
+    assert (q[:, ::3][x[:, ::3] == 0] == 0x80).all() and (scale[1] == 1.0).all()
