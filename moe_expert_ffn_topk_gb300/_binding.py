@@ -342,10 +342,10 @@ def _handle(stream, t):
 
 
 def _vec(t, what, dtype, shape):
-    """Address of a contiguous device tensor of that type and shape."""
+    """Address of a contiguous device tensor of that type (or of one of a tuple of them) and shape."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be in device memory")
-    if t.dtype is not dtype:
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -451,6 +451,27 @@ def moe_fp8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream=
         raise MoeError(status, "moe_fp8_matmul")
 
 
+# types of moe_layer's weights and of their scales, where the format has any (one-byte codes and scale exponents also as uint8),
+# and how many of K's values share a byte, and a scale with how many outputs
+_LAYER_TYPES = {
+    "bf16": (torch.bfloat16, None, 1, 0, 0),
+    "fp8_block": (_FP8_CODES, torch.float32, 1, 128, 128),
+    "fp4_mx": (tuple(t for t in (torch.uint8, getattr(torch, "float4_e2m1fn_x2", None)) if t),
+               tuple(t for t in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if t), 2, 1, 32),
+}
+
+
+def _layer_operand(data, scale, what, weights, experts, n, k):
+    """One of moe_layer's weights, [experts, n, k] with its scales, or bf16 [experts, k, n] (a scale is not read then)."""
+    codes, scales, packed, rows, cols = _LAYER_TYPES[weights]
+    if data is None or (scale is None and scales is not None):
+        raise ValueError(f"{what} of {weights} weights is a tensor{' with its scales' if scales else ''}")
+    if scales is None:
+        return MoeOperand(_vec(data, what, codes, (experts, k, n)), None)
+    return MoeOperand(_vec(data, what, codes, (experts, n, k // packed)),
+                      _vec(scale, what + "_scale", scales, (experts, n // rows, k // cols)))
+
+
 def moe_layer_workspace_bytes(d: MoeDims, weights) -> int:
     return LIB.moe_layer_workspace_bytes(ctypes.byref(d), LAYER_WEIGHTS[weights])
 
@@ -458,14 +479,17 @@ def moe_layer_workspace_bytes(d: MoeDims, weights) -> int:
 def moe_layer(x, router, w1, w1_scale, w2, w2_scale, y, d: MoeDims, weights, workspace, options=None, bias=None,
               topk_ids=None, topk_weights=None, activation_clamp=None, stream=None):
     """The whole layer for up to MOE_LAYER_MAX_TOKENS tokens in one launch: router product, selection, experts, combine.
-    weights: "bf16", "fp8_block" or "fp4_mx". Without a router, topk_ids and topk_weights are inputs; with one they are
+    weights: "bf16", "fp8_block" or "fp4_mx"; w1, w2 and their scales in the shapes moe_ops.h lists for it, the shared experts after
+    the routed ones. Without a router, topk_ids and topk_weights are inputs; with one they are
     optional outputs."""
     T, H, E, K = d.num_tokens, d.hidden, d.num_experts, d.topk
     args = MoeLayerArgs()
     args.x = _vec(x, "x", torch.bfloat16, (T, H))
     args.y = _vec(y, "y", torch.bfloat16, (T, H))
-    args.w1, args.w2 = _operand(w1, w1_scale, "w1"), _operand(w2, w2_scale, "w2")
     args.weights = LAYER_WEIGHTS[weights]
+    experts, inter = E + d.num_shared_experts, d.intermediate
+    args.w1 = _layer_operand(w1, w1_scale, "w1", weights, experts, 2 * inter, H)
+    args.w2 = _layer_operand(w2, w2_scale, "w2", weights, experts, H, inter)
     if router is not None:
         args.router_type = _float_type(router, "router")
         args.router = _vec(router, "router", router.dtype, (E, H))
