@@ -328,17 +328,19 @@ def moe_plan_noalloc(topk_ids, d: MoeDims, counts, offsets, row_src, stream=None
 
 _FLOAT_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
 _FP8_CODES = (torch.float8_e4m3fn, torch.uint8)
-# the current stream's handle without a Stream object around it (a third of a small call's host time otherwise)
+# the current device, and its current stream's handle without a Stream object around it (a third of a small call's host time otherwise)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _handle(stream, t):
-    """Handle of `stream`, or of the current stream of t's device."""
+    """Handle of `stream`, or of the current stream. The library launches on the current device, so t has to be there."""
+    device = t.get_device()
+    if device != _current_device():
+        raise ValueError(f"the tensors are on {t.device}, which is not the current device")
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is None or t.device.type != "cuda":
-        return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(t.get_device())
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(device)
 
 
 def _vec(t, what, dtype, shape):

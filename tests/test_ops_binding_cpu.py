@@ -84,3 +84,43 @@ def test_layer_checks_its_weights_before_the_call(moe, placed, monkeypatch):
             with pytest.raises(ValueError, match="shape"):
                 moe.moe_layer(x, router, short[0], short[1], short[2], short[3], y, d, fmt, ws)
     assert len(reached) == 3
+
+
+def test_tensors_of_another_device_than_the_current_one_are_refused(moe, placed, monkeypatch):
+    """The library launches on the calling thread's device; a stream or pointers of another one do not belong there."""
+    b = moe._binding
+    reached = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: reached.append(name) or 0
+    monkeypatch.setattr(b, "LIB", Lib())
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1)
+    monkeypatch.setattr(b, "_raw_stream", lambda device: 0)
+
+    class Stream:
+        cuda_stream = 0
+    d = moe.dims(T, H, I, E, K, S)
+    x, q = torch.zeros((T, H), dtype=torch.bfloat16), torch.zeros((T, H), dtype=torch.uint8)
+    scale, ids, ws = torch.zeros((T, H // 128)), torch.zeros((T, K), dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    w = weights_of("fp8_block")
+    calls = {
+        "moe_gate": lambda **k: moe.moe_gate(torch.zeros((T, E)), d, ids, torch.zeros((T, K)), **k),
+        "moe_fp8_quantize": lambda **k: moe.moe_fp8_quantize(x, q, scale, **k),
+        "moe_fp8_matmul": lambda **k: moe.moe_fp8_matmul(q, scale, torch.zeros((128, H), dtype=torch.uint8), torch.zeros((1, H // 128)),
+                                                         torch.zeros((T, 128)), ws, **k),
+        "moe_layer": lambda **k: moe.moe_layer(x, torch.zeros((E, H)), *w, x.clone(), d, "fp8_block", ws, **k),
+        "moe_ops_workspace_init": lambda **k: moe.moe_ops_workspace_init(ws, **k),
+    }
+    for current in (0, 1):
+        monkeypatch.setattr(b, "_current_device", lambda: current, raising=False)
+        for name, call in calls.items():
+            for stream in (None, Stream()):
+                reached.clear()
+                if current == 1:
+                    call(stream=stream)
+                    assert reached == [name]
+                else:
+                    with pytest.raises(ValueError, match="current device"):
+                        call(stream=stream)
+                    assert reached == []
