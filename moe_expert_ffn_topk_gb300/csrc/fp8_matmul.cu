@@ -24,7 +24,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "ops.h"
@@ -461,13 +460,12 @@ using Few = Cfg<1, 128, 32, 8>;
 
 template <class C, typename Out>
 cudaError_t prepare_kernel(int* resident) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static int clusters = 0;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(fp8_matmul_kernel<C, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-        if (err == cudaSuccess) err = check_register_split(reinterpret_cast<const void*>(fp8_matmul_kernel<C, Out>), kLaunchRegs);
-        if (C::kCtas == 1 || err != cudaSuccess) return;
+    static int clusters[kMaxDevices];
+    int device = 0;
+    const cudaError_t err = once_per_device(&device, [](int dev) {
+        cudaError_t e = cudaFuncSetAttribute(fp8_matmul_kernel<C, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (e == cudaSuccess) e = check_register_split(reinterpret_cast<const void*>(fp8_matmul_kernel<C, Out>), kLaunchRegs);
+        if (C::kCtas == 1 || e != cudaSuccess) return e;
         // pairs that can be resident at once (a pair needs two free SMs of one GPC)
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * std::max(1, tc_num_sms() / 2));
@@ -479,12 +477,13 @@ cudaError_t prepare_kernel(int* resident) {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&clusters, fp8_matmul_kernel<C, Out>, &cfg) != cudaSuccess || clusters < 1) {
+        if (cudaOccupancyMaxActiveClusters(&clusters[dev], fp8_matmul_kernel<C, Out>, &cfg) != cudaSuccess || clusters[dev] < 1) {
             (void)cudaGetLastError();
-            clusters = std::max(1, tc_num_sms() / 2);
+            clusters[dev] = std::max(1, tc_num_sms() / 2);
         }
+        return e;
     });
-    *resident = clusters;
+    *resident = err == cudaSuccess ? clusters[device] : 0;
     return err;
 }
 

@@ -48,7 +48,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 
 #include "common.cuh"
 #include "gate_select.cuh"
@@ -1159,12 +1158,11 @@ constexpr size_t smem_bytes() {
 
 template <int kFmt, int NT>
 cudaError_t launch_tiles(const Args& p, cudaStream_t s) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
     static_assert(smem_bytes<kFmt>() <= 232448, "shared memory");
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(layer_kernel<kFmt, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<kFmt>());
-        if (err == cudaSuccess) err = check_register_split(reinterpret_cast<const void*>(layer_kernel<kFmt, NT>), kLaunchRegs);
+    int device = 0;
+    const cudaError_t err = once_per_device(&device, [](int) {
+        const cudaError_t e = cudaFuncSetAttribute(layer_kernel<kFmt, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<kFmt>());
+        return e != cudaSuccess ? e : check_register_split(reinterpret_cast<const void*>(layer_kernel<kFmt, NT>), kLaunchRegs);
     });
     if (err != cudaSuccess) return err;
     CUtensorMap m1 = {}, m2 = {};

@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "internal.h"
 #include "moe_ops.h"
 
@@ -29,6 +31,22 @@ inline cudaError_t check_register_split(const void* kernel, int regs) {
     cudaFuncAttributes a;
     const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
     return e != cudaSuccess ? e : a.numRegs >= regs ? cudaSuccess : cudaErrorLaunchOutOfResources;
+}
+
+// What has to be done once before a kernel's first launch on a device (its attributes belong to the device that is current when they are
+// set): calls set(device) the first time on each and returns what it returned there. *device: the current one. Set is a lambda of the
+// one place that uses it.
+constexpr int kMaxDevices = 64;
+template <typename Set>
+cudaError_t once_per_device(int* device, Set set) {
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    const cudaError_t e = cudaGetDevice(device);
+    if (e != cudaSuccess) return e;
+    const int d = *device;
+    if (d < 0 || d >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[d], [&] { err[d] = set(d); });
+    return err[d];
 }
 
 bool gate_options_ok(const moe_gate_options& o, int E, int K);
