@@ -98,7 +98,7 @@ MOE_API moe_status moe_fp8_quantize(const void* x, moe_type type, int64_t rows, 
  *            outside [0, M] are taken as the nearest bound, one below an earlier one as that one.
  *   out      bf16 or fp32 [M,N], out_stride apart
  * The sums over a block of K are the tensor core's fp32 sums, those over the blocks are fp32 fused multiply-adds.
- * Limits: 0 <= M < 2^31, 1 <= N <= 2^20, 16 <= K <= 2^20, 1 <= groups <= 1024, M * out_stride and the other
+ * Limits: 0 <= M <= 2^31 - 512, 1 <= N <= 2^20, 16 <= K <= 2^20, 1 <= groups <= 1024, M * out_stride and the other
  * extents < 2^62; K, a_stride and b_stride multiples of 16, a and b 16-byte aligned (TMA); out aligned to its
  * elements. Errors: MOE_ERR_INVALID_ARG for these, MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
 typedef struct {

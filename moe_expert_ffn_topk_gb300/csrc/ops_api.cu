@@ -22,8 +22,11 @@ bool workspace_ok(const void* ws, size_t have, size_t need) { return ws && align
 // x 2^62: products of the sizes stay inside 64 bits
 bool extent_ok(int64_t rows, int64_t stride) { return stride >= 0 && (rows == 0 || stride <= (int64_t(1) << 62) / rows); }
 
+// M: a tile of 256 rows may begin at any row, and its last row's number stays inside 32 bits
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
+
 bool matmul_sizes_ok(int64_t M, int64_t N, int64_t K, int32_t groups) {
-    return M >= 0 && M < (int64_t(1) << 31) && N >= 1 && N <= (1 << 20) && K >= 16 && K <= (1 << 20) && K % 16 == 0 &&
+    return M >= 0 && M <= kMaxRows && N >= 1 && N <= (1 << 20) && K >= 16 && K <= (1 << 20) && K % 16 == 0 &&
            groups >= 1 && groups <= 1024;
 }
 
