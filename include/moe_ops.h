@@ -147,8 +147,10 @@ enum {
  *   gate, gate_bias  as moe_gate's opt and bias (not read without a router)
  *   topk_ids, topk_weights  int32 and fp32 [T,K]: outputs with a router (NULL: not wanted)
  *   y            bf16 [T,H]; a token with no route and no shared expert gets zeros
- * Weights are converted exactly to the 16-bit operands of the tensor cores; x, the activations (rounded once to 16-bit
- * halves that hold at least 11 bits of them) and all sums are described at the kernel. Deterministic.
+ * Weights are converted exactly to the 16-bit operands of the tensor cores (FP4: where the scales of each 128 of K of a row
+ * lie within 2^36 of the largest of them; codes with smaller ones are rounded to multiples of 2^-37 times it); x, the
+ * activations (rounded once to 16-bit halves that hold at least 11 bits of them) and all sums are described at the
+ * kernel. Deterministic.
  * Limits: those of moe_dims (H and I multiples of 128), T <= MOE_LAYER_MAX_TOKENS (else MOE_ERR_UNSUPPORTED: use
  * moe_forward); all tensors contiguous and 16-byte aligned. */
 typedef struct {

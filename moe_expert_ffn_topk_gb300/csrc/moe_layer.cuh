@@ -30,7 +30,7 @@
 // bf16 x is exact down to 2^-39 of its row's maximum, activations lose up to 2^-11 a value, against 2^-8 of the bf16
 // result). The
 // FP8 weight scale multiplies the fp32 sum over each 64 of K; the UE8M0 scales of FP4 multiply the f16 codes relative to the
-// largest of the four blocks that a stage's sum covers (exact while they lie within 2^20 of it) and that one the fp32 sum.
+// largest of the four blocks that a stage's sum covers (exact while they lie within 2^36 of it) and that one the fp32 sum.
 //
 // Bound by HBM where a call reads much of few experts. Fractions are of the measured copy rate and count the weights of the experts
 // that the routes in fact touched. 3 tokens, top-2 of 8 experts, 4096 / 14336, BF16: 1.41 GB (4 experts) in 228 us, 0.93; 1.76 GB (5)
@@ -205,9 +205,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// 2^-d as f16 twice (d >= 0; 0 below the smallest subnormal)
+// 2^(kFp4Up - d) as f16 twice (d >= 0; 0 below the smallest subnormal). kFp4Up: as far up as the largest e2m1 value, 6, stays finite, so
+// that the codes of blocks with smaller scales have the room below. The rows' inverse scales take it back (kFp4Down).
+constexpr int kFp4Up = 13;
+constexpr float kFp4Down = 1.0f / (1 << kFp4Up);
 __device__ __forceinline__ uint32_t pow2_f16x2(int d) {
-    const uint32_t h = d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+    const uint32_t h = d <= 14 + kFp4Up ? (uint32_t)(15 + kFp4Up - d) << 10 : d <= 24 + kFp4Up ? 1u << (24 + kFp4Up - d) : 0u;
     return h | (h << 16);
 }
 // The power of two that takes magnitudes up to `top` (bits) below 2^15, and its inverse. Zero, infinities and NaNs: 1.
@@ -314,8 +317,8 @@ static __device__ void router_phase(const Args& p, float* parts, int warp, int l
     }
 }
 
-// x of one token as f16, scaled by a power of two (all threads of the CTA).
-static __device__ void round_x(const Args& p, int t, uint32_t* scratch) {
+// x of one token as f16, scaled by a power of two (all threads of the CTA); down: a factor of the inverse scale.
+static __device__ void round_x(const Args& p, int t, float down, uint32_t* scratch) {
     const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.H);
     uint32_t top = 0;
     for (int v = threadIdx.x; v < p.H / 8; v += kThreads) {
@@ -341,7 +344,7 @@ static __device__ void round_x(const Args& p, int t, uint32_t* scratch) {
         for (int i = 0; i < 4; ++i) o[i] = pack_f16(__uint_as_float(u[i] << 16) * s, __uint_as_float(u[i] & 0xffff0000u) * s);
         dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    if (threadIdx.x == 0) p.xinv[t] = inverse;
+    if (threadIdx.x == 0) p.xinv[t] = inverse * down;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -881,7 +884,8 @@ __device__ __forceinline__ void consume(const Args& p, Ring<kFmt>& ring, int& se
                     dst[(2 * t + 1) * G::kRedCol + r8] = acc[m][n][3];
                 }
                 // once per set: by the group that holds the unit's first stage
-                if (kSecond && !G::kBf16 && seq % G::kGroups == group && t == 0) reds[(q + 1) * G::kRed - 8 + g] = ainv[n];
+                if (kSecond && !G::kBf16 && seq % G::kGroups == group && t == 0)
+                    reds[(q + 1) * G::kRed - 8 + g] = G::kFp4 ? ainv[n] * kFp4Down : ainv[n];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(ring.red_full(q));
@@ -1075,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.router) router_phase(p, reds, warp, lane);
     if constexpr (!G::kBf16)
         for (int t = (int)gridDim.x - 1 - (int)blockIdx.x; t < p.T; t += gridDim.x)
-            round_x(p, t, reinterpret_cast<uint32_t*>(reds));
+            round_x(p, t, G::kFp4 ? kFp4Down : 1.0f, reinterpret_cast<uint32_t*>(reds));
     if (p.router || !G::kBf16) grid_barrier(p, ++barriers, abort_flag);
 
     // ---- phase 2

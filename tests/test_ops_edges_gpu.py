@@ -131,3 +131,35 @@ def test_quantize_keeps_the_sign_of_a_zero(moe, cols, dtype, pow2):
     v = x.float().cpu() / scale.cpu().repeat_interleave(128, 1)[:, :cols]
     assert torch.equal(q.cpu(), v.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8))
     assert (q[:, ::3][x[:, ::3] == 0] == 0x80).all() and (scale[1] == 1.0).all()
+
+
+@pytest.mark.parametrize("apart", [8, 20, 25, 30, 36])
+@pytest.mark.parametrize("T,empty", [(2, True), (20, True), (2, False)])
+def test_layer_fp4_scales_far_apart(moe, T, empty, apart):
+    """One block of 32 in every four has a scale 2^apart times its neighbours'; with `empty` all its codes are zero, so that the
+    neighbours alone make the result."""
+    H, I, E, K = 512, 256, 4, 2  # noqa: E741
+    g = gen(apart)
+    d = moe.dims(T, H, I, E, K)
+    table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.double, device="cuda")
+    table = torch.cat([table, -table])
+
+    def operand(n, k):
+        codes = torch.randint(0, 256, (E, n, k // 32, 16), dtype=torch.uint8, generator=g, device="cuda")
+        scale = torch.full((E, n, k // 32), 120, dtype=torch.uint8, device="cuda")
+        far = torch.randint(0, 4, (E, n, k // 128), generator=g, device="cuda") + 4 * torch.arange(k // 128, device="cuda")
+        scale.scatter_(2, far, 120 + apart)
+        if empty:
+            codes[scale > 120] = 0
+        codes = codes.view(E, n, k // 2)
+        dense = torch.stack([table[(codes & 15).long()], table[(codes >> 4).long()]], -1).flatten(-2)
+        return codes, scale, dense * torch.exp2(scale.double() - 127).repeat_interleave(32, 2)
+
+    x = randn(g, T, H).to(torch.bfloat16)
+    w1, w2 = operand(2 * I, H), operand(H, I)
+    ids = torch.stack([torch.randperm(E, generator=g, device="cuda")[:K] for _ in range(T)]).to(torch.int32)
+    weights = torch.rand((T, K), generator=g, device="cuda")
+    y, status = run_layer(moe, x, None, w1, w2, d, "fp4_mx", topk_ids=ids, topk_weights=weights)
+    ref, bound = layer_reference(x, ids, weights, w1[2], w2[2], E, 0)
+    assert status == moe.MOE_OK
+    assert ((y.double() - ref).abs() <= bound).all(), ((y.double() - ref).abs() / bound).max()
