@@ -74,11 +74,11 @@ MOE_API moe_status moe_gate(const void* logits, moe_type type, int64_t row_strid
  * ------------------------------------------------------------------------------------------------------ */
 
 enum {
-    MOE_QUANT_POW2 = 1u /* scales are powers of two: the smallest that is >= amax / 448 */
+    MOE_QUANT_POW2 = 1u /* scales are powers of two: the smallest that is >= amax / 448, and 2^-126 at least */
 };
 
 /* Rows of x in e4m3 with an fp32 scale for each 128 columns (the last block may be smaller):
- *   s = amax / 448 (1 where amax is 0), q = e4m3(x / s): fp32 IEEE division, round half to even.
+ *   s = amax / 448 (1 where that is 0), q = e4m3(x / s): fp32 IEEE division, round half to even.
  * A block that holds a NaN or an infinity gets a NaN or infinite scale, so products with it are not finite.
  *   x      device [rows, cols] of `type`, x_stride >= cols elements apart.
  *   q      device e4m3 [rows, cols], q_stride >= cols apart.
@@ -97,7 +97,8 @@ MOE_API moe_status moe_fp8_quantize(const void* x, moe_type type, int64_t rows, 
  *            [offsets[g], offsets[g+1]) are multiplied by b[g]. Rows from offsets[groups] on are not written. Values
  *            outside [0, M] are taken as the nearest bound, one below an earlier one as that one.
  *   out      bf16 or fp32 [M,N], out_stride apart
- * The sums over a block of K are the tensor core's fp32 sums, those over the blocks are fp32 fused multiply-adds.
+ * The sums over a block of K are the tensor core's fp32 sums, those over the blocks are fp32 fused multiply-adds with the
+ * fp32 product of the two scales.
  * Limits: 0 <= M <= 2^31 - 512, 1 <= N <= 2^20, 16 <= K <= 2^20, 1 <= groups <= 1024, M * out_stride and the other
  * extents < 2^62; K, a_stride and b_stride multiples of 16, a and b 16-byte aligned (TMA); out aligned to its
  * elements. Errors: MOE_ERR_INVALID_ARG for these, MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */

@@ -4,9 +4,9 @@
 //
 // The scales are arbitrary fp32 numbers, so the tensor cores cannot apply them (their block scales are powers of two):
 // P_kb is formed in tensor memory by four tcgen05.mma kind::f8f6f4 (K = 32 each) and added up in registers, one fp32
-// fused multiply-add a value and block of K. Two accumulator buffers in tensor memory let the product of block kb + 1
-// run while eight warps take block kb out. A lane is a row of a and a warp's columns lie in one block of b, so a warp
-// needs one factor a lane and block.
+// fused multiply-add a value and block of K. Two accumulator buffers in tensor memory (all of it with 256 columns a tile,
+// half of it with 128) let the product of block kb + 1 run while eight warps take block kb out. A lane is a row of a and a
+// warp's columns lie in one block of b, so a warp needs one factor a lane and block.
 //
 // Warp roles (384 threads): warp 0 TMA producer, warp 1 tensor-memory allocator and MMA issuer, warp 2 the groups' table,
 // warps 4-11 take the products out (warp w the lanes 32 * (w % 4) .., warps 4-7 the first half of the tile's columns, 8-11
@@ -15,9 +15,11 @@
 //
 // Measured, 8192 x 4096 x 7168 to bf16: 188 us in short runs, 199 in a steady one at the power cap, 206 among other work (2.3-2.6
 // PFLOP/s; 54 % of the tensor pipe). A buffer's way round (MMA, its commit, the warps' reads, their release) holds back the two
-// buffers that tensor memory has room for: 840-860 cycles a block of K, reckoned from the steady run's time and clock; the same loop
+// buffers, for which tensor memory has room here: 840-860 cycles a block of K, reckoned from the steady run's time and clock; the same loop
 // without the eight warps' work takes 144 us. Few rows (1 x 4096 x
-// 7168: 11 us a call, 8.8 on the device, 29 MB) are bound by start-up and the cluster's sum around 14 blocks a CTA.
+// 7168: 11 us a call, 8.8 on the device, 29 MB) are bound by start-up, two buffers in turn and the cluster's sum around 14 blocks a
+// CTA. Few rows of many groups are not split over K: 64 rows, 21 groups with rows, 4096 x 2048: 41 us for 177 MB (0.65 of the copy
+// rate); 6 groups, 512 x 7168: 23 us for 22 MB (0.15), 24 CTAs that walk all of K alone.
 //
 // Every wait is bounded (2 s); on time-out the CTA records MOE_ERR_TIMEOUT and leaves its loops.
 #include <cuda.h>

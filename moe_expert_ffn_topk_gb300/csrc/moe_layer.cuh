@@ -26,18 +26,21 @@
 // depend on timing.
 //
 // Operands. BF16: x as it is; the activations as two bf16 (hi + lo, 16 bits of them) and two MMAs. FP8 and FP4: the weights are
-// exact in f16, x and the activations are scaled by a power of two of their row to below 2^15 and rounded once to f16 (11 bits;
-// bf16 x is exact down to 2^-39 of its row's maximum, activations lose up to 2^-11 a value, against 2^-8 of the bf16
-// result). The
-// FP8 weight scale multiplies the fp32 sum over each 64 of K; the UE8M0 scales of FP4 multiply the f16 codes relative to the
-// largest of the four blocks that a stage's sum covers (exact while they lie within 2^36 of it) and that one the fp32 sum.
+// exact in f16, x and the activations are scaled by a power of two of their row to below 2^15 and rounded once to f16: 11 bits, and
+// below 2^-14 multiples of 2^-24. So bf16 x is exact down to 2^-31 of its row's maximum and rounded to multiples of 2^-38 of it at
+// worst below; activations lose up to 2^-11 a value, against 2^-8 of the bf16 result. The FP8 weight scale multiplies the fp32
+// sum over each 64 of K; the UE8M0 scales of FP4 multiply the f16 codes relative to the largest of the four blocks that a stage's
+// sum covers (exact while they lie within 2^36 of it) and that one the fp32 sum.
 //
 // Bound by HBM where a call reads much of few experts. Fractions are of the measured copy rate and count the weights of the experts
 // that the routes in fact touched. 3 tokens, top-2 of 8 experts, 4096 / 14336, BF16: 1.41 GB (4 experts) in 228 us, 0.93; 1.76 GB (5)
 // in 274, 0.96; 2.11 GB (6) in 320, 0.99. 32 tokens, top-8 of 256 experts in the best 4 of 8 groups and a shared one, hidden 7168,
 // intermediate 2048, FP8: 6.08 GB (138 experts) in 1.11-1.12 ms, 0.81. One token of the same: 397 MB (9) in 82 us, 0.72 (13 us are
 // the router and the selection, whose barriers and latencies no weights hide). 5 tokens, top-6 of 64, 2048 / 768, FP4: 58 MB (23) in
-// 53-54 us, latency all over.
+// 53-58 us, by inputs and machine. With more column tiles an expert, and in FP4, it is not HBM (what it is was not profiled): BF16,
+// 8 experts as above, 16 / 32 / 64 tokens 464 / 666 / 1267 us (0.91, 0.63, 0.33); FP4, top-8 of 128 and a shared one, 4096 / 1536,
+// 5 / 16 / 32 / 64 tokens 169 / 390 / 584 / 986 us (0.30, 0.31, 0.29, 0.19; that of 33-64 tokens spills some 460 bytes a thread);
+// FP8 of that layer, 4 / 16 / 64 tokens 110 / 310 / 706 us (0.75, 0.73, 0.51), 104 for 4 with the routes given.
 //
 // Every wait is bounded (2 s): MOE_ERR_TIMEOUT. From then on the CTA's waits end at once, no slot of the ring is handed back for
 // another copy, its queue of units ends, and it passes the barriers that are left.
