@@ -169,6 +169,8 @@ typedef struct {
     float activation_clamp;       /* as in moe_options */
 } moe_layer_args;
 
+/* Bytes of workspace of moe_layer for up to d->num_tokens tokens, the other sizes as in d (0 when they are outside its
+ * limits); zeroed once. */
 MOE_API size_t moe_layer_workspace_bytes(const moe_dims* d, moe_layer_weights weights);
 MOE_API moe_status moe_layer(const moe_layer_args* args, const moe_dims* d, void* workspace, size_t workspace_bytes,
                              moe_stream_t stream);

@@ -1,6 +1,7 @@
 // Host side of the operators of moe_ops.h: argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "ops.h"
@@ -92,7 +93,10 @@ moe_status moe_fp8_matmul(const moe_fp8_matmul_args* a, void* workspace, size_t 
 
 size_t moe_layer_workspace_bytes(const moe_dims* d, moe_layer_weights weights) {
     if (!layer_dims_ok(d, weights) || d->num_tokens > MOE_LAYER_MAX_TOKENS) return 0;
-    return layer_layout(*d, weights).total;
+    // K is cut into more parts for fewer tokens, which can take more memory: enough for any number up to this one
+    size_t most = 0;
+    for (moe_dims few = *d; few.num_tokens >= 0; --few.num_tokens) most = std::max(most, layer_layout(few, weights).total);
+    return most;
 }
 
 moe_status moe_layer(const moe_layer_args* a, const moe_dims* d, void* workspace, size_t workspace_bytes,

@@ -163,3 +163,19 @@ def test_layer_fp4_scales_far_apart(moe, T, empty, apart):
     ref, bound = layer_reference(x, ids, weights, w1[2], w2[2], E, 0)
     assert status == moe.MOE_OK
     assert ((y.double() - ref).abs() <= bound).all(), ((y.double() - ref).abs() / bound).max()
+
+
+def test_layer_workspace_of_the_most_tokens_serves_fewer(moe):
+    """14 tokens of these sizes take more memory than 15 (their second product's K is cut into more parts)."""
+    T, H, I, E, K = 15, 1024, 8192, 16, 1  # noqa: E741
+    g = gen(31)
+    x, router = randn(g, T, H).to(torch.bfloat16), (randn(g, E, H) * H ** -0.5).to(torch.bfloat16)
+    w1, w2 = layer_weights(g, "fp8_block", E, 2 * I, H), layer_weights(g, "fp8_block", E, H, I)
+    ws = moe.alloc_ops_workspace(moe.moe_layer_workspace_bytes(moe.dims(T, H, I, E, K), "fp8_block"))
+    for t in (15, 14, 1, 9):
+        d = moe.dims(t, H, I, E, K)
+        ids, weights = torch.empty((t, K), dtype=torch.int32, device="cuda"), torch.empty((t, K), device="cuda")
+        y, status = run_layer(moe, x[:t], router, w1, w2, d, "fp8_block", ws, topk_ids=ids, topk_weights=weights)
+        assert status == moe.MOE_OK
+        ref, bound = layer_reference(x[:t], ids, weights, w1[2], w2[2], E, 0)
+        assert ((y.double() - ref).abs() <= bound).all()

@@ -25,3 +25,12 @@ def test_matmul_rows_stay_inside_32_bits(moe, past):
     args = moe._binding.MoeFp8MatmulArgs(*[fields[n] for n, _ in moe._binding.MoeFp8MatmulArgs._fields_])
     # (without a workspace, so that no version of the library gets as far as a launch)
     assert moe._binding.LIB.moe_fp8_matmul(ctypes.byref(args), None, 0, None) == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8_block", "fp4_mx"])
+@pytest.mark.parametrize("sizes", [(6528, 640, 256, 3, 2), (3712, 15104, 60, 1, 2), (1664, 6144, 60, 2, 1), (2944, 12032, 64, 2, 2),
+                                   (4224, 5632, 60, 5, 2), (7168, 2048, 256, 8, 1), (128, 16384, 1, 1, 0)])
+def test_a_layer_workspace_serves_fewer_tokens(moe, fmt, sizes):
+    """Fewer tokens can cut K into more parts; a workspace for the most tokens of a server takes them all the same."""
+    need = [moe.moe_layer_workspace_bytes(moe.dims(t, *sizes), fmt) for t in range(65)]
+    assert all(n > 0 for n in need) and need == sorted(need)
