@@ -1,6 +1,7 @@
 /*
  * moe_ops.h -- C ABI of the operators around the expert FFN of moe_ffn.h: the router, products of 8-bit
- * floating-point matrices with a scale for each block of 128, and the whole MoE layer for a few tokens.
+ * floating-point matrices with a scale for each block of 128, the whole MoE layer for a few tokens, rows sorted
+ * by expert and back with their gradients, and products of 8-bit integer matrices with a scale for each row.
  *
  * The conventions of moe_ffn.h hold: plain device pointers and sizes, nothing allocated, asynchronous on
  * `stream`, argument errors found on the host before anything is launched. What differs:
@@ -22,7 +23,8 @@ extern "C" {
 /* Element types of plain floating-point operands. */
 typedef enum {
     MOE_TYPE_BF16 = 0,
-    MOE_TYPE_F32 = 1
+    MOE_TYPE_F32 = 1,
+    MOE_TYPE_CODES8 = 2 /* one byte an element, copied as it is (int8, e4m3 ..): moe_permute alone */
 } moe_type;
 
 /* Sets a workspace of this header's operators to zero. MOE_ERR_WORKSPACE: missing or not 256-byte aligned. */
@@ -174,6 +176,107 @@ typedef struct {
 MOE_API size_t moe_layer_workspace_bytes(const moe_dims* d, moe_layer_weights weights);
 MOE_API moe_status moe_layer(const moe_layer_args* args, const moe_dims* d, void* workspace, size_t workspace_bytes,
                              moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------------------
+ * Rows in the order of their experts, and back
+ * ------------------------------------------------------------------------------------------------------ */
+
+/* Sorts the T*K slots (token i, k-th expert: slot i*K+k) by expert, slots of one expert in ascending order, and copies
+ * each slot's token to its row: rows[p] = x[row_src[p] / K] for p < R = offsets[E], the routed slots.
+ *   topk_ids   device int32 [T,K]: -1 is a masked route (no row); other ids outside [0,E) have no row either and set
+ *              MOE_ERR_BAD_ROUTE in the workspace's error word. An id may be there twice in a token.
+ *   x          device [T,H] of `type`, x_stride elements apart;    rows  [T*K,H] of it, rows_stride apart
+ *   scale      NULL, or device fp32 [T,scales], contiguous: goes to row_scale [T*K,scales] as x goes to rows
+ *   offsets    device int32 [E+1]: expert e's rows are [offsets[e], offsets[e+1]) (what the grouped products take)
+ *   row_src    device int32 [T*K]: the slot of row p, -1 for p >= R
+ *   slot_row   device int32 [T*K]: the row of each slot, -1 without one (what moe_unpermute takes)
+ * Rows from R on are not written. The order is fixed by the ids alone, unlike moe_plan's. The gradient with respect to x is
+ * moe_unpermute of the rows' gradients, without weights. T = d->num_tokens, K = d->topk, E = d->num_experts; the other
+ * sizes in d are not read. Errors: MOE_ERR_INVALID_ARG (sizes outside 1 <= K <= 32, 1 <= E <= 1024, T*K <= 2^24,
+ * 1 <= H <= 2^30, 0 <= scales <= 2^20; short strides; a missing or misaligned pointer), MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
+typedef struct {
+    const void* x;
+    const float* scale;
+    const int32_t* topk_ids;
+    void* rows;
+    float* row_scale;
+    int32_t* offsets;
+    int32_t* row_src;
+    int32_t* slot_row;
+    int64_t H, x_stride, rows_stride;
+    int32_t type;   /* a moe_type */
+    int32_t scales; /* not read without a scale */
+} moe_permute_args;
+
+/* Bytes of workspace of moe_permute (0 when T, K or E are outside its limits); zeroed once. */
+MOE_API size_t moe_permute_workspace_bytes(const moe_dims* d);
+MOE_API moe_status moe_permute(const moe_permute_args* args, const moe_dims* d, void* workspace, size_t workspace_bytes,
+                               moe_stream_t stream);
+
+/* y[i] = sum over k of topk_weights[i,k] * rows[slot_row[i,k]], in fp32 in the order of k and rounded once.
+ *   rows          device [T*K,H] of `type` (bf16 or fp32), rows_stride elements apart
+ *   slot_row      device int32 [T,K] of moe_permute: a slot whose entry is outside [0, T*K) adds nothing, whatever its
+ *                 weight; a token without any other gets zeros. Rows that no slot names are not read.
+ *   topk_weights  device fp32 [T,K], or NULL: 1 (the gradient of moe_permute)
+ *   y             device [T,H] of y_type (bf16 or fp32), y_stride apart; no part of rows
+ * Sizes, limits and errors as in moe_permute. */
+MOE_API moe_status moe_unpermute(const void* rows, moe_type type, int64_t rows_stride, const int32_t* slot_row,
+                                 const float* topk_weights, const moe_dims* d, int64_t H, void* y, moe_type y_type,
+                                 int64_t y_stride, moe_stream_t stream);
+
+/* Gradients of moe_unpermute from dy, that of y:
+ *   d_rows[slot_row[i,k]] = topk_weights[i,k] * dy[i]           in fp32, rounded once to the rows' type
+ *   d_weights[i,k]        = <rows[slot_row[i,k]], dy[i]>        in fp32; 0 for a slot without a row
+ *   dy         device [T,H] of dy_type (bf16 or fp32), dy_stride apart
+ *   rows       device [T*K,H] of `type`, rows_stride apart; not read (and may be NULL) without d_weights
+ *   d_rows     device [T*K,H] of `type`, d_rows_stride apart; rows that no slot names are not written
+ *   d_weights  device fp32 [T,K], or NULL: not wanted
+ * slot_row and topk_weights as in moe_unpermute; no two slots name one row; the outputs overlap no input. Deterministic.
+ * Errors as in moe_permute. */
+MOE_API moe_status moe_unpermute_backward(const void* dy, moe_type dy_type, int64_t dy_stride, const void* rows, moe_type type,
+                                          int64_t rows_stride, const int32_t* slot_row, const float* topk_weights,
+                                          const moe_dims* d, int64_t H, void* d_rows, int64_t d_rows_stride, float* d_weights,
+                                          moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------------------
+ * 8-bit integers with a scale for each row
+ * ------------------------------------------------------------------------------------------------------ */
+
+/* Rows of x in int8 with an fp32 scale each, as MOE_A8W8_INT8 has its activations (moe_dispatch_quantize):
+ *   s = max(amax / 127, 1e-8), q = x / s rounded half to even, within [-127, 127]: fp32 IEEE division.
+ * A row that holds a NaN or an infinity gets a NaN or infinite scale and zeros, so products with it are not finite.
+ *   x      device [rows, cols] of `type` (bf16 or fp32), x_stride >= cols elements apart
+ *   q      device int8 [rows, cols], q_stride >= cols apart;    scale  device fp32 [rows]
+ * Errors: MOE_ERR_INVALID_ARG (negative sizes, cols = 0 with rows > 0, cols > 2^30, short strides, a missing pointer, x or
+ * scale not aligned to its elements), MOE_ERR_CUDA. */
+MOE_API moe_status moe_int8_quantize(const void* x, moe_type type, int64_t rows, int64_t cols, int64_t x_stride, void* q,
+                                     int64_t q_stride, float* scale, moe_stream_t stream);
+
+/* out[m,n] = (C[m,n] * b_scale[g,n]) * a_scale[m],  C[m,n] = sum_k a[m,k] * b[g,n,k]
+ *   a        int8 [M,K], a_stride apart;                                  a_scale  fp32 [M]
+ *   b        int8 [groups][N,K], rows b_stride apart, groups N * b_stride apart;   b_scale  fp32 [groups][N]
+ *   offsets  as in moe_fp8_matmul (moe_permute and moe_plan write them)
+ *   out      bf16 or fp32 [M,N], out_stride apart
+ * C is the exact 32-bit integer, so the result does not depend on the kernel that formed it; it is rounded to fp32, and
+ * each product with a scale is. Codes may be -128.
+ * Limits: those of moe_fp8_matmul, and K <= 131056 (C stays inside 32 bits). Errors as there. */
+typedef struct {
+    const void* a;
+    const float* a_scale;
+    const void* b;
+    const float* b_scale;
+    const int32_t* offsets;
+    void* out;
+    int64_t M, N, K;
+    int64_t a_stride, b_stride, out_stride;
+    int32_t groups;
+    int32_t out_type; /* a moe_type */
+} moe_int8_matmul_args;
+
+/* Bytes of workspace of moe_int8_matmul for these sizes (0 when they are outside its limits); zeroed once. */
+MOE_API size_t moe_int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t groups);
+MOE_API moe_status moe_int8_matmul(const moe_int8_matmul_args* args, void* workspace, size_t workspace_bytes,
+                                   moe_stream_t stream);
 
 #ifdef __cplusplus
 }

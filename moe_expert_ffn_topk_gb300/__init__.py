@@ -20,6 +20,8 @@ from ._binding import PEAK_KINDS  # noqa: F401
 from ._binding import (LAYER_WEIGHTS, MOE_LAYER_MAX_TOKENS, MoeGateOptions, gate_options, moe_fp8_matmul,  # noqa: F401
                        moe_fp8_matmul_workspace_bytes, moe_fp8_quantize, moe_gate, moe_layer, moe_layer_workspace_bytes,
                        moe_ops_workspace_init)
+from ._binding import (moe_int8_matmul, moe_int8_matmul_workspace_bytes, moe_int8_quantize, moe_permute,  # noqa: F401
+                       moe_permute_workspace_bytes, moe_unpermute, moe_unpermute_backward)
 
 
 def alloc_workspace(d: MoeDims, mode, device="cuda") -> torch.Tensor:
@@ -32,7 +34,7 @@ def alloc_workspace(d: MoeDims, mode, device="cuda") -> torch.Tensor:
 
 
 def alloc_ops_workspace(nbytes: int, device="cuda") -> torch.Tensor:
-    """A zeroed device byte buffer for moe_fp8_matmul or moe_layer (nbytes from their *_workspace_bytes); kept and
+    """A zeroed device byte buffer for moe_fp8_matmul, moe_int8_matmul, moe_permute or moe_layer (nbytes from their *_workspace_bytes); kept and
     passed again, it needs no further initialisation."""
     if nbytes == 0:
         raise ValueError("sizes outside the library's limits")

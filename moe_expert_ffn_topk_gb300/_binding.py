@@ -30,11 +30,13 @@ ABI_FUNCTIONS = ("moe_workspace_bytes", "moe_plan", "moe_dispatch", "moe_expert_
                  "moe_expert_l1_ex", "moe_forward_ex", "moe_expert_ffn", "moe_tensor_peak_probe",
                  "moe_prepared_weights_bytes", "moe_prepare_weights",
                  "moe_ops_workspace_init", "moe_gate", "moe_fp8_quantize", "moe_fp8_matmul_workspace_bytes",
-                 "moe_fp8_matmul", "moe_layer_workspace_bytes", "moe_layer")
+                 "moe_fp8_matmul", "moe_layer_workspace_bytes", "moe_layer",
+                 "moe_permute_workspace_bytes", "moe_permute", "moe_unpermute", "moe_unpermute_backward",
+                 "moe_int8_quantize", "moe_int8_matmul_workspace_bytes", "moe_int8_matmul")
 # moe_peak_kind (include/moe_peak.h): the tcgen05 instruction kinds the probe measures
 PEAK_KINDS = {"bf16": 0, "f16": 1, "e4m3_e2m1": 2, "e4m3_e4m3": 3}
 # moe_ops.h: element types, router scores, weight formats of moe_layer
-MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
+MOE_TYPE_BF16, MOE_TYPE_F32, MOE_TYPE_CODES8 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}
 LAYER_WEIGHTS = {"bf16": 0, "fp8_block": 1, "fp4_mx": 2}
 MOE_QUANT_POW2 = 1
@@ -73,6 +75,15 @@ class MoeFp8MatmulArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("a", "a_scale", "b", "b_scale", "offsets", "out")] + \
         [(n, ctypes.c_int64) for n in ("M", "N", "K", "a_stride", "b_stride", "out_stride")] + \
         [("groups", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
+class MoeInt8MatmulArgs(ctypes.Structure):
+    _fields_ = MoeFp8MatmulArgs._fields_
+
+
+class MoePermuteArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "scale", "topk_ids", "rows", "row_scale", "offsets", "row_src", "slot_row")] + \
+        [(n, ctypes.c_int64) for n in ("H", "x_stride", "rows_stride")] + [("type", ctypes.c_int32), ("scales", ctypes.c_int32)]
 
 
 class MoeLayerArgs(ctypes.Structure):
@@ -120,6 +131,14 @@ def _load():
         "moe_fp8_quantize": (st, [vp, st, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_int64, vp, u32, vp]),
         "moe_fp8_matmul_workspace_bytes": (sz, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]),
         "moe_fp8_matmul": (st, [ctypes.POINTER(MoeFp8MatmulArgs), vp, sz, vp]),
+        "moe_permute_workspace_bytes": (sz, [dims_p]),
+        "moe_permute": (st, [ctypes.POINTER(MoePermuteArgs), dims_p, vp, sz, vp]),
+        "moe_unpermute": (st, [vp, st, ctypes.c_int64, vp, vp, dims_p, ctypes.c_int64, vp, st, ctypes.c_int64, vp]),
+        "moe_unpermute_backward": (st, [vp, st, ctypes.c_int64, vp, st, ctypes.c_int64, vp, vp, dims_p, ctypes.c_int64, vp,
+                                        ctypes.c_int64, vp, vp]),
+        "moe_int8_quantize": (st, [vp, st, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_int64, vp, vp]),
+        "moe_int8_matmul_workspace_bytes": (sz, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]),
+        "moe_int8_matmul": (st, [ctypes.POINTER(MoeInt8MatmulArgs), vp, sz, vp]),
         "moe_layer_workspace_bytes": (sz, [dims_p, st]),
         "moe_layer": (st, [ctypes.POINTER(MoeLayerArgs), dims_p, vp, sz, vp]),
     }
@@ -509,3 +528,133 @@ def moe_layer(x, router, w1, w1_scale, w2, w2_scale, y, d: MoeDims, weights, wor
     status = LIB.moe_layer(args, d, ws, nb, _handle(stream, x))
     if status:
         raise MoeError(status, "moe_layer")
+
+
+def moe_permute_workspace_bytes(d: MoeDims) -> int:
+    return LIB.moe_permute_workspace_bytes(d)
+
+
+_COPIED_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32, torch.int8: MOE_TYPE_CODES8,
+                 torch.uint8: MOE_TYPE_CODES8, torch.float8_e4m3fn: MOE_TYPE_CODES8, torch.float8_e5m2: MOE_TYPE_CODES8}
+
+
+def _same_place(first, *others):
+    """Tensors on other devices than `first` would be read as memory of its device."""
+    device = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"the tensors are on {first.device} and {t.device}")
+
+
+def moe_permute(x, topk_ids, d: MoeDims, rows, offsets, row_src, slot_row, workspace, scale=None, row_scale=None, stream=None):
+    """Rows of x ([T,H]: bf16, fp32 or 8-bit codes) in the order of their experts: rows ([T*K,H]), offsets (int32 [E+1]), row_src
+    (int32 [T*K], the slot of each row) and slot_row (int32 [T,K], the row of each slot), as moe_ops.h has them. With scale (fp32
+    [T,S]) row_scale ([T*K,S]) is written too. Rows of x and rows may be strided. The gradient of x is moe_unpermute of the rows'
+    gradients without weights."""
+    T, E, K = d.num_tokens, d.num_experts, d.topk
+    H = x.shape[-1]
+    try:
+        kind = _COPIED_TYPES[x.dtype]
+    except KeyError:
+        raise TypeError("x must be bfloat16, float32 or 8-bit codes") from None
+    if rows.dtype is not x.dtype:
+        raise TypeError(f"rows must be {x.dtype}, as x is")
+    if (scale is None) != (row_scale is None):
+        raise ValueError("scale and row_scale come together")
+    scales = 0
+    if scale is not None:
+        scales = scale.shape[-1]
+        _vec(scale, "scale", torch.float32, (T, scales))
+        _vec(row_scale, "row_scale", torch.float32, (T * K, scales))
+    _same_place(x, topk_ids, rows, offsets, row_src, slot_row, workspace, scale, row_scale)
+    ws, nbytes = _space(workspace)
+    args = MoePermuteArgs(x.data_ptr(), None if scale is None else scale.data_ptr(), _vec(topk_ids, "topk_ids", torch.int32, (T, K)),
+                          rows.data_ptr(), None if scale is None else row_scale.data_ptr(),
+                          _vec(offsets, "offsets", torch.int32, (E + 1,)), _vec(row_src, "row_src", torch.int32, (T * K,)),
+                          _vec(slot_row, "slot_row", torch.int32, (T, K)), H, _rows(x, "x", (T, H)),
+                          _rows(rows, "rows", (T * K, H)), kind, scales)
+    status = LIB.moe_permute(args, d, ws, nbytes, _handle(stream, x))
+    if status:
+        raise MoeError(status, "moe_permute")
+
+
+def moe_unpermute(rows, slot_row, y, weights=None, stream=None):
+    """y ([T,H], bf16 or fp32) = the sum over k of weights[:,k] * rows[slot_row[:,k]] (rows [T*K,H], bf16 or fp32; slot_row int32 [T,K]
+    of moe_permute, -1: adds nothing; weights fp32 [T,K], or None: 1). Rows of rows and y may be strided."""
+    T, K = slot_row.shape
+    H = y.shape[-1]
+    _same_place(rows, slot_row, y, weights)
+    status = LIB.moe_unpermute(rows.data_ptr(), _float_type(rows, "rows"), _rows(rows, "rows", (T * K, H)),
+                               _vec(slot_row, "slot_row", torch.int32, (T, K)),
+                               None if weights is None else _vec(weights, "weights", torch.float32, (T, K)), MoeDims(T, 0, 0, 0, K, 0),
+                               H, y.data_ptr(), _float_type(y, "y"), _rows(y, "y", (T, H)), _handle(stream, rows))
+    if status:
+        raise MoeError(status, "moe_unpermute")
+
+
+def moe_unpermute_backward(dy, slot_row, d_rows, weights=None, rows=None, d_weights=None, stream=None):
+    """Gradients of moe_unpermute: d_rows ([T*K,H], the rows' type) from dy ([T,H], bf16 or fp32) and the weights, and, with rows
+    ([T*K,H]) and d_weights (fp32 [T,K]), the weights' gradient. Rows of d_rows that no slot names are left as they are."""
+    T, K = slot_row.shape
+    H = dy.shape[-1]
+    if (rows is None) != (d_weights is None):
+        raise ValueError("rows and d_weights come together")
+    if rows is not None and rows.dtype is not d_rows.dtype:
+        raise TypeError(f"d_rows must be {rows.dtype}, as rows is")
+    _same_place(dy, slot_row, d_rows, weights, rows, d_weights)
+    status = LIB.moe_unpermute_backward(dy.data_ptr(), _float_type(dy, "dy"), _rows(dy, "dy", (T, H)),
+                                        None if rows is None else rows.data_ptr(), _float_type(d_rows, "d_rows"),
+                                        H if rows is None else _rows(rows, "rows", (T * K, H)),
+                                        _vec(slot_row, "slot_row", torch.int32, (T, K)),
+                                        None if weights is None else _vec(weights, "weights", torch.float32, (T, K)),
+                                        MoeDims(T, 0, 0, 0, K, 0), H, d_rows.data_ptr(), _rows(d_rows, "d_rows", (T * K, H)),
+                                        None if rows is None else _vec(d_weights, "d_weights", torch.float32, (T, K)),
+                                        _handle(stream, dy))
+    if status:
+        raise MoeError(status, "moe_unpermute_backward")
+
+
+def moe_int8_quantize(x, q, scale, stream=None):
+    """Rows of x (bf16 or fp32 [M,K]) into q (int8 [M,K]) and scale (fp32 [M]); rows of x and q may be strided."""
+    M, K = shape = x.shape
+    if q.dtype is not torch.int8:
+        raise TypeError("q must be int8")
+    _same_place(x, q, scale)
+    status = LIB.moe_int8_quantize(x.data_ptr(), _float_type(x, "x"), M, K, _rows(x, "x", shape), q.data_ptr(), _rows(q, "q", shape),
+                                   _vec(scale, "scale", torch.float32, (M,)), _handle(stream, x))
+    if status:
+        raise MoeError(status, "moe_int8_quantize")
+
+
+def moe_int8_matmul_workspace_bytes(M: int, N: int, K: int, groups: int = 1) -> int:
+    return LIB.moe_int8_matmul_workspace_bytes(M, N, K, groups)
+
+
+def moe_int8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream=None):
+    """out[m,n] = (a . b^T) * b_scale[n] * a_scale[m]: a int8 [M,K], a_scale fp32 [M], b int8 [groups,N,K] (or [N,K]), b_scale fp32
+    [groups,N] (or [N]), out bf16 or fp32 [M,N]; the integer product is exact. With `offsets` (int32 [groups+1]) rows
+    [offsets[g], offsets[g+1]) are multiplied by b[g]. Rows of a, b and out may be strided."""
+    if a.dtype is not torch.int8 or b.dtype is not torch.int8:
+        raise TypeError("a and b must be int8")
+    shape = a.shape
+    M, K = shape
+    if b.dim() == 3:
+        G, N, k2 = b.shape
+        between, b_stride, one = b.stride()
+        if G > 1 and between != N * b_stride:
+            raise ValueError("the groups of b must follow each other")
+    else:
+        G, (N, k2), (b_stride, one) = 1, b.shape, b.stride()
+    if k2 != K or not b.is_cuda or one != 1:
+        raise ValueError(f"b must be device memory of {K} contiguous columns")
+    if G * N == 1:
+        b_stride = K
+    _same_place(a, a_scale, b, b_scale, out, workspace, offsets)
+    ws, nbytes = _space(workspace)
+    args = MoeInt8MatmulArgs(a.data_ptr(), _vec(a_scale, "a_scale", torch.float32, (M,)), b.data_ptr(),
+                             _vec(b_scale, "b_scale", torch.float32, (N,) if b_scale.dim() == 1 and G == 1 else (G, N)),
+                             None if offsets is None else _vec(offsets, "offsets", torch.int32, (G + 1,)), out.data_ptr(), M, N, K,
+                             _rows(a, "a", shape), b_stride, _rows(out, "out", (M, N)), G, _float_type(out, "out"))
+    status = LIB.moe_int8_matmul(args, ws, nbytes, _handle(stream, a))
+    if status:
+        raise MoeError(status, "moe_int8_matmul")

@@ -58,6 +58,29 @@ cudaError_t launch_fp8_quantize(const void* x, int type, int64_t rows, int64_t c
 size_t fp8_matmul_workspace(int64_t M, int64_t N, int64_t K, int groups);
 cudaError_t launch_fp8_matmul(const moe_fp8_matmul_args& a, void* workspace, cudaStream_t s);
 
+// Slots (tokens x K) of a routing call, its experts and the experts of one token.
+constexpr int64_t kMaxSlots = int64_t(1) << 24;
+constexpr int kRowExperts = 1024, kRowTopk = 32;
+cudaError_t launch_permute(const moe_permute_args& a, int T, int K, int E, int32_t* hdr, cudaStream_t s);
+
+struct UnpermuteArgs {
+    const void* rows;  // [T*K, H]
+    const int32_t* slot_row;
+    const float* weights;
+    const void* dy;    // backward
+    void* out;         // y, or d_rows
+    float* d_weights;
+    int64_t H, rows_stride, dy_stride, out_stride;
+    int T, K, type, token_type;  // of the rows (and d_rows); of y and dy
+};
+cudaError_t launch_unpermute(const UnpermuteArgs& a, cudaStream_t s);
+cudaError_t launch_unpermute_backward(const UnpermuteArgs& a, cudaStream_t s);
+
+cudaError_t launch_int8_quantize(const void* x, int type, int64_t rows, int64_t cols, int64_t x_stride, int8_t* q,
+                                 int64_t q_stride, float* scale, cudaStream_t s);
+size_t int8_matmul_workspace(int64_t M, int64_t N, int64_t K, int groups);
+cudaError_t launch_int8_matmul(const moe_int8_matmul_args& a, void* workspace, cudaStream_t s);
+
 // Byte offsets of moe_layer's workspace.
 struct LayerLayout {
     size_t header, dep, cols, amax, logits, ids, weights, x16, xinv, act, comb, total;

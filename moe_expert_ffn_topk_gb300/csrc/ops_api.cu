@@ -31,6 +31,20 @@ bool matmul_sizes_ok(int64_t M, int64_t N, int64_t K, int32_t groups) {
            groups >= 1 && groups <= 1024;
 }
 
+// C of int8 codes down to -128 stays inside 32 bits below K = 2^17
+bool int8_sizes_ok(int64_t M, int64_t N, int64_t K, int32_t groups) {
+    return matmul_sizes_ok(M, N, K, groups) && K < (int64_t(1) << 17);
+}
+
+bool row_dims_ok(const moe_dims* d) {
+    return d && d->num_tokens >= 0 && d->topk >= 1 && d->topk <= kRowTopk && (int64_t)d->num_tokens * d->topk <= kMaxSlots;
+}
+
+// H columns of rows `stride` apart
+bool rows_ok(int64_t rows, int64_t H, int64_t stride) {
+    return H >= 1 && H <= (int64_t(1) << 30) && stride >= H && extent_ok(rows, stride);
+}
+
 bool layer_dims_ok(const moe_dims* d, int weights) {
     return dims_ok(d, MOE_A16W16) && weights >= MOE_LAYER_BF16 && weights <= MOE_LAYER_FP4_MX;
 }
@@ -89,6 +103,98 @@ moe_status moe_fp8_matmul(const moe_fp8_matmul_args* a, void* workspace, size_t 
         return MOE_ERR_INVALID_ARG;
     if (!workspace_ok(workspace, workspace_bytes, fp8_matmul_workspace(a->M, a->N, a->K, a->groups))) return MOE_ERR_WORKSPACE;
     return from_cuda(launch_fp8_matmul(*a, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_permute_workspace_bytes(const moe_dims* d) {
+    return row_dims_ok(d) && d->num_experts >= 1 && d->num_experts <= kRowExperts ? sizeof(int32_t) * kOpsHeaderInts : 0;
+}
+
+moe_status moe_permute(const moe_permute_args* a, const moe_dims* d, void* workspace, size_t workspace_bytes,
+                       moe_stream_t stream) {
+    const size_t need = moe_permute_workspace_bytes(d);
+    if (!a || need == 0 || (!type_ok(a->type) && a->type != MOE_TYPE_CODES8)) return MOE_ERR_INVALID_ARG;
+    const int T = d->num_tokens, K = d->topk;
+    if (!rows_ok(T, a->H, a->x_stride) || !rows_ok((int64_t)T * K, a->H, a->rows_stride)) return MOE_ERR_INVALID_ARG;
+    if (a->scale && (a->scales < 0 || a->scales > (1 << 20))) return MOE_ERR_INVALID_ARG;
+    if (!a->offsets || !aligned(a->offsets, 4)) return MOE_ERR_INVALID_ARG;
+    const uintptr_t size = a->type == MOE_TYPE_CODES8 ? 1 : type_bytes(a->type);
+    if (T > 0) {
+        if (!a->x || !a->topk_ids || !a->rows || !a->row_src || !a->slot_row || (a->scale && !a->row_scale))
+            return MOE_ERR_INVALID_ARG;
+        if (!aligned(a->x, size) || !aligned(a->rows, size)) return MOE_ERR_INVALID_ARG;
+        for (const void* p : {(const void*)a->scale, (const void*)a->row_scale, (const void*)a->topk_ids, (const void*)a->row_src,
+                              (const void*)a->slot_row})
+            if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
+    }
+    if (!workspace_ok(workspace, workspace_bytes, need)) return MOE_ERR_WORKSPACE;
+    return from_cuda(launch_permute(*a, T, K, d->num_experts, static_cast<int32_t*>(workspace),
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_unpermute(const void* rows, moe_type type, int64_t rows_stride, const int32_t* slot_row, const float* topk_weights,
+                         const moe_dims* d, int64_t H, void* y, moe_type y_type, int64_t y_stride, moe_stream_t stream) {
+    if (!row_dims_ok(d) || !type_ok(type) || !type_ok(y_type)) return MOE_ERR_INVALID_ARG;
+    const int T = d->num_tokens, K = d->topk;
+    if (!rows_ok((int64_t)T * K, H, rows_stride) || !rows_ok(T, H, y_stride)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!rows || !slot_row || !y || !aligned(rows, type_bytes(type)) || !aligned(y, type_bytes(y_type)) || !aligned(slot_row, 4) ||
+        !aligned(topk_weights, 4))
+        return MOE_ERR_INVALID_ARG;
+    UnpermuteArgs u = {};
+    u.rows = rows, u.slot_row = slot_row, u.weights = topk_weights, u.out = y;
+    u.H = H, u.rows_stride = rows_stride, u.out_stride = y_stride;
+    u.T = T, u.K = K, u.type = type, u.token_type = y_type;
+    return from_cuda(launch_unpermute(u, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_unpermute_backward(const void* dy, moe_type dy_type, int64_t dy_stride, const void* rows, moe_type type,
+                                  int64_t rows_stride, const int32_t* slot_row, const float* topk_weights, const moe_dims* d,
+                                  int64_t H, void* d_rows, int64_t d_rows_stride, float* d_weights, moe_stream_t stream) {
+    if (!row_dims_ok(d) || !type_ok(type) || !type_ok(dy_type)) return MOE_ERR_INVALID_ARG;
+    const int T = d->num_tokens, K = d->topk;
+    if (!rows_ok(T, H, dy_stride) || !rows_ok((int64_t)T * K, H, d_rows_stride)) return MOE_ERR_INVALID_ARG;
+    if (d_weights && !rows_ok((int64_t)T * K, H, rows_stride)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!dy || !slot_row || !d_rows || (d_weights && !rows)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(dy, type_bytes(dy_type)) || (d_weights && !aligned(rows, type_bytes(type))) || !aligned(d_rows, type_bytes(type)) ||
+        !aligned(slot_row, 4) || !aligned(topk_weights, 4) || !aligned(d_weights, 4))
+        return MOE_ERR_INVALID_ARG;
+    UnpermuteArgs u = {};
+    u.rows = d_weights ? rows : nullptr, u.slot_row = slot_row, u.weights = topk_weights, u.dy = dy, u.out = d_rows;
+    u.d_weights = d_weights;
+    u.H = H, u.rows_stride = rows_stride, u.dy_stride = dy_stride, u.out_stride = d_rows_stride;
+    u.T = T, u.K = K, u.type = type, u.token_type = dy_type;
+    return from_cuda(launch_unpermute_backward(u, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_int8_quantize(const void* x, moe_type type, int64_t rows, int64_t cols, int64_t x_stride, void* q, int64_t q_stride,
+                             float* scale, moe_stream_t stream) {
+    if (!type_ok(type) || rows < 0 || cols < 0 || (cols == 0 && rows > 0) || x_stride < cols || q_stride < cols ||
+        cols > (int64_t(1) << 30) || !extent_ok(rows, x_stride) || !extent_ok(rows, q_stride))
+        return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scale || !aligned(x, type_bytes(type)) || !aligned(scale, 4)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_int8_quantize(x, type, rows, cols, x_stride, static_cast<int8_t*>(q), q_stride, scale,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_int8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t groups) {
+    return int8_sizes_ok(M, N, K, groups) ? int8_matmul_workspace(M, N, K, groups) : 0;
+}
+
+moe_status moe_int8_matmul(const moe_int8_matmul_args* a, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+    if (!a || !int8_sizes_ok(a->M, a->N, a->K, a->groups) || !type_ok(a->out_type)) return MOE_ERR_INVALID_ARG;
+    if (a->a_stride < a->K || a->b_stride < a->K || a->out_stride < a->N || a->a_stride % 16 || a->b_stride % 16)
+        return MOE_ERR_INVALID_ARG;
+    if (!extent_ok(a->M, a->a_stride) || !extent_ok(a->N * a->groups, a->b_stride) || !extent_ok(a->M, a->out_stride))
+        return MOE_ERR_INVALID_ARG;
+    if (a->groups > 1 && !a->offsets) return MOE_ERR_INVALID_ARG;
+    if (a->M == 0) return MOE_OK;
+    if (!a->a || !a->a_scale || !a->b || !a->b_scale || !a->out || !aligned(a->a, 16) || !aligned(a->b, 16) ||
+        !aligned(a->a_scale, 4) || !aligned(a->b_scale, 4) || !aligned(a->offsets, 4) || !aligned(a->out, type_bytes(a->out_type)))
+        return MOE_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, int8_matmul_workspace(a->M, a->N, a->K, a->groups))) return MOE_ERR_WORKSPACE;
+    return from_cuda(launch_int8_matmul(*a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_layer_workspace_bytes(const moe_dims* d, moe_layer_weights weights) {
