@@ -242,8 +242,9 @@ MOE_API moe_status moe_unpermute_backward(const void* dy, moe_type dy_type, int6
  * 8-bit integers with a scale for each row
  * ------------------------------------------------------------------------------------------------------ */
 
-/* Rows of x in int8 with an fp32 scale each, as MOE_A8W8_INT8 has its activations (moe_dispatch_quantize):
- *   s = max(amax / 127, 1e-8), q = x / s rounded half to even, within [-127, 127]: fp32 IEEE division.
+/* Rows of x in int8 with an fp32 scale each, in the format of MOE_A8W8_INT8's x:
+ *   s = max(amax * c, 1e-8), c the fp32 number nearest to 1/127;  q = x / s rounded half to even, within [-127, 127].
+ * All fp32, the quotient IEEE's. (moe_dispatch_quantize divides by 127: its s may be one unit in the last place away.)
  * A row that holds a NaN or an infinity gets a NaN or infinite scale and zeros, so products with it are not finite.
  *   x      device [rows, cols] of `type` (bf16 or fp32), x_stride >= cols elements apart
  *   q      device int8 [rows, cols], q_stride >= cols apart;    scale  device fp32 [rows]

@@ -1,6 +1,9 @@
 // Rows of x in int8 with a scale each (moe_int8_quantize in moe_ops.h). A CTA has a row: its values stay in registers between the largest
-// magnitude and the codes, where they fit (rows of up to kThreads * 32 values), so x is read once. Bound by HBM: 2 (bf16) or 4 (fp32)
-// bytes read and 1 written an element.
+// magnitude and the codes, where they fit, so x is read once. Bound by HBM: 2 (bf16) or 4 (fp32) bytes read and 1 written an
+// element. That takes the division out of the way: x / s is Markstein's quotient from r = 1/s rounded to nearest (y = x r, then
+// y + r (x - y s) with fused multiply-adds is x / s rounded to nearest wherever nothing under- or overflows; s >= 1e-8 and
+// r >= 2^-122, so that only quotients far below one half do, whose code is 0 all the same), and adding 1.5 * 2^23 rounds it half to
+// even into the low bits. |x| / s is at most 127 (1 + 2^-22), so no code passes 127.
 #include <algorithm>
 
 #include "common.cuh"
@@ -13,87 +16,106 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T v) {
-    if constexpr (sizeof(T) == 2) return __bfloat162float(v);
-    else return v;
-}
-
-// kPer values of a thread from column c on (all of them, or the row's last ones)
-template <typename T, int kPer>
-__device__ __forceinline__ void load(const T* row, int64_t c, int64_t cols, float (&v)[kPer]) {
-    if constexpr (kPer == 1) {
-        v[0] = c < cols ? to_f32(row[c]) : 0.0f;
-    } else {
-        constexpr int kW = 16 / sizeof(T);
+// kPer values of a thread, as they lie in memory: kVec 16 bytes of x, else one value
+template <typename T, bool kVec>
+struct Part {
+    static constexpr int kPer = kVec ? 16 / sizeof(T) : 1;
+    uint32_t w[kVec ? 4 : 1];
+    __device__ __forceinline__ void load(const T* row, int64_t c, int64_t cols) {
+        if (c >= cols) {
 #pragma unroll
-        for (int j = 0; j < kPer / kW; ++j) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (c < cols) w = __ldg(reinterpret_cast<const uint4*>(row + c) + j);
-            const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-            for (int k = 0; k < kW; ++k) v[j * kW + k] = to_f32(e[k]);
+            for (uint32_t& u : w) u = 0;
+        } else if constexpr (kVec) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + c));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else if constexpr (sizeof(T) == 2) {
+            w[0] = (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row + c)) << 16;
+        } else {
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(row + c));
         }
     }
-}
-
-template <int kPer>
-__device__ __forceinline__ void put(int8_t* row, int64_t c, int64_t cols, const float (&v)[kPer], float s) {
-    if (c >= cols) return;
-    uint32_t word[(kPer + 3) / 4] = {};
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const float q = fminf(fmaxf(rintf(__fdiv_rn(v[j], s)), -127.0f), 127.0f);
-        if (s < INFINITY) word[j / 4] |= ((uint32_t)(int)q & 0xffu) << (8 * (j % 4));
+    __device__ __forceinline__ uint32_t bits(int i) const {  // of value i in fp32; i known when compiled
+        if constexpr (!kVec || sizeof(T) == 4) return w[i];
+        else return i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16;
     }
-    if constexpr (kPer == 1) row[c] = (int8_t)word[0];
-    else *reinterpret_cast<uint2*>(row + c) = make_uint2(word[0], word[1]);
+};
+
+// low byte: the code
+__device__ __forceinline__ uint32_t code(float x, float s, float r) {
+    const float y = __fmul_rn(x, r);
+    return __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-y, s, x), r, y), 12582912.0f));
 }
 
-// kPer: values of a thread at a time (8 where rows of x start on 16 bytes, those of q on 8, and both have a multiple of 8 of
-// them; else 1); kHold: how often it has some at most, 0: rows of any length, read twice
-template <typename T, int kPer, int kHold>
+template <typename T, bool kVec>
+__device__ __forceinline__ void put(int8_t* row, int64_t c, int64_t cols, const Part<T, kVec>& v, float s, float r, bool finite) {
+    if (c >= cols) return;
+    if constexpr (kVec) {
+        constexpr int kWords = Part<T, kVec>::kPer / 4;
+        uint32_t word[kWords];
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = code(__uint_as_float(v.bits(4 * j + i)), s, r);
+            word[j] = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+            if (!finite) word[j] = 0;
+        }
+        if constexpr (kWords == 1) *reinterpret_cast<uint32_t*>(row + c) = word[0];
+        else *reinterpret_cast<uint2*>(row + c) = make_uint2(word[0], word[1]);
+    } else {
+        row[c] = finite ? (int8_t)code(__uint_as_float(v.bits(0)), s, r) : 0;
+    }
+}
+
+// kHold: parts of a thread at most (all of them in registers); 0: rows of any length, read twice
+template <typename T, bool kVec, int kHold>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const T* __restrict__ x, int64_t cols, int64_t x_stride, int8_t* __restrict__ q, int64_t q_stride,
                     float* __restrict__ scale, int64_t rows) {
-    __shared__ uint32_t best[kThreads / 32];
+    using P = Part<T, kVec>;
+    constexpr int kStep = kThreads * P::kPer;
+    __shared__ uint32_t best[2][kThreads / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
         const T* src = x + r * x_stride;
+        int8_t* dst = q + r * q_stride;
+        const int64_t c0 = threadIdx.x * P::kPer;
         // the largest magnitude as an integer: infinities and NaNs are above every number and survive
         uint32_t top = 0;
-        auto look = [&](const float (&v)[kPer]) {
+        auto look = [&](const P& v) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+            for (int i = 0; i < P::kPer; ++i) top = max(top, v.bits(i) & 0x7fffffffu);
         };
-        float v[kHold > 0 ? kHold : 1][kPer];
+        P v[kHold > 0 ? kHold : 1];
         if constexpr (kHold > 0) {
 #pragma unroll
-            for (int h = 0; h < kHold; ++h) load<T, kPer>(src, ((int64_t)h * kThreads + threadIdx.x) * kPer, cols, v[h]);
+            for (int h = 0; h < kHold; ++h) v[h].load(src, c0 + h * kStep, cols);
 #pragma unroll
             for (int h = 0; h < kHold; ++h) look(v[h]);
         } else {
-            for (int64_t c = threadIdx.x * kPer; c < cols; c += kThreads * kPer) {
-                load<T, kPer>(src, c, cols, v[0]);
+            for (int64_t c = c0; c < cols; c += kStep) {
+                v[0].load(src, c, cols);
                 look(v[0]);
             }
         }
         top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) best[warp] = top;
-        __syncthreads();
+        if (lane == 0) best[turn][warp] = top;
+        __syncthreads();  // (two sets of words in turn: the next row's are written before every warp has read these)
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) top = max(top, best[w]);
-        __syncthreads();
-        float s = __fdiv_rn(__uint_as_float(top), 127.0f);
+        for (int w = 0; w < kThreads / 32; ++w) top = max(top, best[turn][w]);
+        float s = __fmul_rn(__uint_as_float(top), 1.0f / 127.0f);
         if (s < 1e-8f) s = 1e-8f;
+        const bool finite = s < INFINITY;
+        const float inv = __fdiv_rn(1.0f, s);
         if (threadIdx.x == 0) scale[r] = s;
         if constexpr (kHold > 0) {
 #pragma unroll
-            for (int h = 0; h < kHold; ++h) put<kPer>(q + r * q_stride, ((int64_t)h * kThreads + threadIdx.x) * kPer, cols, v[h], s);
+            for (int h = 0; h < kHold; ++h) put(dst, c0 + h * kStep, cols, v[h], s, inv, finite);
         } else {
-            for (int64_t c = threadIdx.x * kPer; c < cols; c += kThreads * kPer) {
-                load<T, kPer>(src, c, cols, v[0]);
-                put<kPer>(q + r * q_stride, c, cols, v[0], s);
+            for (int64_t c = c0; c < cols; c += kStep) {
+                v[0].load(src, c, cols);
+                put(dst, c, cols, v[0], s, inv, finite);
             }
         }
     }
@@ -103,19 +125,22 @@ template <typename T>
 cudaError_t launch(const T* x, int64_t rows, int64_t cols, int64_t x_stride, int8_t* q, int64_t q_stride, float* scale,
                    cudaStream_t s) {
     const unsigned grid = (unsigned)std::min<int64_t>(rows, 0x7fffffff);
+    constexpr int kPer = 16 / sizeof(T);
+    // 16 bytes of x and as many codes at a time where every row starts on such vectors and has whole ones
     const bool vec = !((reinterpret_cast<uintptr_t>(x) | (uint64_t)(x_stride * (int64_t)sizeof(T))) & 15) &&
-                     !((reinterpret_cast<uintptr_t>(q) | (uint64_t)q_stride | (uint64_t)cols) & 7);
-#define MOE_QUANT(per, hold) quantize_kernel<T, per, hold><<<grid, kThreads, 0, s>>>(x, cols, x_stride, q, q_stride, scale, rows)
-    const int64_t times = (cols + kThreads * (vec ? 8 : 1) - 1) / (kThreads * (vec ? 8 : 1));
+                     !((reinterpret_cast<uintptr_t>(q) | (uint64_t)q_stride | (uint64_t)cols) & (kPer - 1));
+    const int64_t step = kThreads * (vec ? kPer : 1), parts = (cols + step - 1) / step;
+#define MOE_QUANT(vec, hold) quantize_kernel<T, vec, hold><<<grid, kThreads, 0, s>>>(x, cols, x_stride, q, q_stride, scale, rows)
     if (vec) {
-        if (times <= 1) MOE_QUANT(8, 1);
-        else if (times <= 2) MOE_QUANT(8, 2);
-        else if (times <= 4) MOE_QUANT(8, 4);
-        else MOE_QUANT(8, 0);
+        if (parts <= 1) MOE_QUANT(true, 1);
+        else if (parts <= 2) MOE_QUANT(true, 2);
+        else if (parts <= 4) MOE_QUANT(true, 4);
+        else if (parts <= 8) MOE_QUANT(true, 8);
+        else MOE_QUANT(true, 0);
     } else {
-        if (times <= 8) MOE_QUANT(1, 8);
-        else if (times <= 32) MOE_QUANT(1, 32);
-        else MOE_QUANT(1, 0);
+        if (parts <= 8) MOE_QUANT(false, 8);
+        else if (parts <= 32) MOE_QUANT(false, 32);
+        else MOE_QUANT(false, 0);
     }
 #undef MOE_QUANT
     return cudaGetLastError();

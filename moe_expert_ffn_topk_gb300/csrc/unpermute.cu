@@ -16,40 +16,51 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
-// N consecutive elements of T: one vector where they are 16 bytes (or two, fp32 opposite bf16), else one by one
+// N consecutive elements of T as they lie in memory: a lane holds these while its loads are on their way
 template <typename T, int N>
-__device__ __forceinline__ void load(const T* p, float (&v)[N]) {
-    if constexpr (N == 1) {
-        if constexpr (sizeof(T) == 2) v[0] = bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(p)));
-        else v[0] = __ldg(reinterpret_cast<const float*>(p));
-    } else if constexpr (sizeof(T) == 2) {
-        static_assert(N == 8, "one vector");
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Packed {
+    static constexpr int kBytes = N * (int)sizeof(T);
+    static_assert(N == 1 || kBytes % 8 == 0, "whole vectors");
+    uint32_t w[kBytes < 4 ? 1 : kBytes / 4];
+
+    // zeros where `on` is false. Predicated loads, not branches: the compiler joined a branch around a load with that around its
+    // use, and a warp had one load on its way instead of eight
+    __device__ __forceinline__ void load(const T* p, bool on) {
+        if constexpr (kBytes == 2) {
+            uint16_t v;
+            asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}" : "=h"(v) : "l"(p), "r"((int)on));
+            w[0] = v;
+        } else if constexpr (kBytes == 4) {
+            asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}" : "=r"(w[0]) : "l"(p), "r"((int)on));
+        } else if constexpr (kBytes == 8) {
+            asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+                : "=r"(w[0]), "=r"(w[1])
+                : "l"(p), "r"((int)on));
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(u[j] << 16);
-            v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < N / 4; ++j) {
-            const float4 w = __ldg(reinterpret_cast<const float4*>(p) + j);
-            v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
+            for (int j = 0; j < kBytes / 16; ++j)
+                asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                    "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                    : "=r"(w[4 * j]), "=r"(w[4 * j + 1]), "=r"(w[4 * j + 2]), "=r"(w[4 * j + 3])
+                    : "l"(reinterpret_cast<const uint4*>(p) + j), "r"((int)on));
         }
     }
-}
+    __device__ __forceinline__ float at(int i) const {  // i known when compiled
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
 
 template <typename T, int N>
 __device__ __forceinline__ void store(T* p, const float (&v)[N]) {
-    if constexpr (N == 1) {
-        if constexpr (sizeof(T) == 2) *reinterpret_cast<uint16_t*>(p) = float_to_bf16_bits(v[0]);
-        else *reinterpret_cast<float*>(p) = v[0];
-    } else if constexpr (sizeof(T) == 2) {
-        uint32_t u[4];
+    if constexpr (N == 1 && sizeof(T) == 2) *reinterpret_cast<uint16_t*>(p) = float_to_bf16_bits(v[0]);
+    else if constexpr (N == 1) *reinterpret_cast<float*>(p) = v[0];
+    else if constexpr (sizeof(T) == 2) {
+        uint32_t u[N / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = (uint32_t)float_to_bf16_bits(v[2 * j]) | ((uint32_t)float_to_bf16_bits(v[2 * j + 1]) << 16);
-        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        for (int j = 0; j < N / 2; ++j) u[j] = (uint32_t)float_to_bf16_bits(v[2 * j]) | ((uint32_t)float_to_bf16_bits(v[2 * j + 1]) << 16);
+        if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+        else *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
 #pragma unroll
         for (int j = 0; j < N / 4; ++j)
@@ -63,36 +74,50 @@ __device__ __forceinline__ int slot_row_of(const UnpermuteArgs& p, int64_t slot,
     return r >= 0 && r < p.T * p.K ? r : -1;
 }
 
+// A warp's item is a token's run of `per` segments of 32 * N columns; the next item's slots and weights are on their way while one is
+// worked on (an item's own are a load that its rows' loads wait for).
 template <typename R, typename Y, int N>
-__global__ void __launch_bounds__(kThreads) unpermute_kernel(UnpermuteArgs p, int64_t segments) {
+__global__ void __launch_bounds__(kThreads, 3) unpermute_kernel(UnpermuteArgs p, int64_t parts, int64_t per) {
     const int lane = threadIdx.x & 31;
-    const int64_t items = p.T * segments;
-    for (int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = item / segments, c = (item - t * segments) * (32 * N) + lane * N;
-        const int my_row = slot_row_of(p, t * p.K + lane, lane < p.K);
-        const float my_w = p.weights && my_row >= 0 ? __ldg(p.weights + t * p.K + lane) : 1.0f;
-        const R* rows = static_cast<const R*>(p.rows);
-        float acc[N];
+    const int64_t items = p.T * parts, step = (int64_t)gridDim.x * kWarps;
+    int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const R* rows = static_cast<const R*>(p.rows);
+    int next_row = -1;
+    float next_w = 0.0f;
+    auto fetch = [&](int64_t i) {
+        const int64_t slot = i / parts * p.K + lane;
+        const bool there = i < items && lane < p.K;
+        next_row = slot_row_of(p, slot, there);
+        next_w = p.weights && there ? __ldg(p.weights + slot) : 1.0f;
+    };
+    fetch(item);
+    for (; item < items; item += step) {
+        const int64_t t = item / parts, c0 = (item - t * parts) * per * (32 * N);
+        const int my_row = next_row;
+        const float my_w = my_row >= 0 ? next_w : 0.0f;
+        fetch(item + step);
+        const int64_t c1 = min(p.H, c0 + per * (32 * N));
+        for (int64_t c = c0 + lane * N; c - lane * N < c1; c += 32 * N) {
+            float acc[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-        constexpr int kBatch = 8;  // rows on their way
-        for (int k0 = 0; k0 < p.K; k0 += kBatch) {
-            float v[kBatch][N], w[kBatch];
-            int r[kBatch];
+            for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+            constexpr int kBatch = 8;  // rows on their way
+            for (int k0 = 0; k0 < p.K; k0 += kBatch) {
+                Packed<R, N> v[kBatch];
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                r[b] = __shfl_sync(0xffffffffu, my_row, (k0 + b) & 31);
-                w[b] = __shfl_sync(0xffffffffu, my_w, (k0 + b) & 31);
-                if (k0 + b >= p.K) r[b] = -1;
-                if (r[b] >= 0 && c < p.H) load<R, N>(rows + (int64_t)r[b] * p.rows_stride + c, v[b]);
+                for (int b = 0; b < kBatch; ++b) {
+                    const int r = __shfl_sync(0xffffffffu, my_row, (k0 + b) & 31);
+                    v[b].load(rows + (int64_t)r * p.rows_stride + c, r >= 0 && k0 + b < p.K && c < c1);
+                }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {  // (a slot without a row: 0 * 0)
+                    const float w = __shfl_sync(0xffffffffu, my_w, (k0 + b) & 31);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) acc[j] = __fmaf_rn(w, v[b].at(j), acc[j]);
+                }
             }
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-                if (r[b] >= 0 && c < p.H)
-#pragma unroll
-                    for (int j = 0; j < N; ++j) acc[j] = __fmaf_rn(w[b], v[b][j], acc[j]);
+            if (c < c1) store<Y, N>(static_cast<Y*>(p.out) + t * p.out_stride + c, acc);
         }
-        if (c < p.H) store<Y, N>(static_cast<Y*>(p.out) + t * p.out_stride + c, acc);
     }
 }
 
@@ -111,14 +136,13 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(UnpermuteArgs p) {
         R* out = static_cast<R*>(p.out) + (int64_t)row * p.out_stride;
         constexpr int kBatch = 4;
         for (int64_t c0 = (int64_t)sub * 32 * N * kBatch; c0 < p.H; c0 += (int64_t)G * 32 * N * kBatch) {
-            float a[kBatch][N], b[kBatch][N];
+            Packed<Y, N> a[kBatch];
+            Packed<R, N> b[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const int64_t c = c0 + (j * 32 + lane) * N;
-                if (c < p.H) {
-                    load<Y, N>(dy + c, a[j]);
-                    if (p.d_weights) load<R, N>(in + c, b[j]);
-                }
+                a[j].load(dy + c, c < p.H);
+                b[j].load(in + c, p.d_weights && c < p.H);
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
@@ -126,10 +150,11 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(UnpermuteArgs p) {
                 if (c >= p.H) continue;
                 if (p.d_weights)
 #pragma unroll
-                    for (int i = 0; i < N; ++i) dot = __fmaf_rn(a[j][i], b[j][i], dot);
+                    for (int i = 0; i < N; ++i) dot = __fmaf_rn(a[j].at(i), b[j].at(i), dot);
+                float grad[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) a[j][i] *= w;
-                store<R, N>(out + c, a[j]);
+                for (int i = 0; i < N; ++i) grad[i] = a[j].at(i) * w;
+                store<R, N>(out + c, grad);
             }
         }
     }
@@ -148,8 +173,12 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(UnpermuteArgs p) {
 
 template <typename R, typename Y, int N>
 cudaError_t launch_forward(const UnpermuteArgs& a, cudaStream_t s) {
-    const int64_t segments = (a.H + 32 * N - 1) / (32 * N), ctas = (a.T * segments + kWarps - 1) / kWarps;
-    unpermute_kernel<R, Y, N><<<(unsigned)std::min<int64_t>(ctas, 0x7fffffff), kThreads, 0, s>>>(a, segments);
+    const int64_t segments = (a.H + 32 * N - 1) / (32 * N), resident = (int64_t)tc_num_sms() * 3 * kWarps;
+    // longer runs a warp where that leaves every resident warp several items
+    int64_t per = 1;
+    while (per < 4 && per * 2 <= segments && a.T * ((segments + 2 * per - 1) / (2 * per)) >= 8 * resident) per *= 2;
+    const int64_t parts = (segments + per - 1) / per, ctas = (a.T * parts + kWarps - 1) / kWarps;
+    unpermute_kernel<R, Y, N><<<(unsigned)std::min<int64_t>(ctas, resident / kWarps), kThreads, 0, s>>>(a, parts, per);
     return cudaGetLastError();
 }
 
@@ -162,7 +191,7 @@ cudaError_t launch_back(const UnpermuteArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// eight columns at a time where every row of either matrix starts on 16 bytes and has a multiple of eight
+// 16 bytes of a row at a time where every row of either matrix starts on 16 bytes and has a multiple of eight columns
 bool vectors(const UnpermuteArgs& a) {
     const uint64_t r = a.type == MOE_TYPE_BF16 ? 2 : 4, t = a.token_type == MOE_TYPE_BF16 ? 2 : 4;
     const bool back = a.dy != nullptr;
@@ -175,8 +204,8 @@ bool vectors(const UnpermuteArgs& a) {
 
 template <bool kBack, typename R, typename Y>
 cudaError_t launch_ry(const UnpermuteArgs& a, cudaStream_t s) {
-    if constexpr (kBack) return vectors(a) ? launch_back<R, Y, 8>(a, s) : launch_back<R, Y, 1>(a, s);
-    else return vectors(a) ? launch_forward<R, Y, 8>(a, s) : launch_forward<R, Y, 1>(a, s);
+    if constexpr (kBack) return vectors(a) ? launch_back<R, Y, 16 / sizeof(R)>(a, s) : launch_back<R, Y, 1>(a, s);
+    else return vectors(a) ? launch_forward<R, Y, 16 / sizeof(R)>(a, s) : launch_forward<R, Y, 1>(a, s);
 }
 
 template <bool kBack>

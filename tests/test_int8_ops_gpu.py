@@ -28,7 +28,7 @@ def gen(seed):
 def quantize_by_definition(x):
     """On the host, fp32 throughout (torch's CPU division is IEEE's)."""
     v = x.float().cpu()
-    scale = torch.clamp_min(v.abs().amax(-1) / torch.tensor(127.0), torch.tensor(1e-8))
+    scale = torch.clamp_min(v.abs().amax(-1) * torch.tensor(1.0 / 127.0), torch.tensor(1e-8))
     return torch.round(v / scale[:, None]).clamp(-127, 127).to(torch.int8), scale
 
 
