@@ -28,6 +28,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "group_tiles.cuh"
 #include "ops.h"
 #include "tc_common.cuh"
 
@@ -87,20 +88,8 @@ struct Tile {
 
 template <class C>
 __device__ __forceinline__ Tile decode(int64_t t, const int* tab, int groups, int n_tiles) {
-    const int *off = tab, *lo = tab + groups + 1, *hi = lo + groups;
-    int a = 0, b = groups - 1;
-    while (a < b) {
-        const int mid = (a + b + 1) >> 1;
-        if ((int64_t)off[mid] * n_tiles <= t) a = mid; else b = mid - 1;
-    }
-    const int mt = off[a + 1] - off[a];
-    const int64_t local = t - (int64_t)off[a] * n_tiles;
-    Tile tl;
-    tl.g = a;
-    tl.n0 = (int)(local / mt) * C::kBN;
-    tl.row0 = lo[a] + (int)(local % mt) * C::kTileRows;
-    tl.hi = hi[a];
-    return tl;
+    const GroupTile f = find_group_tile(t, tab, groups, n_tiles, C::kTileRows);
+    return {f.g, f.n_tile * C::kBN, f.row0, f.hi};
 }
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, bool pair) {
@@ -190,40 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kb0 = kPair ? 0 : (int)((int64_t)p.kb_count * rank / split);
     const int kb1 = kPair ? p.kb_count : (int)((int64_t)p.kb_count * (rank + 1) / split);
 
-    if (warp == 2) {
-        // tile_off: exclusive prefix sum of the groups' row tiles, one warp scan per 32 groups
-        // (offsets are taken into [0, M], and one below an earlier one as that one: the groups' rows never overlap)
-        int *lo = tab + p.groups + 1, *hi = lo + p.groups, carry = 0;
-        int last = p.offsets ? min(max(__ldg(p.offsets), 0), p.M) : 0;  // where the groups so far end
-        for (int b = 0; b < p.groups; b += 32) {
-            const int g = b + lane;
-            int h = p.M;
-            if (p.offsets) h = g < p.groups ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : 0;
-            if (lane == 0) h = max(h, last);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, h, o);
-                if (lane >= o) h = max(h, u);
-            }
-            const int before = __shfl_up_sync(0xffffffffu, h, 1);
-            const int l = lane == 0 ? last : before;
-            last = __shfl_sync(0xffffffffu, h, 31);
-            int v = 0;
-            if (g < p.groups) {
-                lo[g] = l;
-                hi[g] = h;
-                v = h > l ? (h - l - 1) / C::kTileRows + 1 : 0;
-            }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            if (g < p.groups) tab[g + 1] = carry + v;
-            carry += __shfl_sync(0xffffffffu, v, 31);
-        }
-        if (lane == 0) tab[0] = 0;
-    }
+    if (warp == 2) write_group_tiles(p.offsets, p.M, p.groups, C::kTileRows, tab, lane);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full_bar(s), 1);

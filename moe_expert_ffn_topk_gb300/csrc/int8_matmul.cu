@@ -1,7 +1,29 @@
-// Product of int8 matrices with a scale for each row of either (moe_int8_matmul in moe_ops.h).
+// Product of int8 matrices with a scale for each row of either (moe_int8_matmul in moe_ops.h):
+//
+//     out[m,n] = (C[m,n] * b_scale[n]) * a_scale[m],   C = a . b^T exactly
+//
+// The chip has no integer kind of tcgen05.mma, and mma.sync on int8 and dp4a both run at 150 TOP/s, a sixteenth of the f16 rate. So the
+// codes are multiplied as f16 numbers, which hold them exactly: a product is below 2^14 in magnitude and an fp32 sum of 1024 of
+// them at most 2^24, still an exact integer. At least every 1024 of K the sums are taken out of tensor memory and added up as
+// integers in registers, which makes C exact for every input.
+//
+// Codes become f16 inside the kernel, on their way from shared memory: the operands are read from HBM as bytes, and neither a pass of its
+// own nor twice the traffic is needed. Of the two operands the weights (rows of b, the M side of the MMA) go to tensor
+// memory, which the MMA takes its first operand from, and the tokens (rows of a, the N side) back to shared memory: what
+// bounds such a kernel is shared memory's 128 bytes a cycle (bytes in by TMA, out to the converters, f16 tokens in, and out to the
+// MMA), and weights that went back too would add half as much again.
+//
+// Warp roles (640 threads): warp 0 TMA producer, warp 1 tensor-memory allocator and MMA issuer, warp 2 the groups' table, warps
+// 4-11 take sums out and write results, warps 12-15 convert weights (a row a lane), 16-19 tokens.
+//
+// Every wait is bounded (2 s); on time-out the CTA records MOE_ERR_TIMEOUT and leaves its loops.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
 #include <algorithm>
 
 #include "common.cuh"
+#include "group_tiles.cuh"
 #include "ops.h"
 #include "tc_common.cuh"
 
@@ -9,45 +31,632 @@ namespace moe {
 
 namespace {
 
-template <typename Out>
-__global__ void __launch_bounds__(256) simple_kernel(moe_int8_matmul_args p) {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= p.N) return;
-    for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
-        int g = 0;
-        if (p.offsets) {
-            int end = min(max(__ldg(p.offsets), 0), (int)p.M);
-            for (g = 0; g < p.groups; ++g) {
-                end = max(end, min(max(__ldg(p.offsets + g + 1), 0), (int)p.M));
-                if (m < end) break;
-            }
-            if (g == p.groups || m < min(max(__ldg(p.offsets), 0), (int)p.M)) continue;
+using namespace tc;
+
+constexpr int kThreads = 640;
+constexpr int kEpiWarps = 8, kConvWarps = 8;
+// registers of warps 0-3, 4-11 and 12-19: 128 * 32 + 256 * 160 + 256 * 64 = 640 * 96, what the launch holds
+constexpr int kLaunchRegs = 96, kFewRegs = 32, kEpiRegs = 160, kConvRegs = 64;
+static_assert(128 * kFewRegs + 256 * kEpiRegs + 256 * kConvRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kMaxGroups = 1024;
+constexpr int kTmemCols = 512;
+constexpr int kStageK = 128;                 // codes of K in a stage
+constexpr int kChunkStages = 1024 / kStageK; // stages of an exact fp32 sum
+
+struct Args {
+    const float* a_scale;
+    const float* b_scale;
+    const int32_t* offsets;
+    void* out;
+    int32_t* hdr;
+    int64_t out_stride;
+    int M, N, groups, kb_count;
+    int n_tiles;
+    int split;  // CTAs of a cluster that share a tile's stages (one-CTA tiles without groups only)
+};
+
+// A tile is 128 * kCtas weight rows by kHalves * kN tokens. kCtas 2: a pair of CTAs (cta_group::2), each holding 128 of the weight rows
+// and half of the tokens of every MMA. kHalves 2: two MMAs of kN tokens a step, each with a sum of its own; 1: one, whose
+// sum changes between two buffers from chunk to chunk. kRaw, kOps: stages of bytes, and of f16 operands.
+template <int kCtas_, int kN_, int kHalves_, int kRaw_, int kOps_>
+struct Cfg {
+    static constexpr int kCtas = kCtas_, kN = kN_, kHalves = kHalves_, kRaw = kRaw_, kOps = kOps_;
+    static constexpr int kTokens = kN * kHalves;
+    static constexpr int kBRows = kTokens / kCtas, kHalfRows = kN / kCtas;
+    static constexpr int kRawA = 128 * kStageK, kRawBytes = kRawA + kBRows * kStageK;
+    static constexpr int kOpBytes = 2 * kBRows * kStageK, kAtomBytes = kOpBytes / 2;  // two swizzled atoms of 64 of K
+    static constexpr int kOpOff = kRaw * kRawBytes;
+    static constexpr int kBarOff = kOpOff + kOps * kOpBytes;
+    static constexpr int kNumBars = 2 * kRaw + 2 * kOps + 5;
+    static constexpr int kMiscOff = kBarOff + 8 * ((kNumBars + 1) & ~1);
+    static constexpr int kTabOff = kMiscOff + 16;
+    static constexpr size_t kSmem = 1024 + (size_t)kTabOff + 4 * (3 * kMaxGroups + 4);
+    static constexpr int kCols = kHalves == 2 ? kN : kN / 2;  // sums of a lane of the epilogue
+    static constexpr int kTmemA = 2 * kN;                     // first column of the weights' stages, 64 columns each
+    static constexpr int kChunkParts = 128 / kBRows;          // converter threads that share a token row
+    static_assert(kSmem <= 232448, "shared memory");
+    static_assert(kTmemA + kOps * (kStageK / 2) <= kTmemCols, "tensor memory");
+    static_assert(kCols % 16 == 0 && kCols <= 128 && kBRows * kChunkParts == 128 && kChunkParts <= 4, "tile");
+    static_assert(kCtas == 2 || kBarOff >= 4 * 128 * kTokens, "split sums use the stages' memory");
+};
+
+struct Tile {
+    int g, n0, row0, hi;  // weight rows from n0 of group g; tokens [row0, hi)
+    int n;                // tokens of an MMA
+};
+
+template <class C>
+__device__ __forceinline__ Tile decode(int64_t t, const int* tab, int groups, int n_tiles) {
+    const GroupTile f = find_group_tile(t, tab, groups, n_tiles, C::kTokens);
+    // (the N of an MMA is a multiple of 16)
+    return {f.g, f.n_tile * 128 * C::kCtas, f.row0, f.hi, C::kHalves == 2 ? C::kN : min(C::kN, (f.hi - f.row0 + 15) & ~15)};
+}
+
+// Whether the sum of a half is taken out after step d of n (a step is two stages). The halves' MMAs alternate as 0 1 | 1 0 | 0 1 | ...,
+// so the half that was first in step 0 has a gap of two steps of the other half's after every even step, the other one after
+// every odd step: the sums are taken out in these gaps. At most four steps, 1024 of K, are added up.
+__device__ __forceinline__ bool taken_out(bool first, int d, int n) {
+    return d == n - 1 || (n > kChunkStages / 2 && (d & 3) == (first ? 0 : 1));
+}
+
+// four codes as f16 numbers: c + 128 is put into the fraction of 1024, from which 1152 is subtracted
+__device__ __forceinline__ void to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = codes ^ 0x80808080u;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+// 16 consecutive 32-bit columns of this thread's lane
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// D += A (128 or 256 rows, tensor memory) x B (shared memory), K = 16
+__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, bool pair) {
+    if (pair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+
+// mbar_wait for a barrier that the other CTA of the pair arrives on, too: what that CTA wrote before is seen
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int32_t* hdr, volatile int* abort_flag) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_cluster(bar, parity)) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+            record_error(hdr, MOE_ERR_TIMEOUT);
+            *abort_flag = 1;
+            return false;
         }
-        const uint4* a = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.a) + m * p.a_stride);
-        const uint4* b = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.b) + (g * p.N + n) * p.b_stride);
-        int c = 0;
-        for (int64_t k = 0; k < p.K / 16; ++k) {
-            const uint4 u = __ldg(a + k), v = __ldg(b + k);
-            c = __dp4a((int)u.x, (int)v.x, c);
-            c = __dp4a((int)u.y, (int)v.y, c);
-            c = __dp4a((int)u.z, (int)v.z, c);
-            c = __dp4a((int)u.w, (int)v.w, c);
-        }
-        const float y = __fmul_rn(__fmul_rn((float)c, __ldg(p.b_scale + (int64_t)g * p.N + n)), __ldg(p.a_scale + m));
-        if constexpr (sizeof(Out) == 2) static_cast<uint16_t*>(p.out)[m * p.out_stride + n] = float_to_bf16_bits(y);
-        else static_cast<float*>(p.out)[m * p.out_stride + n] = y;
     }
+    return true;
+}
+
+// Arrives on a barrier of either CTA of the pair after this warp's reads of tensor memory (ordered by tcgen05.wait::ld) alone.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <typename Out>
+__device__ __forceinline__ void store_if(bool on, Out* p, float v) {
+    if constexpr (sizeof(Out) == 2) st_global_u16_if(on, p, float_to_bf16_bits(v));
+    else asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.f32 [%1], %2;\n\t}" ::"r"((int)on), "l"(p), "f"(v));
+}
+
+__device__ __forceinline__ float scaled(int c, float b_scale, float a_scale) {
+    return __fmul_rn(__fmul_rn((float)c, b_scale), a_scale);
+}
+
+template <class C, typename Out>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_matmul_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Args p) {
+    constexpr bool kPair = C::kCtas == 2;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const uint32_t bars = base + C::kBarOff;
+    auto raw_full = [&](int s) { return bars + 8u * s; };                                 // bytes have landed
+    auto raw_free = [&](int s) { return bars + 8u * (C::kRaw + s); };                     // and have been read
+    auto op_full = [&](int s) { return bars + 8u * (2 * C::kRaw + s); };                  // operands are written
+    auto op_free = [&](int s) { return bars + 8u * (2 * C::kRaw + C::kOps + s); };        // and their MMAs finished
+    auto acc_full = [&](int a) { return bars + 8u * (2 * C::kRaw + 2 * C::kOps + a); };   // a sum is ready
+    auto acc_free = [&](int a) { return bars + 8u * (2 * C::kRaw + 2 * C::kOps + 2 + a); };  // and has been read
+    const uint32_t end_bar = bars + 8u * (C::kNumBars - 1);                                  // every MMA is finished
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    int* tab = reinterpret_cast<int*>(smem + C::kTabOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = kPair ? 1 : p.split;
+    const int share = kPair ? 2 : split;  // CTAs of a cluster
+    const uint32_t rank = share > 1 ? cluster_ctarank() : 0u;
+    const int half_cta = kPair ? (int)rank : 0;
+    const bool even = half_cta == 0;
+    const int64_t first = blockIdx.x / share, step = gridDim.x / share;
+    const int kb0 = kPair ? 0 : (int)((int64_t)p.kb_count * rank / split);
+    const int kb1 = kPair ? p.kb_count : (int)((int64_t)p.kb_count * (rank + 1) / split);
+    const int steps = (kb1 - kb0 + 1) / 2;  // pairs of stages (kHalves 2)
+
+    if (warp == 2) write_group_tiles(p.offsets, p.M, p.groups, C::kTokens, tab, lane);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kRaw; ++s) {
+            mbar_init(raw_full(s), 1);
+            mbar_init(raw_free(s), kConvWarps);
+        }
+        for (int s = 0; s < C::kOps; ++s) {
+            mbar_init(op_full(s), kConvWarps + (kPair && even ? 1 : 0));  // and the odd CTA's warps, as one
+            mbar_init(op_free(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(acc_full(a), 1);
+            mbar_init(acc_free(a), kEpiWarps / C::kHalves * C::kCtas);
+        }
+        mbar_init(end_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+    }
+    if (warp == 1) {
+        if constexpr (kPair) tmem_alloc_pair(smem_u32(tmem_holder), kTmemCols);
+        else tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (kPair) cluster_sync();  // both CTAs' barriers are initialised before either signals the other's
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    const int64_t total = (int64_t)tab[p.groups] * p.n_tiles;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 0 && lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int64_t t = first; t < total && ok; t += step) {
+                const Tile tl = decode<C>(t, tab, p.groups, p.n_tiles);
+                const int wrow = tl.g * p.N + tl.n0 + half_cta * 128;
+                const int trow = tl.row0 + half_cta * (tl.n / C::kCtas);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % C::kRaw;
+                    if (!mbar_wait(raw_free(s), ((uint32_t)(it / C::kRaw) & 1u) ^ 1u, p.hdr, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = base + s * C::kRawBytes;
+                    mbar_arrive_expect_tx(raw_full(s), C::kRawBytes);
+                    tma_load_2d(dst, &tmB, kb * kStageK, wrow, raw_full(s));
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load_2d(dst + C::kRawA + h * C::kHalfRows * kStageK, &tmA, kb * kStageK, trow + h * C::kN, raw_full(s));
+                }
+            }
+            // drain: every copy issued has landed (bounded)
+            for (int j = it - C::kRaw < 0 ? 0 : it - C::kRaw; j < it; ++j)
+                if (!mbar_drain(raw_full(j % C::kRaw), (uint32_t)(j / C::kRaw) & 1u, p.hdr)) break;
+        } else if (warp == 1 && even) {
+            // the whole warp walks the loop and one elected lane issues
+            const uint64_t bd0 = kmajor_desc(base + C::kOpOff, 0);
+            int it = 0, sums[2] = {0, 0};
+            bool ok = true;
+            auto wait_op = [&](int i) {
+                const uint32_t bar = op_full(i % C::kOps), parity = (uint32_t)(i / C::kOps) & 1u;
+                const bool there = kPair ? mbar_wait_cluster(bar, parity, p.hdr, abort_flag) : mbar_wait(bar, parity, p.hdr, abort_flag);
+                ok = __all_sync(0xffffffffu, there);
+                if (ok) tc_fence_after();
+                return ok;
+            };
+            auto wait_acc = [&](int a) {
+                ok = __all_sync(0xffffffffu, mbar_wait(acc_free(a), ((uint32_t)sums[a] & 1u) ^ 1u, p.hdr, abort_flag));
+                if (ok) tc_fence_after();
+                return ok;
+            };
+            // a stage's MMAs of one half into buffer a; then what is finished with them
+            auto issue = [&](int i, int h, int a, uint32_t idesc, bool fresh, bool frees, bool ready) {
+                const int s = i % C::kOps;
+                if (elect_one()) {
+                    const uint32_t d = tmem_base + (uint32_t)(a * C::kN), wa = tmem_base + (uint32_t)(C::kTmemA + s * (kStageK / 2));
+                    const uint64_t bd = bd0 + (uint64_t)((s * C::kOpBytes + h * C::kHalfRows * 128) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kStageK / 16; ++kk)
+                        mma_ta(d, wa + 8 * kk, bd + (uint64_t)((kk / 4 * C::kAtomBytes + kk % 4 * 32) >> 4), idesc, !(fresh && kk == 0), kPair);
+                    if constexpr (kPair) {
+                        if (frees) tc2_commit_mc(op_free(s), 0x3);
+                        if (ready) tc2_commit_mc(acc_full(a), 0x3);
+                    } else {
+                        if (frees) tc_commit(op_free(s));
+                        if (ready) tc_commit(acc_full(a));
+                    }
+                }
+                __syncwarp();
+                if (ready) ++sums[a];
+            };
+            int lead = 0;  // the half whose MMAs come first in the tile
+            for (int64_t t = first; t < total && ok; t += step) {
+                const Tile tl = decode<C>(t, tab, p.groups, p.n_tiles);
+                // kind::f16: fp32 sums (bit 4), f16 x f16, both K-major, N >> 3 (bits 17-22), M >> 4 (24-28)
+                const uint32_t idesc = (1u << 4) | ((uint32_t)(tl.n >> 3) << 17) | ((uint32_t)(8 * C::kCtas) << 24);
+                if constexpr (C::kHalves == 1) {
+                    for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                        const bool fresh = (kb - kb0) % kChunkStages == 0;
+                        const bool ready = (kb - kb0) % kChunkStages == kChunkStages - 1 || kb == kb1 - 1;
+                        const int a = sums[0] & 1;
+                        if (fresh) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(acc_free(a), ((uint32_t)(sums[0] >> 1) & 1u) ^ 1u, p.hdr, abort_flag));
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        if (!wait_op(it)) break;
+                        issue(it, 0, a, idesc, fresh, true, false);
+                        if (ready) {
+                            if (elect_one()) {
+                                if constexpr (kPair) tc2_commit_mc(acc_full(a), 0x3);
+                                else tc_commit(acc_full(a));
+                            }
+                            __syncwarp();
+                            ++sums[0];
+                        }
+                    }
+                } else {
+                    uint32_t fresh = 3;  // bit h: the next MMA of half h begins a sum
+                    for (int d = 0; d < steps && ok; ++d) {
+                        const int n = min(2, kb1 - kb0 - 2 * d);
+                        for (int o = 0; o < 2 && ok; ++o) {
+                            const int h = lead ^ (d & 1) ^ o;
+                            const bool out = taken_out(h == lead, d, steps);
+                            if (fresh >> h & 1)
+                                if (!wait_acc(h)) break;
+                            for (int i = 0; i < n; ++i) {
+                                if (o == 0 && !wait_op(it + i)) break;
+                                issue(it + i, h, h, idesc, fresh >> h & 1, o == 1, out && i == n - 1);
+                                fresh &= ~(1u << h);
+                            }
+                            if (out) fresh |= 1u << h;
+                        }
+                        it += n;
+                    }
+                    lead ^= (steps - 1) & 1;  // the half that was first in the last step has had the longer pause
+                }
+            }
+            // drain: every MMA issued has completed before shared and tensor memory are given up, after a time-out too
+            if (elect_one()) {
+                if constexpr (kPair) tc2_commit_mc(end_bar, 0x1);
+                else tc_commit(end_bar);
+            }
+            __syncwarp();
+            mbar_drain(end_bar, 0, p.hdr);
+        } else if (warp == 1) {
+            // the odd CTA: its converters' arrivals go to the even CTA's barrier as one, with what they wrote
+            int it = 0;
+            bool ok = true;
+            for (int64_t t = first; t < total && ok; t += step)
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % C::kOps;
+                    ok = __all_sync(0xffffffffu, mbar_wait(op_full(s), (uint32_t)(it / C::kOps) & 1u, p.hdr, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(op_full(s), 0));
+                }
+        }
+    } else if (warp >= 4 + kEpiWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+        const bool weights = warp < 4 + kEpiWarps + 4;
+        const int q = warp & 3, row = weights ? q * 32 + lane : (q * 32 + lane) % C::kBRows;
+        const int part = weights ? 0 : (q * 32 + lane) / C::kBRows;
+        const uint32_t tmem_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)C::kTmemA;
+        int it = 0;
+        bool ok = true;
+        for (int64_t t = first; t < total && ok; t += step) {
+            const Tile tl = decode<C>(t, tab, p.groups, p.n_tiles);
+            const bool mine = row < (C::kHalves == 2 ? C::kBRows : tl.n / C::kCtas);  // a token row that an MMA reads
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % C::kRaw, o = it % C::kOps;
+                ok = mbar_wait(raw_full(s), (uint32_t)(it / C::kRaw) & 1u, p.hdr, abort_flag) &&
+                     mbar_wait(op_free(o), ((uint32_t)(it / C::kOps) & 1u) ^ 1u, p.hdr, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sw = (uint32_t)(row & 7);
+                if (weights) {
+                    const uint32_t src = base + s * C::kRawBytes + row * kStageK;
+#pragma unroll
+                    for (int c = 0; c < 8; c += 4) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = ld_shared16(src + (((uint32_t)(c + j) ^ sw) << 4));
+                        if (c == 4) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(raw_free(s));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2) {
+                            uint32_t f[16];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                to_f16(w[j + k].x, f[8 * k + 0], f[8 * k + 1]);
+                                to_f16(w[j + k].y, f[8 * k + 2], f[8 * k + 3]);
+                                to_f16(w[j + k].z, f[8 * k + 4], f[8 * k + 5]);
+                                to_f16(w[j + k].w, f[8 * k + 6], f[8 * k + 7]);
+                            }
+                            tmem_st16(tmem_row + (uint32_t)(o * (kStageK / 2) + 8 * (c + j)), f);
+                        }
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                } else {
+                    constexpr int kChunks = 8 / C::kChunkParts, kBatch = kChunks < 4 ? kChunks : 4;
+                    const uint32_t src = base + s * C::kRawBytes + C::kRawA + row * kStageK;
+                    const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + row * 128;
+#pragma unroll
+                    for (int c = 0; c < kChunks; c += kBatch) {
+                        uint4 w[kBatch];
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j)
+                            if (mine) w[j] = ld_shared16(src + (((uint32_t)(part * kChunks + c + j) ^ sw) << 4));
+                        if (c + kBatch == kChunks) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(raw_free(s));
+                        }
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j) {
+                            uint32_t f[8];
+                            to_f16(w[j].x, f[0], f[1]);
+                            to_f16(w[j].y, f[2], f[3]);
+                            to_f16(w[j].z, f[4], f[5]);
+                            to_f16(w[j].w, f[6], f[7]);
+                            // chunk ch holds 16 of K: the 16-byte slots 2 (ch % 4) and the next of atom ch / 4
+                            const uint32_t ch = (uint32_t)(part * kChunks + c + j), at = dst + (ch >> 2) * C::kAtomBytes;
+                            if (mine) {
+                                st_shared16(at + ((((ch & 3) * 2) ^ sw) << 4), f);
+                                st_shared16(at + ((((ch & 3) * 2 + 1) ^ sw) << 4), f + 4);
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(op_full(o));
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        int sums = 0, lead = 0;
+        bool ok = true;
+        for (int64_t t = first; t < total && ok; t += step) {
+            const Tile tl = decode<C>(t, tab, p.groups, p.n_tiles);
+            const int n = tl.n0 + half_cta * 128 + q * 32 + lane;                            // the lane's weight row
+            const int m0 = tl.row0 + half * C::kCols;                                        // its first token
+            const int cols = C::kHalves == 2 ? C::kCols : min(C::kCols, tl.n - half * C::kCols);  // (multiples of 16; or none)
+            const bool live = n - lane < p.N && m0 < tl.hi && cols > 0;
+            int acc[C::kCols];
+#pragma unroll
+            for (int j = 0; j < C::kCols; ++j) acc[j] = 0;
+            auto take = [&](int a, uint32_t parity) {
+                ok = __all_sync(0xffffffffu, mbar_wait(acc_full(a), parity, p.hdr, abort_flag));
+                if (!ok) return;
+                tc_fence_after();
+                if (live) {
+                    const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * C::kN + (C::kHalves == 2 ? 0 : half * C::kCols));
+#pragma unroll
+                    for (int c = 0; c < C::kCols / 16; ++c) {
+                        if (16 * c >= cols) break;
+                        uint32_t r[16];
+                        tmem_ld16(ta + 16 * c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[16 * c + j] += __float2int_rn(__uint_as_float(r[j]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (kPair) mbar_arrive_relaxed(mapa_shared(acc_free(a), 0));
+                    else mbar_arrive(acc_free(a));
+                }
+            };
+            if constexpr (C::kHalves == 1) {
+                for (int kb = kb0; kb < kb1 && ok; kb += kChunkStages, ++sums) take(sums & 1, (uint32_t)(sums >> 1) & 1u);
+            } else {
+                for (int d = 0; d < steps && ok; ++d)
+                    if (taken_out(half == lead, d, steps)) {
+                        take(half, (uint32_t)sums & 1u);
+                        ++sums;
+                    }
+                lead ^= (steps - 1) & 1;
+            }
+            if (!ok) break;
+            if (split > 1) {
+                // the partial sums go where the stages were (all of them have been read): [token][weight row]
+                if (live) {
+                    int* dst = reinterpret_cast<int*>(smem) + half * C::kCols * 128 + q * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < C::kCols; ++j) dst[j * 128] = acc[j];
+                }
+            } else if (live) {
+                const float bs = n < p.N ? __ldg(p.b_scale + (int64_t)tl.g * p.N + n) : 0.0f;
+                Out* dst = static_cast<Out*>(p.out) + (int64_t)m0 * p.out_stride + n;
+#pragma unroll
+                for (int j = 0; j < C::kCols; ++j) {
+                    const int m = m0 + j;
+                    store_if(n < p.N && m < tl.hi, dst + j * p.out_stride, scaled(acc[j], bs, __ldg(p.a_scale + min(m, tl.hi - 1))));
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (share > 1) cluster_sync();  // pairs: neither leaves while the other uses its memory; splits: the sums are written
+    tc_fence_after();
+    if (!kPair && split > 1) {
+        if (first < total) {
+            // every CTA adds its share of the tile's values
+            const Tile tl = decode<C>(first, tab, p.groups, p.n_tiles);
+            const int rows = min(C::kTokens, tl.hi - tl.row0), n_end = min(128, p.N - tl.n0);
+            for (int i = (int)rank * kThreads + threadIdx.x; i < rows * 128; i += split * kThreads) {
+                const int j = i / 128, w = i % 128;
+                if (w >= n_end) continue;
+                int sum = 0;
+                for (int k = 0; k < split; ++k) {
+                    int v;
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(base + (uint32_t)i * 4u, (uint32_t)k)) : "memory");
+                    sum += v;
+                }
+                const float y = scaled(sum, __ldg(p.b_scale + (int64_t)tl.g * p.N + tl.n0 + w), __ldg(p.a_scale + tl.row0 + j));
+                store_if(true, static_cast<Out*>(p.out) + (int64_t)(tl.row0 + j) * p.out_stride + tl.n0 + w, y);
+            }
+        }
+        __syncthreads();
+        cluster_sync();  // nobody leaves while its sums are read
+    }
+    if (warp == 1) {
+        if constexpr (kPair) tmem_dealloc_pair(tmem_base, kTmemCols);
+        else tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------------------
+
+using Large = Cfg<2, 128, 2, 3, 3>;
+using Pair = Cfg<2, 128, 1, 4, 4>;
+using Mid = Cfg<1, 64, 1, 4, 4>;
+
+template <class C, typename Out>
+cudaError_t prepare_kernel(int* resident) {
+    static int clusters[kMaxDevices];
+    int device = 0;
+    const cudaError_t err = once_per_device(&device, [](int dev) {
+        cudaError_t e = cudaFuncSetAttribute(int8_matmul_kernel<C, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (e == cudaSuccess) e = check_register_split(reinterpret_cast<const void*>(int8_matmul_kernel<C, Out>), kLaunchRegs);
+        if (C::kCtas == 1 || e != cudaSuccess) return e;
+        // pairs that can be resident at once (a pair needs two free SMs of one GPC)
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * std::max(1, tc_num_sms() / 2));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = C::kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&clusters[dev], int8_matmul_kernel<C, Out>, &cfg) != cudaSuccess || clusters[dev] < 1) {
+            (void)cudaGetLastError();
+            clusters[dev] = std::max(1, tc_num_sms() / 2);
+        }
+        return e;
+    });
+    *resident = err == cudaSuccess ? clusters[device] : 0;
+    return err;
+}
+
+template <class C, typename Out>
+cudaError_t launch(const moe_int8_matmul_args& a, Args p, int split, cudaStream_t s) {
+    int resident = 0;
+    const cudaError_t err = prepare_kernel<C, Out>(&resident);
+    if (err != cudaSuccess) return err;
+    CUtensorMap ma, mb;
+    const uint64_t da[2] = {(uint64_t)a.K, (uint64_t)a.M}, db[2] = {(uint64_t)a.K, (uint64_t)a.N * a.groups};
+    const uint64_t sa[1] = {(uint64_t)a.a_stride}, sb[1] = {(uint64_t)a.b_stride};
+    const uint32_t boxa[2] = {kStageK, (uint32_t)(C::kHalves == 2 ? C::kHalfRows : C::kBRows)}, boxb[2] = {kStageK, 128};
+    if (!tc_make_map_nd(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.a, da, sa, boxa, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !tc_make_map_nd(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.b, db, sb, boxb, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    p.n_tiles = (p.N + 128 * C::kCtas - 1) / (128 * C::kCtas);
+    p.split = split;
+    // row tiles: at most one unfilled per group (and none for groups without rows)
+    const int64_t row_tiles = (a.M + C::kTokens - 1) / C::kTokens + std::min<int64_t>(a.groups - 1, a.M);
+    const int64_t tiles = row_tiles * p.n_tiles;
+    const int share = C::kCtas == 2 ? 2 : split;
+    const int64_t clusters = split > 1 ? tiles : std::min<int64_t>(tiles, C::kCtas == 2 ? resident : tc_num_sms());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * share));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)share;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = share > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, int8_matmul_kernel<C, Out>, ma, mb, p);
+}
+
+template <typename Out>
+cudaError_t launch_out(const moe_int8_matmul_args& a, const Args& p, cudaStream_t s) {
+    const int sms = tc_num_sms();
+    const int64_t n_tiles = (a.N + 255) / 256;
+    if (a.M / a.groups >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, 1, s);
+    const int64_t row_tiles = (a.M + 127) / 128 + (a.groups > 1 ? std::min<int64_t>(a.groups, a.M) / 2 : 0);
+    if (row_tiles * n_tiles * 4 >= sms) return launch<Pair, Out>(a, p, 1, s);
+    // few tiles: the stages are shared by a cluster's CTAs as long as all tiles run at once
+    int split = 1;
+    const int64_t tiles = ((a.M + 63) / 64) * ((a.N + 127) / 128);
+    if (a.groups == 1)
+        while (split < 8 && tiles * split * 2 <= sms && p.kb_count >= split * 4) split *= 2;
+    return launch<Mid, Out>(a, p, split, s);
 }
 
 }  // namespace
 
 size_t int8_matmul_workspace(int64_t, int64_t, int64_t, int) { return sizeof(int32_t) * kOpsHeaderInts; }
 
-cudaError_t launch_int8_matmul(const moe_int8_matmul_args& a, void*, cudaStream_t s) {
-    const dim3 grid((unsigned)((a.N + 255) / 256), (unsigned)std::min<int64_t>(a.M, 65535));
-    if (a.out_type == MOE_TYPE_BF16) simple_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-    else simple_kernel<float><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_int8_matmul(const moe_int8_matmul_args& a, void* workspace, cudaStream_t s) {
+    if (a.M == 0) return cudaSuccess;
+    Args p = {};
+    p.a_scale = a.a_scale;
+    p.b_scale = a.b_scale;
+    p.offsets = a.offsets;
+    p.out = a.out;
+    p.hdr = static_cast<int32_t*>(workspace);
+    p.out_stride = a.out_stride;
+    p.M = (int)a.M;
+    p.N = (int)a.N;
+    p.groups = a.groups;
+    p.kb_count = (int)((a.K + kStageK - 1) / kStageK);
+    return a.out_type == MOE_TYPE_BF16 ? launch_out<__nv_bfloat16>(a, p, s) : launch_out<float>(a, p, s);
 }
 
 }  // namespace moe
