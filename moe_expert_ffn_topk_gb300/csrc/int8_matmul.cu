@@ -38,10 +38,10 @@ constexpr int kEpiWarps = 8, kConvWarps = 8;
 // registers of warps 0-3, 4-11 and 12-19: 128 * 32 + 256 * 160 + 256 * 64 = 640 * 96, what the launch holds
 constexpr int kLaunchRegs = 96, kFewRegs = 32, kEpiRegs = 160, kConvRegs = 64;
 static_assert(128 * kFewRegs + 256 * kEpiRegs + 256 * kConvRegs <= kThreads * kLaunchRegs, "register split");
-constexpr int kMaxGroups = 1024;
 constexpr int kTmemCols = 512;
-constexpr int kStageK = 128;                 // codes of K in a stage
-constexpr int kChunkStages = 1024 / kStageK; // stages of an exact fp32 sum
+constexpr int kStageK = 128;                  // codes of K in a stage of bytes
+constexpr int kOpK = 64;                      // and in one of operands, two to a stage of bytes
+constexpr int kChunkStages = 1024 / kStageK;  // stages of bytes of an exact fp32 sum
 
 struct Args {
     const float* a_scale;
@@ -64,18 +64,20 @@ struct Cfg {
     static constexpr int kTokens = kN * kHalves;
     static constexpr int kBRows = kTokens / kCtas, kHalfRows = kN / kCtas;
     static constexpr int kRawA = 128 * kStageK, kRawBytes = kRawA + kBRows * kStageK;
-    static constexpr int kOpBytes = 2 * kBRows * kStageK, kAtomBytes = kOpBytes / 2;  // two swizzled atoms of 64 of K
+    static constexpr int kOpBytes = 2 * kBRows * kOpK;  // tokens in f16, rows of 128 bytes
     static constexpr int kOpOff = kRaw * kRawBytes;
     static constexpr int kBarOff = kOpOff + kOps * kOpBytes;
     static constexpr int kNumBars = 2 * kRaw + 2 * kOps + 5;
     static constexpr int kMiscOff = kBarOff + 8 * ((kNumBars + 1) & ~1);
     static constexpr int kTabOff = kMiscOff + 16;
-    static constexpr size_t kSmem = 1024 + (size_t)kTabOff + 4 * (3 * kMaxGroups + 4);
+    static constexpr int kMaxTab = 232448 - 1024 - kTabOff;
+    static size_t smem(int groups) { return 1024 + (size_t)kTabOff + 4 * (3 * groups + 4); }
     static constexpr int kCols = kHalves == 2 ? kN : kN / 2;  // sums of a lane of the epilogue
-    static constexpr int kTmemA = 2 * kN;                     // first column of the weights' stages, 64 columns each
+    static constexpr int kTmemA = 2 * kN;                     // first column of the weights' stages, kOpK / 2 columns each
+    static constexpr int kMaxGroups = kMaxTab / 12 - 2;       // whose table fits
     static constexpr int kChunkParts = 128 / kBRows;          // converter threads that share a token row
-    static_assert(kSmem <= 232448, "shared memory");
-    static_assert(kTmemA + kOps * (kStageK / 2) <= kTmemCols, "tensor memory");
+    static_assert(kMaxGroups >= 1, "shared memory");
+    static_assert(kTmemA + kOps * (kOpK / 2) <= kTmemCols, "tensor memory");
     static_assert(kCols % 16 == 0 && kCols <= 128 && kBRows * kChunkParts == 128 && kChunkParts <= 4, "tile");
     static_assert(kCtas == 2 || kBarOff >= 4 * 128 * kTokens, "split sums use the stages' memory");
 };
@@ -92,11 +94,11 @@ __device__ __forceinline__ Tile decode(int64_t t, const int* tab, int groups, in
     return {f.g, f.n_tile * 128 * C::kCtas, f.row0, f.hi, C::kHalves == 2 ? C::kN : min(C::kN, (f.hi - f.row0 + 15) & ~15)};
 }
 
-// Whether the sum of a half is taken out after step d of n (a step is two stages). The halves' MMAs alternate as 0 1 | 1 0 | 0 1 | ...,
-// so the half that was first in step 0 has a gap of two steps of the other half's after every even step, the other one after
-// every odd step: the sums are taken out in these gaps. At most four steps, 1024 of K, are added up.
+// Whether the sum of a half is taken out after step d of n (a step is a stage of bytes). The halves' MMAs alternate as
+// 0 1 | 1 0 | 0 1 | ..., so the half that was first in step 0 has a gap of two steps of the other half's after every even step, the
+// other one after every odd step: the sums are taken out in these gaps. At most eight steps, 1024 of K, are added up.
 __device__ __forceinline__ bool taken_out(bool first, int d, int n) {
-    return d == n - 1 || (n > kChunkStages / 2 && (d & 3) == (first ? 0 : 1));
+    return d == n - 1 || (n > kChunkStages && d % kChunkStages == (first ? 0 : 1));
 }
 
 // four codes as f16 numbers: c + 128 is put into the fraction of 1024, from which 1152 is subtracted
@@ -168,6 +170,13 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     return true;
 }
 
+// Arrives on a barrier of either CTA of the pair for operands that this warp has written to its own CTA's shared memory (and made visible to
+// the MMA by fence.proxy.async) or tensor memory (tcgen05.wait::st): the tensor cores of the CTA that holds them read them, so
+// the release of CTA scope suffices. One of cluster scope waits for all of the warp's accesses and took 850 cycles a stage.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Arrives on a barrier of either CTA of the pair after this warp's reads of tensor memory (ordered by tcgen05.wait::ld) alone.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t first = blockIdx.x / share, step = gridDim.x / share;
     const int kb0 = kPair ? 0 : (int)((int64_t)p.kb_count * rank / split);
     const int kb1 = kPair ? p.kb_count : (int)((int64_t)p.kb_count * (rank + 1) / split);
-    const int steps = (kb1 - kb0 + 1) / 2;  // pairs of stages (kHalves 2)
+    const int steps = kb1 - kb0;
 
     if (warp == 2) write_group_tiles(p.offsets, p.M, p.groups, C::kTokens, tab, lane);
     if (threadIdx.x == 0) {
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(raw_free(s), kConvWarps);
         }
         for (int s = 0; s < C::kOps; ++s) {
-            mbar_init(op_full(s), kConvWarps + (kPair && even ? 1 : 0));  // and the odd CTA's warps, as one
+            mbar_init(op_full(s), kConvWarps * C::kCtas);  // (the even CTA's; the odd one's is not used)
             mbar_init(op_free(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -283,20 +292,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok) tc_fence_after();
                 return ok;
             };
-            auto wait_acc = [&](int a) {
-                ok = __all_sync(0xffffffffu, mbar_wait(acc_free(a), ((uint32_t)sums[a] & 1u) ^ 1u, p.hdr, abort_flag));
+            auto wait_acc = [&](int a, int times) {
+                ok = __all_sync(0xffffffffu, mbar_wait(acc_free(a), ((uint32_t)times & 1u) ^ 1u, p.hdr, abort_flag));
                 if (ok) tc_fence_after();
                 return ok;
             };
-            // a stage's MMAs of one half into buffer a; then what is finished with them
+            // the MMAs of operand stage i and half h into buffer a; then what is finished with them
             auto issue = [&](int i, int h, int a, uint32_t idesc, bool fresh, bool frees, bool ready) {
                 const int s = i % C::kOps;
                 if (elect_one()) {
-                    const uint32_t d = tmem_base + (uint32_t)(a * C::kN), wa = tmem_base + (uint32_t)(C::kTmemA + s * (kStageK / 2));
+                    const uint32_t d = tmem_base + (uint32_t)(a * C::kN), wa = tmem_base + (uint32_t)(C::kTmemA + s * (kOpK / 2));
                     const uint64_t bd = bd0 + (uint64_t)((s * C::kOpBytes + h * C::kHalfRows * 128) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kStageK / 16; ++kk)
-                        mma_ta(d, wa + 8 * kk, bd + (uint64_t)((kk / 4 * C::kAtomBytes + kk % 4 * 32) >> 4), idesc, !(fresh && kk == 0), kPair);
+                    for (int kk = 0; kk < kOpK / 16; ++kk) mma_ta(d, wa + 8 * kk, bd + (uint64_t)(kk * 2), idesc, !(fresh && kk == 0), kPair);
                     if constexpr (kPair) {
                         if (frees) tc2_commit_mc(op_free(s), 0x3);
                         if (ready) tc2_commit_mc(acc_full(a), 0x3);
@@ -306,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (ready) ++sums[a];
             };
             int lead = 0;  // the half whose MMAs come first in the tile
             for (int64_t t = first; t < total && ok; t += step) {
@@ -314,43 +321,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // kind::f16: fp32 sums (bit 4), f16 x f16, both K-major, N >> 3 (bits 17-22), M >> 4 (24-28)
                 const uint32_t idesc = (1u << 4) | ((uint32_t)(tl.n >> 3) << 17) | ((uint32_t)(8 * C::kCtas) << 24);
                 if constexpr (C::kHalves == 1) {
-                    for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                        const bool fresh = (kb - kb0) % kChunkStages == 0;
-                        const bool ready = (kb - kb0) % kChunkStages == kChunkStages - 1 || kb == kb1 - 1;
+                    for (int d = 0; d < steps && ok; ++d, it += 2) {
+                        const bool fresh = d % kChunkStages == 0, ready = d % kChunkStages == kChunkStages - 1 || d == steps - 1;
                         const int a = sums[0] & 1;
-                        if (fresh) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(acc_free(a), ((uint32_t)(sums[0] >> 1) & 1u) ^ 1u, p.hdr, abort_flag));
-                            if (!ok) break;
-                            tc_fence_after();
+                        if (fresh && !wait_acc(a, sums[0] >> 1)) break;
+                        for (int i = 0; i < 2; ++i) {
+                            if (!wait_op(it + i)) break;
+                            issue(it + i, 0, a, idesc, fresh && i == 0, true, ready && i == 1);
                         }
-                        if (!wait_op(it)) break;
-                        issue(it, 0, a, idesc, fresh, true, false);
-                        if (ready) {
-                            if (elect_one()) {
-                                if constexpr (kPair) tc2_commit_mc(acc_full(a), 0x3);
-                                else tc_commit(acc_full(a));
-                            }
-                            __syncwarp();
-                            ++sums[0];
-                        }
+                        if (ready) ++sums[0];
                     }
                 } else {
                     uint32_t fresh = 3;  // bit h: the next MMA of half h begins a sum
-                    for (int d = 0; d < steps && ok; ++d) {
-                        const int n = min(2, kb1 - kb0 - 2 * d);
+                    for (int d = 0; d < steps && ok; ++d, it += 2) {
                         for (int o = 0; o < 2 && ok; ++o) {
                             const int h = lead ^ (d & 1) ^ o;
                             const bool out = taken_out(h == lead, d, steps);
-                            if (fresh >> h & 1)
-                                if (!wait_acc(h)) break;
-                            for (int i = 0; i < n; ++i) {
+                            if ((fresh >> h & 1) && !wait_acc(h, sums[h])) break;
+                            for (int i = 0; i < 2; ++i) {
                                 if (o == 0 && !wait_op(it + i)) break;
-                                issue(it + i, h, h, idesc, fresh >> h & 1, o == 1, out && i == n - 1);
-                                fresh &= ~(1u << h);
+                                issue(it + i, h, h, idesc, (fresh >> h & 1) && i == 0, o == 1, out && i == 1);
                             }
-                            if (out) fresh |= 1u << h;
+                            fresh = out ? fresh | 1u << h : fresh & ~(1u << h);
+                            if (out) ++sums[h];
                         }
-                        it += n;
                     }
                     lead ^= (steps - 1) & 1;  // the half that was first in the last step has had the longer pause
                 }
@@ -362,19 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             mbar_drain(end_bar, 0, p.hdr);
-        } else if (warp == 1) {
-            // the odd CTA: its converters' arrivals go to the even CTA's barrier as one, with what they wrote
-            int it = 0;
-            bool ok = true;
-            for (int64_t t = first; t < total && ok; t += step)
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % C::kOps;
-                    ok = __all_sync(0xffffffffu, mbar_wait(op_full(s), (uint32_t)(it / C::kOps) & 1u, p.hdr, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(op_full(s), 0));
-                }
         }
     } else if (warp >= 4 + kEpiWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
@@ -387,25 +368,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t t = first; t < total && ok; t += step) {
             const Tile tl = decode<C>(t, tab, p.groups, p.n_tiles);
             const bool mine = row < (C::kHalves == 2 ? C::kBRows : tl.n / C::kCtas);  // a token row that an MMA reads
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % C::kRaw, o = it % C::kOps;
-                ok = mbar_wait(raw_full(s), (uint32_t)(it / C::kRaw) & 1u, p.hdr, abort_flag) &&
-                     mbar_wait(op_free(o), ((uint32_t)(it / C::kOps) & 1u) ^ 1u, p.hdr, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
+            for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                const int s = it % C::kRaw;
+                ok = __all_sync(0xffffffffu, mbar_wait(raw_full(s), (uint32_t)(it / C::kRaw) & 1u, p.hdr, abort_flag));
                 if (!ok) break;
-                tc_fence_after();
                 const uint32_t sw = (uint32_t)(row & 7);
-                if (weights) {
-                    const uint32_t src = base + s * C::kRawBytes + row * kStageK;
+                const uint32_t src = base + s * C::kRawBytes + (weights ? 0 : C::kRawA) + row * kStageK;
 #pragma unroll
-                    for (int c = 0; c < 8; c += 4) {
-                        uint4 w[4];
+                for (int i = 0; i < 2; ++i) {
+                    const int turn = 2 * it + i, o = turn % C::kOps;
+                    // a thread's 16-byte chunks, 16 of K each: 4 of a row, fewer where threads share a row
+                    constexpr int kMine = 4 / C::kChunkParts;
+                    uint4 w[4];
+                    if (weights) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = ld_shared16(src + (((uint32_t)(c + j) ^ sw) << 4));
-                        if (c == 4) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(raw_free(s));
-                        }
+                        for (int j = 0; j < 4; ++j) w[j] = ld_shared16(src + (((uint32_t)(4 * i + j) ^ sw) << 4));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kMine; ++j)
+                            if (mine) w[j] = ld_shared16(src + (((uint32_t)(4 * i + part * kMine + j) ^ sw) << 4));
+                    }
+                    if (i == 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_free(s));
+                    }
+                    ok = __all_sync(0xffffffffu, mbar_wait(op_free(o), ((uint32_t)(turn / C::kOps) & 1u) ^ 1u, p.hdr, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (weights) {
 #pragma unroll
                         for (int j = 0; j < 4; j += 2) {
                             uint32_t f[16];
@@ -416,44 +406,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 to_f16(w[j + k].z, f[8 * k + 4], f[8 * k + 5]);
                                 to_f16(w[j + k].w, f[8 * k + 6], f[8 * k + 7]);
                             }
-                            tmem_st16(tmem_row + (uint32_t)(o * (kStageK / 2) + 8 * (c + j)), f);
+                            tmem_st16(tmem_row + (uint32_t)(o * (kOpK / 2) + 8 * j), f);
                         }
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                } else {
-                    constexpr int kChunks = 8 / C::kChunkParts, kBatch = kChunks < 4 ? kChunks : 4;
-                    const uint32_t src = base + s * C::kRawBytes + C::kRawA + row * kStageK;
-                    const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + row * 128;
+                        tmem_st_wait();
+                        tc_fence_before();
+                    } else {
+                        const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + row * 128;
 #pragma unroll
-                    for (int c = 0; c < kChunks; c += kBatch) {
-                        uint4 w[kBatch];
-#pragma unroll
-                        for (int j = 0; j < kBatch; ++j)
-                            if (mine) w[j] = ld_shared16(src + (((uint32_t)(part * kChunks + c + j) ^ sw) << 4));
-                        if (c + kBatch == kChunks) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(raw_free(s));
-                        }
-#pragma unroll
-                        for (int j = 0; j < kBatch; ++j) {
+                        for (int j = 0; j < kMine; ++j) {
                             uint32_t f[8];
                             to_f16(w[j].x, f[0], f[1]);
                             to_f16(w[j].y, f[2], f[3]);
                             to_f16(w[j].z, f[4], f[5]);
                             to_f16(w[j].w, f[6], f[7]);
-                            // chunk ch holds 16 of K: the 16-byte slots 2 (ch % 4) and the next of atom ch / 4
-                            const uint32_t ch = (uint32_t)(part * kChunks + c + j), at = dst + (ch >> 2) * C::kAtomBytes;
+                            const uint32_t slot = (uint32_t)(2 * (part * kMine + j));  // 8 of K
                             if (mine) {
-                                st_shared16(at + ((((ch & 3) * 2) ^ sw) << 4), f);
-                                st_shared16(at + ((((ch & 3) * 2 + 1) ^ sw) << 4), f + 4);
+                                st_shared16(dst + ((slot ^ sw) << 4), f);
+                                st_shared16(dst + (((slot + 1) ^ sw) << 4), f + 4);
                             }
                         }
+                        fence_proxy_async_smem();
                     }
-                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kPair) mbar_arrive_remote(mapa_shared(op_full(o), 0));
+                        else mbar_arrive(op_full(o));
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(op_full(o));
             }
         }
     } else {
@@ -558,23 +537,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 // host side
 // ---------------------------------------------------------------------------------------
 
-using Large = Cfg<2, 128, 2, 3, 3>;
-using Pair = Cfg<2, 128, 1, 4, 4>;
-using Mid = Cfg<1, 64, 1, 4, 4>;
+using Large = Cfg<2, 128, 2, 5, 4>;
+using Pair = Cfg<2, 128, 1, 7, 4>;
+using Mid = Cfg<1, 64, 1, 7, 4>;
 
 template <class C, typename Out>
 cudaError_t prepare_kernel(int* resident) {
     static int clusters[kMaxDevices];
     int device = 0;
     const cudaError_t err = once_per_device(&device, [](int dev) {
-        cudaError_t e = cudaFuncSetAttribute(int8_matmul_kernel<C, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        cudaError_t e = cudaFuncSetAttribute(int8_matmul_kernel<C, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
         if (e == cudaSuccess) e = check_register_split(reinterpret_cast<const void*>(int8_matmul_kernel<C, Out>), kLaunchRegs);
         if (C::kCtas == 1 || e != cudaSuccess) return e;
         // pairs that can be resident at once (a pair needs two free SMs of one GPC)
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * std::max(1, tc_num_sms() / 2));
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = C::kSmem;
+        cfg.dynamicSmemBytes = C::smem(1);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -613,7 +592,7 @@ cudaError_t launch(const moe_int8_matmul_args& a, Args p, int split, cudaStream_
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * share));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.dynamicSmemBytes = C::smem(p.groups);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -628,7 +607,7 @@ template <typename Out>
 cudaError_t launch_out(const moe_int8_matmul_args& a, const Args& p, cudaStream_t s) {
     const int sms = tc_num_sms();
     const int64_t n_tiles = (a.N + 255) / 256;
-    if (a.M / a.groups >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, 1, s);
+    if (a.groups <= Large::kMaxGroups && a.M / a.groups >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, 1, s);
     const int64_t row_tiles = (a.M + 127) / 128 + (a.groups > 1 ? std::min<int64_t>(a.groups, a.M) / 2 : 0);
     if (row_tiles * n_tiles * 4 >= sms) return launch<Pair, Out>(a, p, 1, s);
     // few tiles: the stages are shared by a cluster's CTAs as long as all tiles run at once
