@@ -14,7 +14,7 @@
 // MMA), and weights that went back too would add half as much again.
 //
 // Warp roles (640 threads): warp 0 TMA producer, warp 1 tensor-memory allocator and MMA issuer, warp 2 the groups' table, warps
-// 4-11 take sums out and write results, warps 12-15 convert weights (a row a lane), 16-19 tokens.
+// 4-11 take sums out and write results, warps 12-19 convert.
 //
 // Every wait is bounded (2 s); on time-out the CTA records MOE_ERR_TIMEOUT and leaves its loops.
 #include <cuda.h>
@@ -35,8 +35,8 @@ using namespace tc;
 
 constexpr int kThreads = 640;
 constexpr int kEpiWarps = 8, kConvWarps = 8;
-// registers of warps 0-3, 4-11 and 12-19: 128 * 32 + 256 * 160 + 256 * 64 = 640 * 96, what the launch holds
-constexpr int kLaunchRegs = 96, kFewRegs = 32, kEpiRegs = 160, kConvRegs = 64;
+// registers of warps 0-3, 4-11 and 12-19: 128 * 48 + 256 * 160 + 256 * 56 = 640 * 96, what the launch holds
+constexpr int kLaunchRegs = 96, kFewRegs = 48, kEpiRegs = 160, kConvRegs = 56;
 static_assert(128 * kFewRegs + 256 * kEpiRegs + 256 * kConvRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kTmemCols = 512;
 constexpr int kStageK = 128;                  // codes of K in a stage of bytes
@@ -61,6 +61,8 @@ struct Args {
 template <int kCtas_, int kN_, int kHalves_, int kRaw_, int kOps_>
 struct Cfg {
     static constexpr int kCtas = kCtas_, kN = kN_, kHalves = kHalves_, kRaw = kRaw_, kOps = kOps_;
+    static constexpr int kStep = kHalves;                   // stages of bytes of a step
+    static constexpr int kChunkSteps = kChunkStages / kStep;  // steps of an exact fp32 sum
     static constexpr int kTokens = kN * kHalves;
     static constexpr int kBRows = kTokens / kCtas, kHalfRows = kN / kCtas;
     static constexpr int kRawA = 128 * kStageK, kRawBytes = kRawA + kBRows * kStageK;
@@ -75,10 +77,11 @@ struct Cfg {
     static constexpr int kCols = kHalves == 2 ? kN : kN / 2;  // sums of a lane of the epilogue
     static constexpr int kTmemA = 2 * kN;                     // first column of the weights' stages, kOpK / 2 columns each
     static constexpr int kMaxGroups = kMaxTab / 12 - 2;       // whose table fits
-    static constexpr int kChunkParts = 128 / kBRows;          // converter threads that share a token row
+    static constexpr int kMine = kBRows / 64;                 // 16-byte chunks of a token row that a converter thread takes
     static_assert(kMaxGroups >= 1, "shared memory");
     static_assert(kTmemA + kOps * (kOpK / 2) <= kTmemCols, "tensor memory");
-    static_assert(kCols % 16 == 0 && kCols <= 128 && kBRows * kChunkParts == 128 && kChunkParts <= 4, "tile");
+    static_assert(kCols % 16 == 0 && kCols <= 128 && kMine >= 1 && kMine <= 2 && kBRows == 64 * kMine, "tile");
+    static_assert(kOps >= 4 * kStep, "two steps of operands");
     static_assert(kCtas == 2 || kBarOff >= 4 * 128 * kTokens, "split sums use the stages' memory");
 };
 
@@ -94,11 +97,12 @@ __device__ __forceinline__ Tile decode(int64_t t, const int* tab, int groups, in
     return {f.g, f.n_tile * 128 * C::kCtas, f.row0, f.hi, C::kHalves == 2 ? C::kN : min(C::kN, (f.hi - f.row0 + 15) & ~15)};
 }
 
-// Whether the sum of a half is taken out after step d of n (a step is a stage of bytes). The halves' MMAs alternate as
-// 0 1 | 1 0 | 0 1 | ..., so the half that was first in step 0 has a gap of two steps of the other half's after every even step, the
-// other one after every odd step: the sums are taken out in these gaps. At most eight steps, 1024 of K, are added up.
+// Whether the sum of a half is taken out after step d of n. The halves' MMAs alternate as 0 1 | 1 0 | 0 1 | ..., so the half that was first
+// in step 0 has a gap of two steps of the other half's after every even step, the other one after every odd step: the sums are
+// taken out in these gaps. At most C::kChunkSteps steps, 1024 of K, are added up.
+template <class C>
 __device__ __forceinline__ bool taken_out(bool first, int d, int n) {
-    return d == n - 1 || (n > kChunkStages && d % kChunkStages == (first ? 0 : 1));
+    return d == n - 1 || d % C::kChunkSteps == C::kChunkSteps - (first ? 2 : 1);
 }
 
 // four codes as f16 numbers: c + 128 is put into the fraction of 1024, from which 1152 is subtracted
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t first = blockIdx.x / share, step = gridDim.x / share;
     const int kb0 = kPair ? 0 : (int)((int64_t)p.kb_count * rank / split);
     const int kb1 = kPair ? p.kb_count : (int)((int64_t)p.kb_count * (rank + 1) / split);
-    const int steps = kb1 - kb0;
+    const int steps = (kb1 - kb0 + C::kStep - 1) / C::kStep;
 
     if (warp == 2) write_group_tiles(p.offsets, p.M, p.groups, C::kTokens, tab, lane);
     if (threadIdx.x == 0) {
@@ -285,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t bd0 = kmajor_desc(base + C::kOpOff, 0);
             int it = 0, sums[2] = {0, 0};
             bool ok = true;
-            auto wait_op = [&](int i) {
-                const uint32_t bar = op_full(i % C::kOps), parity = (uint32_t)(i / C::kOps) & 1u;
+            // both operand stages from i on: a converter arrives for the first before it does for the second
+            auto wait_ops = [&](int i) {
+                const uint32_t bar = op_full((i + 1) % C::kOps), parity = (uint32_t)((i + 1) / C::kOps) & 1u;
                 const bool there = kPair ? mbar_wait_cluster(bar, parity, p.hdr, abort_flag) : mbar_wait(bar, parity, p.hdr, abort_flag);
                 ok = __all_sync(0xffffffffu, there);
                 if (ok) tc_fence_after();
@@ -297,20 +302,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok) tc_fence_after();
                 return ok;
             };
-            // the MMAs of operand stage i and half h into buffer a; then what is finished with them
+            // the MMAs of operand stages i and i + 1 and half h into buffer a; then what is finished with them
             auto issue = [&](int i, int h, int a, uint32_t idesc, bool fresh, bool frees, bool ready) {
-                const int s = i % C::kOps;
                 if (elect_one()) {
-                    const uint32_t d = tmem_base + (uint32_t)(a * C::kN), wa = tmem_base + (uint32_t)(C::kTmemA + s * (kOpK / 2));
-                    const uint64_t bd = bd0 + (uint64_t)((s * C::kOpBytes + h * C::kHalfRows * 128) >> 4);
+                    const uint32_t d = tmem_base + (uint32_t)(a * C::kN);
 #pragma unroll
-                    for (int kk = 0; kk < kOpK / 16; ++kk) mma_ta(d, wa + 8 * kk, bd + (uint64_t)(kk * 2), idesc, !(fresh && kk == 0), kPair);
-                    if constexpr (kPair) {
-                        if (frees) tc2_commit_mc(op_free(s), 0x3);
-                        if (ready) tc2_commit_mc(acc_full(a), 0x3);
-                    } else {
-                        if (frees) tc_commit(op_free(s));
-                        if (ready) tc_commit(acc_full(a));
+                    for (int j = 0; j < 2; ++j) {
+                        const int s = (i + j) % C::kOps;
+                        const uint32_t wa = tmem_base + (uint32_t)(C::kTmemA + s * (kOpK / 2));
+                        const uint64_t bd = bd0 + (uint64_t)((s * C::kOpBytes + h * C::kHalfRows * 128) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kOpK / 16; ++kk)
+                            mma_ta(d, wa + 8 * kk, bd + (uint64_t)(kk * 2), idesc, !(fresh && j == 0 && kk == 0), kPair);
+                        if (frees) {
+                            if constexpr (kPair) tc2_commit_mc(op_free(s), 0x3);
+                            else tc_commit(op_free(s));
+                        }
+                    }
+                    if (ready) {
+                        if constexpr (kPair) tc2_commit_mc(acc_full(a), 0x3);
+                        else tc_commit(acc_full(a));
                     }
                 }
                 __syncwarp();
@@ -325,26 +336,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool fresh = d % kChunkStages == 0, ready = d % kChunkStages == kChunkStages - 1 || d == steps - 1;
                         const int a = sums[0] & 1;
                         if (fresh && !wait_acc(a, sums[0] >> 1)) break;
-                        for (int i = 0; i < 2; ++i) {
-                            if (!wait_op(it + i)) break;
-                            issue(it + i, 0, a, idesc, fresh && i == 0, true, ready && i == 1);
-                        }
+                        if (!wait_ops(it)) break;
+                        issue(it, 0, a, idesc, fresh, true, ready);
                         if (ready) ++sums[0];
                     }
                 } else {
                     uint32_t fresh = 3;  // bit h: the next MMA of half h begins a sum
-                    for (int d = 0; d < steps && ok; ++d, it += 2) {
+                    for (int d = 0; d < steps && ok; ++d) {
+                        const int n = min(C::kStep, kb1 - kb0 - d * C::kStep);
                         for (int o = 0; o < 2 && ok; ++o) {
                             const int h = lead ^ (d & 1) ^ o;
-                            const bool out = taken_out(h == lead, d, steps);
+                            const bool out = taken_out<C>(h == lead, d, steps);
                             if ((fresh >> h & 1) && !wait_acc(h, sums[h])) break;
-                            for (int i = 0; i < 2; ++i) {
-                                if (o == 0 && !wait_op(it + i)) break;
-                                issue(it + i, h, h, idesc, (fresh >> h & 1) && i == 0, o == 1, out && i == 1);
+                            for (int i = 0; i < n; ++i) {
+                                if (o == 0 && !wait_ops(it + 2 * i)) break;
+                                issue(it + 2 * i, h, h, idesc, (fresh >> h & 1) && i == 0, o == 1, out && i == n - 1);
                             }
                             fresh = out ? fresh | 1u << h : fresh & ~(1u << h);
                             if (out) ++sums[h];
                         }
+                        it += 2 * n;
                     }
                     lead ^= (steps - 1) & 1;  // the half that was first in the last step has had the longer pause
                 }
@@ -359,9 +370,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 4 + kEpiWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-        const bool weights = warp < 4 + kEpiWarps + 4;
-        const int q = warp & 3, row = weights ? q * 32 + lane : (q * 32 + lane) % C::kBRows;
-        const int part = weights ? 0 : (q * 32 + lane) / C::kBRows;
+        // every warp converts half of the 64 codes of 32 weight rows (a row a lane: tensor memory gives a warp the 32 lanes of its place in
+        // four) and a 32nd of the tokens' chunks
+        const int q = warp & 3, part = (warp - 4 - kEpiWarps) >> 2, id = threadIdx.x - 32 * (4 + kEpiWarps);
+        const int wrow = q * 32 + lane, row = id % C::kBRows, chunk = id / C::kBRows * C::kMine;
+        const uint32_t wsw = (uint32_t)(wrow & 7), sw = (uint32_t)(row & 7);
         const uint32_t tmem_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)C::kTmemA;
         int it = 0;
         bool ok = true;
@@ -372,22 +385,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = it % C::kRaw;
                 ok = __all_sync(0xffffffffu, mbar_wait(raw_full(s), (uint32_t)(it / C::kRaw) & 1u, p.hdr, abort_flag));
                 if (!ok) break;
-                const uint32_t sw = (uint32_t)(row & 7);
-                const uint32_t src = base + s * C::kRawBytes + (weights ? 0 : C::kRawA) + row * kStageK;
+                const uint32_t wsrc = base + s * C::kRawBytes + wrow * kStageK, src = base + s * C::kRawBytes + C::kRawA + row * kStageK;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int turn = 2 * it + i, o = turn % C::kOps;
-                    // a thread's 16-byte chunks, 16 of K each: 4 of a row, fewer where threads share a row
-                    constexpr int kMine = 4 / C::kChunkParts;
-                    uint4 w[4];
-                    if (weights) {
+                    // chunks of 16 bytes: 16 of K each
+                    uint4 w[2], v[C::kMine];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = ld_shared16(src + (((uint32_t)(4 * i + j) ^ sw) << 4));
-                    } else {
+                    for (int j = 0; j < 2; ++j) w[j] = ld_shared16(wsrc + (((uint32_t)(4 * i + 2 * part + j) ^ wsw) << 4));
 #pragma unroll
-                        for (int j = 0; j < kMine; ++j)
-                            if (mine) w[j] = ld_shared16(src + (((uint32_t)(4 * i + part * kMine + j) ^ sw) << 4));
-                    }
+                    for (int j = 0; j < C::kMine; ++j)
+                        if (mine) v[j] = ld_shared16(src + (((uint32_t)(4 * i + chunk + j) ^ sw) << 4));
                     if (i == 1) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(raw_free(s));
@@ -395,38 +403,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xffffffffu, mbar_wait(op_free(o), ((uint32_t)(turn / C::kOps) & 1u) ^ 1u, p.hdr, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    if (weights) {
+                    uint32_t f[16];
 #pragma unroll
-                        for (int j = 0; j < 4; j += 2) {
-                            uint32_t f[16];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                to_f16(w[j + k].x, f[8 * k + 0], f[8 * k + 1]);
-                                to_f16(w[j + k].y, f[8 * k + 2], f[8 * k + 3]);
-                                to_f16(w[j + k].z, f[8 * k + 4], f[8 * k + 5]);
-                                to_f16(w[j + k].w, f[8 * k + 6], f[8 * k + 7]);
-                            }
-                            tmem_st16(tmem_row + (uint32_t)(o * (kOpK / 2) + 8 * j), f);
-                        }
-                        tmem_st_wait();
-                        tc_fence_before();
-                    } else {
-                        const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + row * 128;
-#pragma unroll
-                        for (int j = 0; j < kMine; ++j) {
-                            uint32_t f[8];
-                            to_f16(w[j].x, f[0], f[1]);
-                            to_f16(w[j].y, f[2], f[3]);
-                            to_f16(w[j].z, f[4], f[5]);
-                            to_f16(w[j].w, f[6], f[7]);
-                            const uint32_t slot = (uint32_t)(2 * (part * kMine + j));  // 8 of K
-                            if (mine) {
-                                st_shared16(dst + ((slot ^ sw) << 4), f);
-                                st_shared16(dst + (((slot + 1) ^ sw) << 4), f + 4);
-                            }
-                        }
-                        fence_proxy_async_smem();
+                    for (int j = 0; j < 2; ++j) {
+                        to_f16(w[j].x, f[8 * j + 0], f[8 * j + 1]);
+                        to_f16(w[j].y, f[8 * j + 2], f[8 * j + 3]);
+                        to_f16(w[j].z, f[8 * j + 4], f[8 * j + 5]);
+                        to_f16(w[j].w, f[8 * j + 6], f[8 * j + 7]);
                     }
+                    tmem_st16(tmem_row + (uint32_t)(o * (kOpK / 2) + 16 * part), f);
+                    const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + row * 128;
+#pragma unroll
+                    for (int j = 0; j < C::kMine; ++j) {
+                        uint32_t u[8];
+                        to_f16(v[j].x, u[0], u[1]);
+                        to_f16(v[j].y, u[2], u[3]);
+                        to_f16(v[j].z, u[4], u[5]);
+                        to_f16(v[j].w, u[6], u[7]);
+                        const uint32_t slot = (uint32_t)(2 * (chunk + j));  // 8 of K
+                        if (mine) {
+                            st_shared16(dst + ((slot ^ sw) << 4), u);
+                            st_shared16(dst + (((slot + 1) ^ sw) << 4), u + 4);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    tmem_st_wait();
+                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
                         if constexpr (kPair) mbar_arrive_remote(mapa_shared(op_full(o), 0));
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kb = kb0; kb < kb1 && ok; kb += kChunkStages, ++sums) take(sums & 1, (uint32_t)(sums >> 1) & 1u);
             } else {
                 for (int d = 0; d < steps && ok; ++d)
-                    if (taken_out(half == lead, d, steps)) {
+                    if (taken_out<C>(half == lead, d, steps)) {
                         take(half, (uint32_t)sums & 1u);
                         ++sums;
                     }
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // host side
 // ---------------------------------------------------------------------------------------
 
-using Large = Cfg<2, 128, 2, 5, 4>;
+using Large = Cfg<2, 128, 2, 3, 8>;
 using Pair = Cfg<2, 128, 1, 7, 4>;
 using Mid = Cfg<1, 64, 1, 7, 4>;
 
