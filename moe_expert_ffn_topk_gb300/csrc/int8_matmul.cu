@@ -13,8 +13,8 @@
 // bounds such a kernel is shared memory's 128 bytes a cycle (bytes in by TMA, out to the converters, f16 tokens in, and out to the
 // MMA), and weights that went back too would add half as much again.
 //
-// Warp roles (640 threads): warp 0 TMA producer, warp 1 tensor-memory allocator and MMA issuer, warp 2 the groups' table, warps
-// 4-11 take sums out and write results, warps 12-19 convert.
+// Warp roles: warp 0 TMA producer, warp 1 tensor-memory allocator and MMA issuer, warp 2 the groups' table, warps 4-11 take sums out and
+// write results, the others (8 or 16) convert.
 //
 // Every wait is bounded (2 s); on time-out the CTA records MOE_ERR_TIMEOUT and leaves its loops.
 #include <cuda.h>
@@ -33,11 +33,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 640;
-constexpr int kEpiWarps = 8, kConvWarps = 8;
-// registers of warps 0-3, 4-11 and 12-19: 128 * 48 + 256 * 160 + 256 * 56 = 640 * 96, what the launch holds
-constexpr int kLaunchRegs = 96, kFewRegs = 48, kEpiRegs = 160, kConvRegs = 56;
-static_assert(128 * kFewRegs + 256 * kEpiRegs + 256 * kConvRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kEpiWarps = 8;
+constexpr int kFewRegs = 48, kConvRegs = 56;  // registers of warps 0-3 and of the converters
 constexpr int kTmemCols = 512;
 constexpr int kStageK = 128;                  // codes of K in a stage of bytes
 constexpr int kOpK = 64;                      // and in one of operands, two to a stage of bytes
@@ -57,9 +54,15 @@ struct Args {
 
 // A tile is 128 * kCtas weight rows by kHalves * kN tokens. kCtas 2: a pair of CTAs (cta_group::2), each holding 128 of the weight rows
 // and half of the tokens of every MMA. kHalves 2: two MMAs of kN tokens a step, each with a sum of its own; 1: one, whose
-// sum changes between two buffers from chunk to chunk. kRaw, kOps: stages of bytes, and of f16 operands.
-template <int kCtas_, int kN_, int kHalves_, int kRaw_, int kOps_>
+// sum changes between two buffers from chunk to chunk. kRaw, kOps: stages of bytes, and of f16 operands. kConvWarps: converters; kEpiRegs,
+// kLaunchRegs: registers of a thread of the warps that hold the sums, and of every thread at launch.
+template <int kCtas_, int kN_, int kHalves_, int kRaw_, int kOps_, int kConvWarps_, int kEpiRegs_, int kLaunchRegs_>
 struct Cfg {
+    static constexpr int kConvWarps = kConvWarps_, kEpiRegs = kEpiRegs_, kLaunchRegs = kLaunchRegs_;
+    static constexpr int kThreads = 32 * (4 + kEpiWarps + kConvWarps);
+    static constexpr int kGroups = kConvWarps / 4;  // of converters, an operand stage each in turn
+    static_assert(128 * kFewRegs + 32 * kEpiWarps * kEpiRegs + 32 * kConvWarps * kConvRegs <= kThreads * kLaunchRegs, "register split");
+    static_assert(kThreads * kLaunchRegs <= 65536 && (kGroups == 2 || kGroups == 4), "warps");
     static constexpr int kCtas = kCtas_, kN = kN_, kHalves = kHalves_, kRaw = kRaw_, kOps = kOps_;
     static constexpr int kStep = kHalves;                   // stages of bytes of a step
     static constexpr int kChunkSteps = kChunkStages / kStep;  // steps of an exact fp32 sum
@@ -77,10 +80,10 @@ struct Cfg {
     static constexpr int kCols = kHalves == 2 ? kN : kN / 2;  // sums of a lane of the epilogue
     static constexpr int kTmemA = 2 * kN;                     // first column of the weights' stages, kOpK / 2 columns each
     static constexpr int kMaxGroups = kMaxTab / 12 - 2;       // whose table fits
-    static constexpr int kMine = kBRows / 64;                 // 16-byte chunks of a token row that a converter thread takes
+    static constexpr int kMine = kBRows / 32;                 // 16-byte chunks of a token row that a converter thread takes
     static_assert(kMaxGroups >= 1, "shared memory");
     static_assert(kTmemA + kOps * (kOpK / 2) <= kTmemCols, "tensor memory");
-    static_assert(kCols % 16 == 0 && kCols <= 128 && kMine >= 1 && kMine <= 2 && kBRows == 64 * kMine, "tile");
+    static_assert(kCols % 16 == 0 && kCols <= 128 && kMine >= 1 && kMine <= 4 && kBRows == 32 * kMine, "tile");
     static_assert(kOps >= 4 * kStep, "two steps of operands");
     static_assert(kCtas == 2 || kBarOff >= 4 * 128 * kTokens, "split sums use the stages' memory");
 };
@@ -150,28 +153,24 @@ __device__ __forceinline__ bool elect_one() {
     return on != 0;
 }
 
-// mbar_wait for a barrier that the other CTA of the pair arrives on, too: what that CTA wrote before is seen
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+// A test and a bounded wait that begins with it: a try_wait costs 170-280 cycles when the phase has long completed, a test a fraction.
+// kCluster: for a barrier that the other CTA of the pair arrives on, too (what that CTA wrote is seen).
+template <bool kCluster = false>
+__device__ __forceinline__ bool completed(uint32_t bar, uint32_t parity) {
+    if constexpr (!kCluster) return mbar_test(bar, parity);
     uint32_t done;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
         : "r"(bar), "r"(parity)
         : "memory");
     return done != 0;
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int32_t* hdr, volatile int* abort_flag) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait_cluster(bar, parity)) {
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
-            record_error(hdr, MOE_ERR_TIMEOUT);
-            *abort_flag = 1;
-            return false;
-        }
-    }
-    return true;
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int32_t* hdr, volatile int* abort_flag) {
+    if (completed<kCluster>(bar, parity)) return true;
+    if (!mbar_wait(bar, parity, hdr, abort_flag)) return false;
+    return !kCluster || completed<kCluster>(bar, parity);
 }
 
 // Arrives on a barrier of either CTA of the pair for operands that this warp has written to its own CTA's shared memory (and made visible to
@@ -197,7 +196,7 @@ __device__ __forceinline__ float scaled(int c, float b_scale, float a_scale) {
 }
 
 template <class C, typename Out>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(C::kThreads, 1)
     int8_matmul_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Args p) {
     constexpr bool kPair = C::kCtas == 2;
     extern __shared__ uint8_t smem_raw[];
@@ -231,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kRaw; ++s) {
             mbar_init(raw_full(s), 1);
-            mbar_init(raw_free(s), kConvWarps);
+            mbar_init(raw_free(s), 8);  // (two groups of converters)
         }
         for (int s = 0; s < C::kOps; ++s) {
-            mbar_init(op_full(s), kConvWarps * C::kCtas);  // (the even CTA's; the odd one's is not used)
+            mbar_init(op_full(s), 4 * C::kCtas);  // (the even CTA's; the odd one's is not used)
             mbar_init(op_free(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -261,15 +260,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (warp == 0 && lane == 0) {
-            int it = 0;
+            int it = 0, s = 0;
+            uint32_t parity = 1;
             bool ok = true;
             for (int64_t t = first; t < total && ok; t += step) {
                 const Tile tl = decode<C>(t, tab, p.groups, p.n_tiles);
                 const int wrow = tl.g * p.N + tl.n0 + half_cta * 128;
                 const int trow = tl.row0 + half_cta * (tl.n / C::kCtas);
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % C::kRaw;
-                    if (!mbar_wait(raw_free(s), ((uint32_t)(it / C::kRaw) & 1u) ^ 1u, p.hdr, abort_flag)) {
+                    if (!wait_for(raw_free(s), parity, p.hdr, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -279,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h)
                         tma_load_2d(dst + C::kRawA + h * C::kHalfRows * kStageK, &tmA, kb * kStageK, trow + h * C::kN, raw_full(s));
+                    if (++s == C::kRaw) s = 0, parity ^= 1u;
                 }
             }
             // drain: every copy issued has landed (bounded)
@@ -289,16 +289,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t bd0 = kmajor_desc(base + C::kOpOff, 0);
             int it = 0, sums[2] = {0, 0};
             bool ok = true;
-            // both operand stages from i on: a converter arrives for the first before it does for the second
-            auto wait_ops = [&](int i) {
-                const uint32_t bar = op_full((i + 1) % C::kOps), parity = (uint32_t)((i + 1) / C::kOps) & 1u;
-                const bool there = kPair ? mbar_wait_cluster(bar, parity, p.hdr, abort_flag) : mbar_wait(bar, parity, p.hdr, abort_flag);
-                ok = __all_sync(0xffffffffu, there);
-                if (ok) tc_fence_after();
+            auto wait_ops = [&](int i) {  // operand stages i and i + 1
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t bar = op_full((i + j) % C::kOps), parity = (uint32_t)((i + j) / C::kOps) & 1u;
+                    const bool there = wait_for<kPair>(bar, parity, p.hdr, abort_flag);
+                    ok = __all_sync(0xffffffffu, there);
+                    if (!ok) return ok;
+                }
+                tc_fence_after();
                 return ok;
             };
             auto wait_acc = [&](int a, int times) {
-                ok = __all_sync(0xffffffffu, mbar_wait(acc_free(a), ((uint32_t)times & 1u) ^ 1u, p.hdr, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_for(acc_free(a), ((uint32_t)times & 1u) ^ 1u, p.hdr, abort_flag));
                 if (ok) tc_fence_after();
                 return ok;
             };
@@ -368,77 +371,90 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             mbar_drain(end_bar, 0, p.hdr);
         }
-    } else if (warp >= 4 + kEpiWarps) {
+    } else if (warp >= 4 + kEpiWarps) {  // (the last warps)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-        // every warp converts half of the 64 codes of 32 weight rows (a row a lane: tensor memory gives a warp the 32 lanes of its place in
-        // four) and a 32nd of the tokens' chunks
-        const int q = warp & 3, part = (warp - 4 - kEpiWarps) >> 2, id = threadIdx.x - 32 * (4 + kEpiWarps);
-        const int wrow = q * 32 + lane, row = id % C::kBRows, chunk = id / C::kBRows * C::kMine;
-        const uint32_t wsw = (uint32_t)(wrow & 7), sw = (uint32_t)(row & 7);
+        // groups of four warps convert an operand stage each, in turn: a stage's chain of waits, loads, stores and fences is longer than its MMAs.
+        // A warp has 32 weight rows (a row a lane: tensor memory gives a warp the 32 lanes of its place in four) and a fourth of
+        // the tokens' chunks.
+        const int q = warp & 3, group = (warp - 4 - kEpiWarps) >> 2, i = group & 1, id = q * 32 + lane;
+        const int row = id % C::kBRows, chunk = id / C::kBRows * C::kMine;
+        const uint32_t wsw = (uint32_t)(id & 7), sw = (uint32_t)(row & 7);
         const uint32_t tmem_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)C::kTmemA;
-        int it = 0;
-        bool ok = true;
+        int s = group >> 1;                  // stage of bytes, and its round
+        uint32_t parity = 0;
+        uint32_t turn = (uint32_t)group;     // of the operand stages
+        int others = s;                      // stages of bytes until this group's next
+        bool ok = true, landed = false, freed = true;  // tests made a turn ahead
         for (int64_t t = first; t < total && ok; t += step) {
             const Tile tl = decode<C>(t, tab, p.groups, p.n_tiles);
             const bool mine = row < (C::kHalves == 2 ? C::kBRows : tl.n / C::kCtas);  // a token row that an MMA reads
-            for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                const int s = it % C::kRaw;
-                ok = __all_sync(0xffffffffu, mbar_wait(raw_full(s), (uint32_t)(it / C::kRaw) & 1u, p.hdr, abort_flag));
-                if (!ok) break;
-                const uint32_t wsrc = base + s * C::kRawBytes + wrow * kStageK, src = base + s * C::kRawBytes + C::kRawA + row * kStageK;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int turn = 2 * it + i, o = turn % C::kOps;
-                    // chunks of 16 bytes: 16 of K each
-                    uint4 w[2], v[C::kMine];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) w[j] = ld_shared16(wsrc + (((uint32_t)(4 * i + 2 * part + j) ^ wsw) << 4));
-#pragma unroll
-                    for (int j = 0; j < C::kMine; ++j)
-                        if (mine) v[j] = ld_shared16(src + (((uint32_t)(4 * i + chunk + j) ^ sw) << 4));
-                    if (i == 1) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(raw_free(s));
-                    }
-                    ok = __all_sync(0xffffffffu, mbar_wait(op_free(o), ((uint32_t)(turn / C::kOps) & 1u) ^ 1u, p.hdr, abort_flag));
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (others > 0) {
+                    --others;
+                    continue;
+                }
+                others = C::kGroups / 2 - 1;
+                const uint32_t o = turn % C::kOps;
+                if (!__all_sync(0xffffffffu, landed && freed)) {
+                    ok = wait_for(raw_full(s), parity, p.hdr, abort_flag) &&
+                         wait_for(op_free(o), (turn / C::kOps & 1u) ^ 1u, p.hdr, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    tc_fence_after();
+                }
+                tc_fence_after();
+                const uint32_t wsrc = base + s * C::kRawBytes + id * kStageK, src = base + s * C::kRawBytes + C::kRawA + row * kStageK;
+                // chunks of 16 bytes: 16 of K each
+                uint4 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = ld_shared16(wsrc + (((uint32_t)(4 * i + j) ^ wsw) << 4));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     uint32_t f[16];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        to_f16(w[j].x, f[8 * j + 0], f[8 * j + 1]);
-                        to_f16(w[j].y, f[8 * j + 2], f[8 * j + 3]);
-                        to_f16(w[j].z, f[8 * j + 4], f[8 * j + 5]);
-                        to_f16(w[j].w, f[8 * j + 6], f[8 * j + 7]);
+                        to_f16(w[2 * h + j].x, f[8 * j + 0], f[8 * j + 1]);
+                        to_f16(w[2 * h + j].y, f[8 * j + 2], f[8 * j + 3]);
+                        to_f16(w[2 * h + j].z, f[8 * j + 4], f[8 * j + 5]);
+                        to_f16(w[2 * h + j].w, f[8 * j + 6], f[8 * j + 7]);
                     }
-                    tmem_st16(tmem_row + (uint32_t)(o * (kOpK / 2) + 16 * part), f);
-                    const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + row * 128;
+                    tmem_st16(tmem_row + (uint32_t)(o * (kOpK / 2) + 16 * h), f);
+                }
 #pragma unroll
-                    for (int j = 0; j < C::kMine; ++j) {
-                        uint32_t u[8];
-                        to_f16(v[j].x, u[0], u[1]);
-                        to_f16(v[j].y, u[2], u[3]);
-                        to_f16(v[j].z, u[4], u[5]);
-                        to_f16(v[j].w, u[6], u[7]);
-                        const uint32_t slot = (uint32_t)(2 * (chunk + j));  // 8 of K
-                        if (mine) {
-                            st_shared16(dst + ((slot ^ sw) << 4), u);
-                            st_shared16(dst + (((slot + 1) ^ sw) << 4), u + 4);
-                        }
+                for (int j = 0; j < C::kMine; ++j)
+                    if (mine) w[j] = ld_shared16(src + (((uint32_t)(4 * i + chunk + j) ^ sw) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(raw_free(s));
+                s += C::kGroups / 2;
+                if (s >= C::kRaw) s -= C::kRaw, parity ^= 1u;
+                turn += C::kGroups;
+                landed = completed(raw_full(s), parity);
+                freed = completed(op_free(turn % C::kOps), (turn / C::kOps & 1u) ^ 1u);
+                const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + row * 128;
+#pragma unroll
+                for (int j = 0; j < C::kMine; ++j) {
+                    uint32_t u[8];
+                    to_f16(w[j].x, u[0], u[1]);
+                    to_f16(w[j].y, u[2], u[3]);
+                    to_f16(w[j].z, u[4], u[5]);
+                    to_f16(w[j].w, u[6], u[7]);
+                    const uint32_t slot = (uint32_t)(2 * (chunk + j));  // 8 of K
+                    if (mine) {
+                        st_shared16(dst + ((slot ^ sw) << 4), u);
+                        st_shared16(dst + (((slot + 1) ^ sw) << 4), u + 4);
                     }
-                    fence_proxy_async_smem();
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (kPair) mbar_arrive_remote(mapa_shared(op_full(o), 0));
-                        else mbar_arrive(op_full(o));
-                    }
+                }
+                fence_proxy_async_smem();
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (kPair) mbar_arrive_remote(mapa_shared(op_full(o), 0));
+                    else mbar_arrive(op_full(o));
                 }
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
         const int q = warp & 3, half = (warp - 4) >> 2;
         int sums = 0, lead = 0;
         bool ok = true;
@@ -452,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < C::kCols; ++j) acc[j] = 0;
             auto take = [&](int a, uint32_t parity) {
-                ok = __all_sync(0xffffffffu, mbar_wait(acc_full(a), parity, p.hdr, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_for(acc_full(a), parity, p.hdr, abort_flag));
                 if (!ok) return;
                 tc_fence_after();
                 if (live) {
@@ -513,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every CTA adds its share of the tile's values
             const Tile tl = decode<C>(first, tab, p.groups, p.n_tiles);
             const int rows = min(C::kTokens, tl.hi - tl.row0), n_end = min(128, p.N - tl.n0);
-            for (int i = (int)rank * kThreads + threadIdx.x; i < rows * 128; i += split * kThreads) {
+            for (int i = (int)rank * C::kThreads + threadIdx.x; i < rows * 128; i += split * C::kThreads) {
                 const int j = i / 128, w = i % 128;
                 if (w >= n_end) continue;
                 int sum = 0;
@@ -539,9 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // host side
 // ---------------------------------------------------------------------------------------
 
-using Large = Cfg<2, 128, 2, 3, 8>;
-using Pair = Cfg<2, 128, 1, 7, 4>;
-using Mid = Cfg<1, 64, 1, 7, 4>;
+using Large = Cfg<2, 128, 2, 3, 8, 8, 160, 96>;
+using Pair = Cfg<2, 128, 1, 7, 4, 16, 104, 72>;
+using Mid = Cfg<1, 64, 1, 7, 4, 16, 104, 72>;
 
 template <class C, typename Out>
 cudaError_t prepare_kernel(int* resident) {
@@ -549,12 +565,12 @@ cudaError_t prepare_kernel(int* resident) {
     int device = 0;
     const cudaError_t err = once_per_device(&device, [](int dev) {
         cudaError_t e = cudaFuncSetAttribute(int8_matmul_kernel<C, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-        if (e == cudaSuccess) e = check_register_split(reinterpret_cast<const void*>(int8_matmul_kernel<C, Out>), kLaunchRegs);
+        if (e == cudaSuccess) e = check_register_split(reinterpret_cast<const void*>(int8_matmul_kernel<C, Out>), C::kLaunchRegs);
         if (C::kCtas == 1 || e != cudaSuccess) return e;
         // pairs that can be resident at once (a pair needs two free SMs of one GPC)
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * std::max(1, tc_num_sms() / 2));
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(C::kThreads);
         cfg.dynamicSmemBytes = C::smem(1);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -593,7 +609,7 @@ cudaError_t launch(const moe_int8_matmul_args& a, Args p, int split, cudaStream_
     const int64_t clusters = split > 1 ? tiles : std::min<int64_t>(tiles, C::kCtas == 2 ? resident : tc_num_sms());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * share));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::smem(p.groups);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
