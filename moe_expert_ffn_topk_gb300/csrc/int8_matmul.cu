@@ -36,9 +36,8 @@ using namespace tc;
 constexpr int kEpiWarps = 8;
 constexpr int kFewRegs = 48, kConvRegs = 56;  // registers of warps 0-3 and of the converters
 constexpr int kTmemCols = 512;
-constexpr int kStageK = 128;                  // codes of K in a stage of bytes
-constexpr int kOpK = 64;                      // and in one of operands, two to a stage of bytes
-constexpr int kChunkStages = 1024 / kStageK;  // stages of bytes of an exact fp32 sum
+constexpr int kStageK = 128;                  // codes of K in a stage
+constexpr int kChunkStages = 1024 / kStageK;  // stages of an exact fp32 sum
 
 struct Args {
     const float* a_scale;
@@ -54,22 +53,22 @@ struct Args {
 
 // A tile is 128 * kCtas weight rows by kHalves * kN tokens. kCtas 2: a pair of CTAs (cta_group::2), each holding 128 of the weight rows
 // and half of the tokens of every MMA. kHalves 2: two MMAs of kN tokens a step, each with a sum of its own; 1: one, whose
-// sum changes between two buffers from chunk to chunk. kRaw, kOps: stages of bytes, and of f16 operands. kConvWarps: converters; kEpiRegs,
+// sum changes between two buffers from chunk to chunk. kRaw, kOps: stages of bytes, and of operands. kConvWarps: converters; kEpiRegs,
 // kLaunchRegs: registers of a thread of the warps that hold the sums, and of every thread at launch.
 template <int kCtas_, int kN_, int kHalves_, int kRaw_, int kOps_, int kConvWarps_, int kEpiRegs_, int kLaunchRegs_>
 struct Cfg {
     static constexpr int kConvWarps = kConvWarps_, kEpiRegs = kEpiRegs_, kLaunchRegs = kLaunchRegs_;
     static constexpr int kThreads = 32 * (4 + kEpiWarps + kConvWarps);
-    static constexpr int kGroups = kConvWarps / 4;  // of converters, an operand stage each in turn
+    static constexpr int kGroups = kConvWarps / 4;  // of converters, half a stage each in turn
     static_assert(128 * kFewRegs + 32 * kEpiWarps * kEpiRegs + 32 * kConvWarps * kConvRegs <= kThreads * kLaunchRegs, "register split");
     static_assert(kThreads * kLaunchRegs <= 65536 && (kGroups == 2 || kGroups == 4), "warps");
     static constexpr int kCtas = kCtas_, kN = kN_, kHalves = kHalves_, kRaw = kRaw_, kOps = kOps_;
-    static constexpr int kStep = kHalves;                   // stages of bytes of a step
+    static constexpr int kStep = kHalves;                   // stages of a step
     static constexpr int kChunkSteps = kChunkStages / kStep;  // steps of an exact fp32 sum
     static constexpr int kTokens = kN * kHalves;
     static constexpr int kBRows = kTokens / kCtas, kHalfRows = kN / kCtas;
     static constexpr int kRawA = 128 * kStageK, kRawBytes = kRawA + kBRows * kStageK;
-    static constexpr int kOpBytes = 2 * kBRows * kOpK;  // tokens in f16, rows of 128 bytes
+    static constexpr int kAtomBytes = kBRows * 128, kOpBytes = 2 * kAtomBytes;  // tokens in f16: two swizzled atoms of 64 of K
     static constexpr int kOpOff = kRaw * kRawBytes;
     static constexpr int kBarOff = kOpOff + kOps * kOpBytes;
     static constexpr int kNumBars = 2 * kRaw + 2 * kOps + 5;
@@ -78,13 +77,13 @@ struct Cfg {
     static constexpr int kMaxTab = 232448 - 1024 - kTabOff;
     static size_t smem(int groups) { return 1024 + (size_t)kTabOff + 4 * (3 * groups + 4); }
     static constexpr int kCols = kHalves == 2 ? kN : kN / 2;  // sums of a lane of the epilogue
-    static constexpr int kTmemA = 2 * kN;                     // first column of the weights' stages, kOpK / 2 columns each
+    static constexpr int kTmemA = 2 * kN;                     // first column of the weights' stages, kStageK / 2 columns each
     static constexpr int kMaxGroups = kMaxTab / 12 - 2;       // whose table fits
     static constexpr int kMine = kBRows / 32;                 // 16-byte chunks of a token row that a converter thread takes
     static_assert(kMaxGroups >= 1, "shared memory");
-    static_assert(kTmemA + kOps * (kOpK / 2) <= kTmemCols, "tensor memory");
+    static_assert(kTmemA + kOps * (kStageK / 2) <= kTmemCols, "tensor memory");
     static_assert(kCols % 16 == 0 && kCols <= 128 && kMine >= 1 && kMine <= 4 && kBRows == 32 * kMine, "tile");
-    static_assert(kOps >= 4 * kStep, "two steps of operands");
+    static_assert(kOps >= 2 * kStep, "two steps of operands");
     static_assert(kCtas == 2 || kBarOff >= 4 * 128 * kTokens, "split sums use the stages' memory");
 };
 
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             mbar_init(raw_free(s), 8);  // (two groups of converters)
         }
         for (int s = 0; s < C::kOps; ++s) {
-            mbar_init(op_full(s), 4 * C::kCtas);  // (the even CTA's; the odd one's is not used)
+            mbar_init(op_full(s), 8 * C::kCtas);  // (the even CTA's; the odd one's is not used)
             mbar_init(op_free(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -289,42 +288,34 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const uint64_t bd0 = kmajor_desc(base + C::kOpOff, 0);
             int it = 0, sums[2] = {0, 0};
             bool ok = true;
-            auto wait_ops = [&](int i) {  // operand stages i and i + 1
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t bar = op_full((i + j) % C::kOps), parity = (uint32_t)((i + j) / C::kOps) & 1u;
-                    const bool there = wait_for<kPair>(bar, parity, p.hdr, abort_flag);
-                    ok = __all_sync(0xffffffffu, there);
-                    if (!ok) return ok;
-                }
-                tc_fence_after();
+            bool ready_op = false;  // operand stage `it` was seen written, by a test a turn ahead
+            auto wait_ops = [&](int i) {
+                if (!__all_sync(0xffffffffu, ready_op))
+                    ok = __all_sync(0xffffffffu, wait_for<kPair>(op_full(i % C::kOps), (uint32_t)(i / C::kOps) & 1u, p.hdr, abort_flag));
+                if (ok) tc_fence_after();
                 return ok;
             };
+            auto test_ops = [&](int i) { ready_op = completed<kPair>(op_full(i % C::kOps), (uint32_t)(i / C::kOps) & 1u); };
             auto wait_acc = [&](int a, int times) {
                 ok = __all_sync(0xffffffffu, wait_for(acc_free(a), ((uint32_t)times & 1u) ^ 1u, p.hdr, abort_flag));
                 if (ok) tc_fence_after();
                 return ok;
             };
-            // the MMAs of operand stages i and i + 1 and half h into buffer a; then what is finished with them
+            // the MMAs of operand stage i and half h into buffer a; then what is finished with them
             auto issue = [&](int i, int h, int a, uint32_t idesc, bool fresh, bool frees, bool ready) {
+                const int s = i % C::kOps;
                 if (elect_one()) {
-                    const uint32_t d = tmem_base + (uint32_t)(a * C::kN);
+                    const uint32_t d = tmem_base + (uint32_t)(a * C::kN), wa = tmem_base + (uint32_t)(C::kTmemA + s * (kStageK / 2));
+                    const uint64_t bd = bd0 + (uint64_t)((s * C::kOpBytes + h * C::kHalfRows * 128) >> 4);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int s = (i + j) % C::kOps;
-                        const uint32_t wa = tmem_base + (uint32_t)(C::kTmemA + s * (kOpK / 2));
-                        const uint64_t bd = bd0 + (uint64_t)((s * C::kOpBytes + h * C::kHalfRows * 128) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < kOpK / 16; ++kk)
-                            mma_ta(d, wa + 8 * kk, bd + (uint64_t)(kk * 2), idesc, !(fresh && j == 0 && kk == 0), kPair);
-                        if (frees) {
-                            if constexpr (kPair) tc2_commit_mc(op_free(s), 0x3);
-                            else tc_commit(op_free(s));
-                        }
-                    }
-                    if (ready) {
-                        if constexpr (kPair) tc2_commit_mc(acc_full(a), 0x3);
-                        else tc_commit(acc_full(a));
+                    for (int kk = 0; kk < kStageK / 16; ++kk)
+                        mma_ta(d, wa + 8 * kk, bd + (uint64_t)((kk / 4 * C::kAtomBytes + kk % 4 * 32) >> 4), idesc, !(fresh && kk == 0), kPair);
+                    if constexpr (kPair) {
+                        if (frees) tc2_commit_mc(op_free(s), 0x3);
+                        if (ready) tc2_commit_mc(acc_full(a), 0x3);
+                    } else {
+                        if (frees) tc_commit(op_free(s));
+                        if (ready) tc_commit(acc_full(a));
                     }
                 }
                 __syncwarp();
@@ -335,11 +326,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 // kind::f16: fp32 sums (bit 4), f16 x f16, both K-major, N >> 3 (bits 17-22), M >> 4 (24-28)
                 const uint32_t idesc = (1u << 4) | ((uint32_t)(tl.n >> 3) << 17) | ((uint32_t)(8 * C::kCtas) << 24);
                 if constexpr (C::kHalves == 1) {
-                    for (int d = 0; d < steps && ok; ++d, it += 2) {
+                    for (int d = 0; d < steps && ok; ++d, ++it) {
                         const bool fresh = d % kChunkStages == 0, ready = d % kChunkStages == kChunkStages - 1 || d == steps - 1;
                         const int a = sums[0] & 1;
                         if (fresh && !wait_acc(a, sums[0] >> 1)) break;
                         if (!wait_ops(it)) break;
+                        test_ops(it + 1);
                         issue(it, 0, a, idesc, fresh, true, ready);
                         if (ready) ++sums[0];
                     }
@@ -352,13 +344,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                             const bool out = taken_out<C>(h == lead, d, steps);
                             if ((fresh >> h & 1) && !wait_acc(h, sums[h])) break;
                             for (int i = 0; i < n; ++i) {
-                                if (o == 0 && !wait_ops(it + 2 * i)) break;
-                                issue(it + 2 * i, h, h, idesc, (fresh >> h & 1) && i == 0, o == 1, out && i == n - 1);
+                                if (o == 0 && !wait_ops(it + i)) break;
+                                if (o == 0 || i == n - 1) test_ops(o == 0 ? it + i + 1 : it + n);
+                                issue(it + i, h, h, idesc, (fresh >> h & 1) && i == 0, o == 1, out && i == n - 1);
                             }
                             fresh = out ? fresh | 1u << h : fresh & ~(1u << h);
                             if (out) ++sums[h];
                         }
-                        it += 2 * n;
+                        it += n;
                     }
                     lead ^= (steps - 1) & 1;  // the half that was first in the last step has had the longer pause
                 }
@@ -373,7 +366,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         }
     } else if (warp >= 4 + kEpiWarps) {  // (the last warps)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-        // groups of four warps convert an operand stage each, in turn: a stage's chain of waits, loads, stores and fences is longer than its MMAs.
+        // groups of four warps convert half a stage each, in turn: the chain of waits, loads, stores and fences is longer than the half's MMAs.
         // A warp has 32 weight rows (a row a lane: tensor memory gives a warp the 32 lanes of its place in four) and a fourth of
         // the tokens' chunks.
         const int q = warp & 3, group = (warp - 4 - kEpiWarps) >> 2, i = group & 1, id = q * 32 + lane;
@@ -382,7 +375,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const uint32_t tmem_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)C::kTmemA;
         int s = group >> 1;                  // stage of bytes, and its round
         uint32_t parity = 0;
-        uint32_t turn = (uint32_t)group;     // of the operand stages
+        uint32_t turn = (uint32_t)s;         // of the operand stages
         int others = s;                      // stages of bytes until this group's next
         bool ok = true, landed = false, freed = true;  // tests made a turn ahead
         for (int64_t t = first; t < total && ok; t += step) {
@@ -417,7 +410,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         to_f16(w[2 * h + j].z, f[8 * j + 4], f[8 * j + 5]);
                         to_f16(w[2 * h + j].w, f[8 * j + 6], f[8 * j + 7]);
                     }
-                    tmem_st16(tmem_row + (uint32_t)(o * (kOpK / 2) + 16 * h), f);
+                    tmem_st16(tmem_row + (uint32_t)(o * (kStageK / 2) + 32 * i + 16 * h), f);
                 }
 #pragma unroll
                 for (int j = 0; j < C::kMine; ++j)
@@ -426,10 +419,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 if (lane == 0) mbar_arrive(raw_free(s));
                 s += C::kGroups / 2;
                 if (s >= C::kRaw) s -= C::kRaw, parity ^= 1u;
-                turn += C::kGroups;
+                turn += C::kGroups / 2;
                 landed = completed(raw_full(s), parity);
                 freed = completed(op_free(turn % C::kOps), (turn / C::kOps & 1u) ^ 1u);
-                const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + row * 128;
+                const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + i * C::kAtomBytes + row * 128;
 #pragma unroll
                 for (int j = 0; j < C::kMine; ++j) {
                     uint32_t u[8];
@@ -555,9 +548,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 // host side
 // ---------------------------------------------------------------------------------------
 
-using Large = Cfg<2, 128, 2, 3, 8, 8, 160, 96>;
-using Pair = Cfg<2, 128, 1, 7, 4, 16, 104, 72>;
-using Mid = Cfg<1, 64, 1, 7, 4, 16, 104, 72>;
+using Large = Cfg<2, 128, 2, 3, 4, 8, 160, 96>;
+using Pair = Cfg<2, 128, 1, 5, 4, 16, 104, 72>;
+using Mid = Cfg<1, 64, 1, 5, 4, 16, 104, 72>;
 
 template <class C, typename Out>
 cudaError_t prepare_kernel(int* resident) {
