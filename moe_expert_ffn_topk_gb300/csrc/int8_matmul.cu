@@ -190,9 +190,8 @@ __device__ __forceinline__ void store_if(bool on, Out* p, float v) {
     else asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.f32 [%1], %2;\n\t}" ::"r"((int)on), "l"(p), "f"(v));
 }
 
-__device__ __forceinline__ float scaled(int c, float b_scale, float a_scale) {
-    return __fmul_rn(__fmul_rn((float)c, b_scale), a_scale);
-}
+// of the integer sum, rounded to fp32
+__device__ __forceinline__ float scaled(float c, float b_scale, float a_scale) { return __fmul_rn(__fmul_rn(c, b_scale), a_scale); }
 
 template <class C, typename Out>
 __global__ void __launch_bounds__(C::kThreads, 1)
@@ -457,7 +456,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             const int m0 = tl.row0 + half * C::kCols;                                        // its first token
             const int cols = C::kHalves == 2 ? C::kCols : min(C::kCols, tl.n - half * C::kCols);  // (multiples of 16; or none)
             const bool live = n - lane < p.N && m0 < tl.hi && cols > 0;
-            int acc[C::kCols];
+            // The sums so far, in fp32 as long as they are integers below 2^24 for certain (`room` is what a lane's next chunks may add up
+            // to), as most sums are to the end; from then on (`wide`, a whole warp's) as integers: the conversion of every value of
+            // every chunk runs at a sixteenth of the rate of an addition and held the MMAs up.
+            uint32_t acc[C::kCols];
+            bool wide = false;
+            float room = 16777216.0f;
 #pragma unroll
             for (int j = 0; j < C::kCols; ++j) acc[j] = 0;
             auto take = [&](int a, uint32_t parity) {
@@ -466,14 +470,45 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 tc_fence_after();
                 if (live) {
                     const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * C::kN + (C::kHalves == 2 ? 0 : half * C::kCols));
+                    int from = 0;  // first group of 16 columns that is added as integers
+                    if (!wide) {
+                        from = C::kCols / 16;
+                        float most = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < C::kCols / 16; ++c) {
-                        if (16 * c >= cols) break;
-                        uint32_t r[16];
-                        tmem_ld16(ta + 16 * c, r);
-                        tmem_ld_wait();
+                        for (int c = 0; c < C::kCols / 16; ++c) {
+                            if (16 * c >= cols) break;
+                            uint32_t r[16];
+                            tmem_ld16(ta + 16 * c, r);
+                            tmem_ld_wait();
+                            float top = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[16 * c + j] += __float2int_rn(__uint_as_float(r[j]));
+                            for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(__uint_as_float(r[j])));
+                            if (__any_sync(0xffffffffu, top > room)) {
+                                from = c;
+                                break;
+                            }
+                            most = fmaxf(most, top);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[16 * c + j] = __float_as_uint(__uint_as_float(acc[16 * c + j]) + __uint_as_float(r[j]));
+                        }
+                        room -= most;
+                        if (from < C::kCols / 16 && 16 * from < cols) {
+                            wide = true;
+#pragma unroll
+                            for (int j = 0; j < C::kCols; ++j) acc[j] = (uint32_t)__float2int_rn(__uint_as_float(acc[j]));
+                        }
+                    }
+                    if (wide) {
+#pragma unroll
+                        for (int c = 0; c < C::kCols / 16; ++c) {
+                            if (16 * c >= cols) break;
+                            if (c < from) continue;
+                            uint32_t r[16];
+                            tmem_ld16(ta + 16 * c, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[16 * c + j] += (uint32_t)__float2int_rn(__uint_as_float(r[j]));
+                        }
                     }
                 }
                 tc_fence_before();
@@ -499,15 +534,21 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 if (live) {
                     int* dst = reinterpret_cast<int*>(smem) + half * C::kCols * 128 + q * 32 + lane;
 #pragma unroll
-                    for (int j = 0; j < C::kCols; ++j) dst[j * 128] = acc[j];
+                    for (int j = 0; j < C::kCols; ++j) dst[j * 128] = wide ? (int)acc[j] : __float2int_rn(__uint_as_float(acc[j]));
                 }
             } else if (live) {
+                if (wide)
+#pragma unroll
+                    for (int j = 0; j < C::kCols; ++j) acc[j] = __float_as_uint((float)(int)acc[j]);
                 const float bs = n < p.N ? __ldg(p.b_scale + (int64_t)tl.g * p.N + n) : 0.0f;
+                const int rows = n < p.N ? min(tl.hi - m0, cols) : 0;
                 Out* dst = static_cast<Out*>(p.out) + (int64_t)m0 * p.out_stride + n;
 #pragma unroll
-                for (int j = 0; j < C::kCols; ++j) {
-                    const int m = m0 + j;
-                    store_if(n < p.N && m < tl.hi, dst + j * p.out_stride, scaled(acc[j], bs, __ldg(p.a_scale + min(m, tl.hi - 1))));
+                for (int c = 0; c < C::kCols; c += 32) {
+                    const float as = __ldg(p.a_scale + min(m0 + c + lane, tl.hi - 1));
+#pragma unroll
+                    for (int j = 0; j < 32; ++j, dst += p.out_stride)
+                        store_if(c + j < rows, dst, scaled(__uint_as_float(acc[c + j]), bs, __shfl_sync(0xffffffffu, as, j)));
                 }
             }
         }
@@ -531,7 +572,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(base + (uint32_t)i * 4u, (uint32_t)k)) : "memory");
                     sum += v;
                 }
-                const float y = scaled(sum, __ldg(p.b_scale + (int64_t)tl.g * p.N + tl.n0 + w), __ldg(p.a_scale + tl.row0 + j));
+                const float y = scaled((float)sum, __ldg(p.b_scale + (int64_t)tl.g * p.N + tl.n0 + w), __ldg(p.a_scale + tl.row0 + j));
                 store_if(true, static_cast<Out*>(p.out) + (int64_t)(tl.row0 + j) * p.out_stride + tl.n0 + w, y);
             }
         }
