@@ -24,7 +24,7 @@
 
 #include "common.cuh"
 #include "group_tiles.cuh"
-#include "ops.h"
+#include "int8_matmul.h"
 #include "tc_common.cuh"
 
 namespace moe {
@@ -189,9 +189,6 @@ __device__ __forceinline__ void store_if(bool on, Out* p, float v) {
     if constexpr (sizeof(Out) == 2) st_global_u16_if(on, p, float_to_bf16_bits(v));
     else asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.f32 [%1], %2;\n\t}" ::"r"((int)on), "l"(p), "f"(v));
 }
-
-// of the integer sum, rounded to fp32
-__device__ __forceinline__ float scaled(float c, float b_scale, float a_scale) { return __fmul_rn(__fmul_rn(c, b_scale), a_scale); }
 
 template <class C, typename Out>
 __global__ void __launch_bounds__(C::kThreads, 1)
@@ -548,7 +545,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     const float as = __ldg(p.a_scale + min(m0 + c + lane, tl.hi - 1));
 #pragma unroll
                     for (int j = 0; j < 32; ++j, dst += p.out_stride)
-                        store_if(c + j < rows, dst, scaled(__uint_as_float(acc[c + j]), bs, __shfl_sync(0xffffffffu, as, j)));
+                        store_if(c + j < rows, dst, int8_scaled(__uint_as_float(acc[c + j]), bs, __shfl_sync(0xffffffffu, as, j)));
                 }
             }
         }
@@ -572,7 +569,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(base + (uint32_t)i * 4u, (uint32_t)k)) : "memory");
                     sum += v;
                 }
-                const float y = scaled((float)sum, __ldg(p.b_scale + (int64_t)tl.g * p.N + tl.n0 + w), __ldg(p.a_scale + tl.row0 + j));
+                const float y = int8_scaled((float)sum, __ldg(p.b_scale + (int64_t)tl.g * p.N + tl.n0 + w), __ldg(p.a_scale + tl.row0 + j));
                 store_if(true, static_cast<Out*>(p.out) + (int64_t)(tl.row0 + j) * p.out_stride + tl.n0 + w, y);
             }
         }
@@ -591,7 +588,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
 using Large = Cfg<2, 128, 2, 3, 4, 8, 160, 96>;
 using Pair = Cfg<2, 128, 1, 5, 4, 16, 104, 72>;
-using Mid = Cfg<1, 64, 1, 5, 4, 16, 104, 72>;
+using Mid = Cfg<1, 128, 1, 3, 3, 16, 104, 72>;
+using Small = Cfg<1, 64, 1, 5, 4, 16, 104, 72>;
 
 template <class C, typename Out>
 cudaError_t prepare_kernel(int* resident) {
@@ -659,15 +657,17 @@ template <typename Out>
 cudaError_t launch_out(const moe_int8_matmul_args& a, const Args& p, cudaStream_t s) {
     const int sms = tc_num_sms();
     const int64_t n_tiles = (a.N + 255) / 256;
+    if (a.groups == 1 ? a.M <= 16 : a.M <= 16 * a.groups && a.groups * ((a.N + 127) / 128) < sms) return launch_int8_few(a, s);
     if (a.groups <= Large::kMaxGroups && a.M / a.groups >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, 1, s);
     const int64_t row_tiles = (a.M + 127) / 128 + (a.groups > 1 ? std::min<int64_t>(a.groups, a.M) / 2 : 0);
-    if (row_tiles * n_tiles * 4 >= sms) return launch<Pair, Out>(a, p, 1, s);
+    if (a.M / a.groups > 16 && row_tiles * n_tiles * 4 >= sms) return launch<Pair, Out>(a, p, 1, s);
     // few tiles: the stages are shared by a cluster's CTAs as long as all tiles run at once
+    const bool wide = a.M / a.groups > 64;
     int split = 1;
-    const int64_t tiles = ((a.M + 63) / 64) * ((a.N + 127) / 128);
+    const int64_t tokens = wide ? Mid::kTokens : Small::kTokens, tiles = ((a.M + tokens - 1) / tokens) * ((a.N + 127) / 128);
     if (a.groups == 1)
         while (split < 8 && tiles * split * 2 <= sms && p.kb_count >= split * 4) split *= 2;
-    return launch<Mid, Out>(a, p, split, s);
+    return wide ? launch<Mid, Out>(a, p, split, s) : launch<Small, Out>(a, p, split, s);
 }
 
 }  // namespace
