@@ -538,12 +538,36 @@ _COPIED_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32, tor
                  torch.uint8: MOE_TYPE_CODES8, torch.float8_e4m3fn: MOE_TYPE_CODES8, torch.float8_e5m2: MOE_TYPE_CODES8}
 
 
-def _same_place(first, *others):
-    """Tensors on other devices than `first` would be read as memory of its device."""
-    device = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"the tensors are on {first.device} and {t.device}")
+def _there(t, what, dtype, shape, device):
+    """Address of a contiguous tensor of that type and shape on that device (each tensor is looked at once: a small call's time is
+    the host's)."""
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on device {device}, with the other tensors, not on {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_there(t, what, rows, cols, device):
+    """Row stride of a matrix of that shape on that device whose rows are contiguous (a column slice of a wider one is)."""
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on device {device}, with the other tensors, not on {t.device}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} must have shape {(rows, cols)}, not {tuple(t.shape)}")
+    stride, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    return stride if rows > 1 else cols
+
+
+def _space_there(workspace, device):
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous memory of device {device}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def moe_permute(x, topk_ids, d: MoeDims, rows, offsets, row_src, slot_row, workspace, scale=None, row_scale=None, stream=None):
@@ -552,28 +576,28 @@ def moe_permute(x, topk_ids, d: MoeDims, rows, offsets, row_src, slot_row, works
     [T,S]) row_scale ([T*K,S]) is written too. Rows of x and rows may be strided. The gradient of x is moe_unpermute of the rows'
     gradients without weights."""
     T, E, K = d.num_tokens, d.num_experts, d.topk
-    H = x.shape[-1]
+    H, device, dtype = x.shape[-1], x.get_device(), x.dtype
+    handle = _handle(stream, x)
     try:
-        kind = _COPIED_TYPES[x.dtype]
+        kind = _COPIED_TYPES[dtype]
     except KeyError:
         raise TypeError("x must be bfloat16, float32 or 8-bit codes") from None
-    if rows.dtype is not x.dtype:
-        raise TypeError(f"rows must be {x.dtype}, as x is")
+    if rows.dtype is not dtype:
+        raise TypeError(f"rows must be {dtype}, as x is")
     if (scale is None) != (row_scale is None):
         raise ValueError("scale and row_scale come together")
-    scales = 0
+    scales, from_scale, to_scale = 0, None, None
     if scale is not None:
         scales = scale.shape[-1]
-        _vec(scale, "scale", torch.float32, (T, scales))
-        _vec(row_scale, "row_scale", torch.float32, (T * K, scales))
-    _same_place(x, topk_ids, rows, offsets, row_src, slot_row, workspace, scale, row_scale)
-    ws, nbytes = _space(workspace)
-    args = MoePermuteArgs(x.data_ptr(), None if scale is None else scale.data_ptr(), _vec(topk_ids, "topk_ids", torch.int32, (T, K)),
-                          rows.data_ptr(), None if scale is None else row_scale.data_ptr(),
-                          _vec(offsets, "offsets", torch.int32, (E + 1,)), _vec(row_src, "row_src", torch.int32, (T * K,)),
-                          _vec(slot_row, "slot_row", torch.int32, (T, K)), H, _rows(x, "x", (T, H)),
-                          _rows(rows, "rows", (T * K, H)), kind, scales)
-    status = LIB.moe_permute(args, d, ws, nbytes, _handle(stream, x))
+        from_scale = _there(scale, "scale", torch.float32, (T, scales), device)
+        to_scale = _there(row_scale, "row_scale", torch.float32, (T * K, scales), device)
+    ws, nbytes = _space_there(workspace, device)
+    i32 = torch.int32
+    args = MoePermuteArgs(x.data_ptr(), from_scale, _there(topk_ids, "topk_ids", i32, (T, K), device), rows.data_ptr(), to_scale,
+                          _there(offsets, "offsets", i32, (E + 1,), device), _there(row_src, "row_src", i32, (T * K,), device),
+                          _there(slot_row, "slot_row", i32, (T, K), device), H, _rows_there(x, "x", T, H, device),
+                          _rows_there(rows, "rows", T * K, H, device), kind, scales)
+    status = LIB.moe_permute(args, d, ws, nbytes, handle)
     if status:
         raise MoeError(status, "moe_permute")
 
@@ -582,12 +606,12 @@ def moe_unpermute(rows, slot_row, y, weights=None, stream=None):
     """y ([T,H], bf16 or fp32) = the sum over k of weights[:,k] * rows[slot_row[:,k]] (rows [T*K,H], bf16 or fp32; slot_row int32 [T,K]
     of moe_permute, -1: adds nothing; weights fp32 [T,K], or None: 1). Rows of rows and y may be strided."""
     T, K = slot_row.shape
-    H = y.shape[-1]
-    _same_place(rows, slot_row, y, weights)
-    status = LIB.moe_unpermute(rows.data_ptr(), _float_type(rows, "rows"), _rows(rows, "rows", (T * K, H)),
-                               _vec(slot_row, "slot_row", torch.int32, (T, K)),
-                               None if weights is None else _vec(weights, "weights", torch.float32, (T, K)), MoeDims(T, 0, 0, 0, K, 0),
-                               H, y.data_ptr(), _float_type(y, "y"), _rows(y, "y", (T, H)), _handle(stream, rows))
+    H, device = y.shape[-1], rows.get_device()
+    status = LIB.moe_unpermute(rows.data_ptr(), _float_type(rows, "rows"), _rows_there(rows, "rows", T * K, H, device),
+                               _there(slot_row, "slot_row", torch.int32, (T, K), device),
+                               None if weights is None else _there(weights, "weights", torch.float32, (T, K), device),
+                               MoeDims(T, 0, 0, 0, K), H, y.data_ptr(), _float_type(y, "y"), _rows_there(y, "y", T, H, device),
+                               _handle(stream, rows))
     if status:
         raise MoeError(status, "moe_unpermute")
 
@@ -596,32 +620,33 @@ def moe_unpermute_backward(dy, slot_row, d_rows, weights=None, rows=None, d_weig
     """Gradients of moe_unpermute: d_rows ([T*K,H], the rows' type) from dy ([T,H], bf16 or fp32) and the weights, and, with rows
     ([T*K,H]) and d_weights (fp32 [T,K]), the weights' gradient. Rows of d_rows that no slot names are left as they are."""
     T, K = slot_row.shape
-    H = dy.shape[-1]
+    H, device = dy.shape[-1], dy.get_device()
     if (rows is None) != (d_weights is None):
         raise ValueError("rows and d_weights come together")
-    if rows is not None and rows.dtype is not d_rows.dtype:
-        raise TypeError(f"d_rows must be {rows.dtype}, as rows is")
-    _same_place(dy, slot_row, d_rows, weights, rows, d_weights)
-    status = LIB.moe_unpermute_backward(dy.data_ptr(), _float_type(dy, "dy"), _rows(dy, "dy", (T, H)),
-                                        None if rows is None else rows.data_ptr(), _float_type(d_rows, "d_rows"),
-                                        H if rows is None else _rows(rows, "rows", (T * K, H)),
-                                        _vec(slot_row, "slot_row", torch.int32, (T, K)),
-                                        None if weights is None else _vec(weights, "weights", torch.float32, (T, K)),
-                                        MoeDims(T, 0, 0, 0, K, 0), H, d_rows.data_ptr(), _rows(d_rows, "d_rows", (T * K, H)),
-                                        None if rows is None else _vec(d_weights, "d_weights", torch.float32, (T, K)),
-                                        _handle(stream, dy))
+    values, stride, gradient = None, H, None
+    if rows is not None:
+        if rows.dtype is not d_rows.dtype:
+            raise TypeError(f"d_rows must be {rows.dtype}, as rows is")
+        values, stride = rows.data_ptr(), _rows_there(rows, "rows", T * K, H, device)
+        gradient = _there(d_weights, "d_weights", torch.float32, (T, K), device)
+    status = LIB.moe_unpermute_backward(dy.data_ptr(), _float_type(dy, "dy"), _rows_there(dy, "dy", T, H, device), values,
+                                        _float_type(d_rows, "d_rows"), stride, _there(slot_row, "slot_row", torch.int32, (T, K), device),
+                                        None if weights is None else _there(weights, "weights", torch.float32, (T, K), device),
+                                        MoeDims(T, 0, 0, 0, K), H, d_rows.data_ptr(), _rows_there(d_rows, "d_rows", T * K, H, device),
+                                        gradient, _handle(stream, dy))
     if status:
         raise MoeError(status, "moe_unpermute_backward")
 
 
 def moe_int8_quantize(x, q, scale, stream=None):
     """Rows of x (bf16 or fp32 [M,K]) into q (int8 [M,K]) and scale (fp32 [M]); rows of x and q may be strided."""
-    M, K = shape = x.shape
+    M, K = x.shape
+    device = x.get_device()
     if q.dtype is not torch.int8:
         raise TypeError("q must be int8")
-    _same_place(x, q, scale)
-    status = LIB.moe_int8_quantize(x.data_ptr(), _float_type(x, "x"), M, K, _rows(x, "x", shape), q.data_ptr(), _rows(q, "q", shape),
-                                   _vec(scale, "scale", torch.float32, (M,)), _handle(stream, x))
+    status = LIB.moe_int8_quantize(x.data_ptr(), _float_type(x, "x"), M, K, _rows_there(x, "x", M, K, device), q.data_ptr(),
+                                   _rows_there(q, "q", M, K, device), _there(scale, "scale", torch.float32, (M,), device),
+                                   _handle(stream, x))
     if status:
         raise MoeError(status, "moe_int8_quantize")
 
@@ -636,8 +661,8 @@ def moe_int8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream
     [offsets[g], offsets[g+1]) are multiplied by b[g]. Rows of a, b and out may be strided."""
     if a.dtype is not torch.int8 or b.dtype is not torch.int8:
         raise TypeError("a and b must be int8")
-    shape = a.shape
-    M, K = shape
+    M, K = a.shape
+    device = a.get_device()
     if b.dim() == 3:
         G, N, k2 = b.shape
         between, b_stride, one = b.stride()
@@ -645,16 +670,16 @@ def moe_int8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream
             raise ValueError("the groups of b must follow each other")
     else:
         G, (N, k2), (b_stride, one) = 1, b.shape, b.stride()
-    if k2 != K or not b.is_cuda or one != 1:
-        raise ValueError(f"b must be device memory of {K} contiguous columns")
+    if k2 != K or b.get_device() != device or one != 1:
+        raise ValueError(f"b must be memory of device {device} of {K} contiguous columns")
     if G * N == 1:
         b_stride = K
-    _same_place(a, a_scale, b, b_scale, out, workspace, offsets)
-    ws, nbytes = _space(workspace)
-    args = MoeInt8MatmulArgs(a.data_ptr(), _vec(a_scale, "a_scale", torch.float32, (M,)), b.data_ptr(),
-                             _vec(b_scale, "b_scale", torch.float32, (N,) if b_scale.dim() == 1 and G == 1 else (G, N)),
-                             None if offsets is None else _vec(offsets, "offsets", torch.int32, (G + 1,)), out.data_ptr(), M, N, K,
-                             _rows(a, "a", shape), b_stride, _rows(out, "out", (M, N)), G, _float_type(out, "out"))
+    ws, nbytes = _space_there(workspace, device)
+    args = MoeInt8MatmulArgs(a.data_ptr(), _there(a_scale, "a_scale", torch.float32, (M,), device), b.data_ptr(),
+                             _there(b_scale, "b_scale", torch.float32, (N,) if b_scale.dim() == 1 and G == 1 else (G, N), device),
+                             None if offsets is None else _there(offsets, "offsets", torch.int32, (G + 1,), device), out.data_ptr(), M,
+                             N, K, _rows_there(a, "a", M, K, device), b_stride, _rows_there(out, "out", M, N, device), G,
+                             _float_type(out, "out"))
     status = LIB.moe_int8_matmul(args, ws, nbytes, _handle(stream, a))
     if status:
         raise MoeError(status, "moe_int8_matmul")

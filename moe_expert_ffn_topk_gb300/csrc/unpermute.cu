@@ -127,35 +127,39 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(UnpermuteArgs p) {
     __shared__ float part[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % G;
     const int64_t slot = (int64_t)blockIdx.x * (kWarps / G) + warp / G, slots = (int64_t)p.T * p.K;
-    const int row = slot_row_of(p, slot, slot < slots);
+    const bool there = slot < slots;
+    const float w = p.weights && there ? __ldg(p.weights + slot) : 1.0f;
+    const int row = slot_row_of(p, slot, there);
+    const Y* dy = static_cast<const Y*>(p.dy) + (there ? slot / p.K : 0) * p.dy_stride;
+    const R* in = static_cast<const R*>(p.rows) + (int64_t)row * p.rows_stride;
+    R* out = static_cast<R*>(p.out) + (int64_t)row * p.out_stride;
     float dot = 0.0f;
-    if (row >= 0) {
-        const float w = p.weights ? __ldg(p.weights + slot) : 1.0f;
-        const Y* dy = static_cast<const Y*>(p.dy) + slot / p.K * p.dy_stride;
-        const R* in = static_cast<const R*>(p.rows) + (int64_t)row * p.rows_stride;
-        R* out = static_cast<R*>(p.out) + (int64_t)row * p.out_stride;
-        constexpr int kBatch = 4;
-        for (int64_t c0 = (int64_t)sub * 32 * N * kBatch; c0 < p.H; c0 += (int64_t)G * 32 * N * kBatch) {
-            Packed<Y, N> a[kBatch];
-            Packed<R, N> b[kBatch];
+    constexpr int kBatch = N == 1 ? 8 : 4;
+    for (int64_t c0 = (int64_t)sub * 32 * N * kBatch; c0 < p.H; c0 += (int64_t)G * 32 * N * kBatch) {
+        Packed<Y, N> a[kBatch];
+        Packed<R, N> b[kBatch];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int64_t c = c0 + (j * 32 + lane) * N;
-                a[j].load(dy + c, c < p.H);
-                b[j].load(in + c, p.d_weights && c < p.H);
-            }
+        for (int j = 0; j < kBatch; ++j) {  // (the token's values first: they do not wait for the slot's row)
+            const int64_t c = c0 + (j * 32 + lane) * N;
+            a[j].load(dy + c, there && c < p.H);
+        }
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int64_t c = c0 + (j * 32 + lane) * N;
-                if (c >= p.H) continue;
-                if (p.d_weights)
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t c = c0 + (j * 32 + lane) * N;
+            b[j].load(in + c, p.d_weights && row >= 0 && c < p.H);
+        }
+        if (row < 0) break;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) dot = __fmaf_rn(a[j].at(i), b[j].at(i), dot);
-                float grad[N];
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t c = c0 + (j * 32 + lane) * N;
+            if (c >= p.H) continue;
+            if (p.d_weights)
 #pragma unroll
-                for (int i = 0; i < N; ++i) grad[i] = a[j].at(i) * w;
-                store<R, N>(out + c, grad);
-            }
+                for (int i = 0; i < N; ++i) dot = __fmaf_rn(a[j].at(i), b[j].at(i), dot);
+            float grad[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) grad[i] = a[j].at(i) * w;
+            store<R, N>(out + c, grad);
         }
     }
     if (!p.d_weights) return;
