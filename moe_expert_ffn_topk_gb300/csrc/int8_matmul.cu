@@ -36,6 +36,7 @@ using namespace tc;
 constexpr int kEpiWarps = 8;
 constexpr int kFewRegs = 48, kConvRegs = 56;  // registers of warps 0-3 and of the converters
 constexpr int kTmemCols = 512;
+constexpr int kMaxSplit = 8;  // CTAs of a cluster that share a tile
 constexpr int kStageK = 128;                  // codes of K in a stage
 constexpr int kChunkStages = 1024 / kStageK;  // stages of an exact fp32 sum
 
@@ -221,6 +222,17 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int kb1 = kPair ? p.kb_count : (int)((int64_t)p.kb_count * (rank + 1) / split);
     const int steps = (kb1 - kb0 + C::kStep - 1) / C::kStep;
 
+    // bytes of stage kb of the tile whose weight rows begin at wrow and tokens at trow, into slot s
+    auto load_stage = [&](int s, int kb, int wrow, int trow) {
+        const uint32_t dst = base + s * C::kRawBytes;
+        mbar_arrive_expect_tx(raw_full(s), C::kRawBytes);
+        tma_load_2d(dst, &tmB, kb * kStageK, wrow, raw_full(s));
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+            tma_load_2d(dst + C::kRawA + h * C::kHalfRows * kStageK, &tmA, kb * kStageK, trow + h * C::kN, raw_full(s));
+    };
+    int early = 0;  // stages that the producer has sent for already
+
     if (warp == 2) write_group_tiles(p.offsets, p.M, p.groups, C::kTokens, tab, lane);
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kRaw; ++s) {
@@ -238,8 +250,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         mbar_init(end_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
+        // without groups the first tile is known before the table: its first stages are on their way while the rest is set up (in this CTA's
+        // memory, on barriers that this thread has just made)
+        if (!p.offsets && first < (int64_t)((p.M - 1) / C::kTokens + 1) * p.n_tiles) {
+            const int mt = (p.M - 1) / C::kTokens + 1, row0 = (int)(first % mt) * C::kTokens;
+            const int n = C::kHalves == 2 ? C::kN : min(C::kN, (p.M - row0 + 15) & ~15);
+            for (early = 0; early < min(C::kRaw, kb1 - kb0); ++early)
+                load_stage(early, kb0 + early, (int)(first / mt) * 128 * C::kCtas + half_cta * 128, row0 + half_cta * (n / C::kCtas));
+        }
     }
     if (warp == 1) {
         if constexpr (kPair) tmem_alloc_pair(smem_u32(tmem_holder), kTmemCols);
@@ -263,16 +281,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 const int wrow = tl.g * p.N + tl.n0 + half_cta * 128;
                 const int trow = tl.row0 + half_cta * (tl.n / C::kCtas);
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    if (!wait_for(raw_free(s), parity, p.hdr, abort_flag)) {
-                        ok = false;
-                        break;
+                    if (it >= early) {
+                        if (!wait_for(raw_free(s), parity, p.hdr, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        load_stage(s, kb, wrow, trow);
                     }
-                    const uint32_t dst = base + s * C::kRawBytes;
-                    mbar_arrive_expect_tx(raw_full(s), C::kRawBytes);
-                    tma_load_2d(dst, &tmB, kb * kStageK, wrow, raw_full(s));
-#pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-                        tma_load_2d(dst + C::kRawA + h * C::kHalfRows * kStageK, &tmA, kb * kStageK, trow + h * C::kN, raw_full(s));
                     if (++s == C::kRaw) s = 0, parity ^= 1u;
                 }
             }
@@ -560,17 +575,28 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             // every CTA adds its share of the tile's values
             const Tile tl = decode<C>(first, tab, p.groups, p.n_tiles);
             const int rows = min(C::kTokens, tl.hi - tl.row0), n_end = min(128, p.N - tl.n0);
-            for (int i = (int)rank * C::kThreads + threadIdx.x; i < rows * 128; i += split * C::kThreads) {
-                const int j = i / 128, w = i % 128;
-                if (w >= n_end) continue;
-                int sum = 0;
-                for (int k = 0; k < split; ++k) {
-                    int v;
-                    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(base + (uint32_t)i * 4u, (uint32_t)k)) : "memory");
-                    sum += v;
+            for (int i = (int)rank * C::kThreads + threadIdx.x; i < rows * 32; i += split * C::kThreads) {
+                const int j = i / 32, w = i % 32 * 4;  // token, and the first of four weight rows
+                int v[kMaxSplit][4];
+#pragma unroll
+                for (int k = 0; k < kMaxSplit; ++k) {  // (all on their way at once)
+                    if (k < split)
+                        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v[k][0]), "=r"(v[k][1]), "=r"(v[k][2]), "=r"(v[k][3])
+                                     : "r"(mapa_shared(base + (uint32_t)i * 16u, (uint32_t)k))
+                                     : "memory");
+                    else v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0;
                 }
-                const float y = int8_scaled((float)sum, __ldg(p.b_scale + (int64_t)tl.g * p.N + tl.n0 + w), __ldg(p.a_scale + tl.row0 + j));
-                store_if(true, static_cast<Out*>(p.out) + (int64_t)(tl.row0 + j) * p.out_stride + tl.n0 + w, y);
+                const float as = __ldg(p.a_scale + tl.row0 + j);
+                const float* bs = p.b_scale + (int64_t)tl.g * p.N + tl.n0 + w;
+                Out* dst = static_cast<Out*>(p.out) + (int64_t)(tl.row0 + j) * p.out_stride + tl.n0 + w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    int sum = 0;
+#pragma unroll
+                    for (int k = 0; k < kMaxSplit; ++k) sum += v[k][e];
+                    if (w + e < n_end) store_if(true, dst + e, int8_scaled((float)sum, __ldg(bs + e), as));
+                }
             }
         }
         __syncthreads();
@@ -666,7 +692,7 @@ cudaError_t launch_out(const moe_int8_matmul_args& a, const Args& p, cudaStream_
     int split = 1;
     const int64_t tokens = wide ? Mid::kTokens : Small::kTokens, tiles = ((a.M + tokens - 1) / tokens) * ((a.N + 127) / 128);
     if (a.groups == 1)
-        while (split < 8 && tiles * split * 2 <= sms && p.kb_count >= split * 4) split *= 2;
+        while (split < kMaxSplit && tiles * split * 2 <= sms && p.kb_count >= split * 4) split *= 2;
     return wide ? launch<Mid, Out>(a, p, split, s) : launch<Small, Out>(a, p, split, s);
 }
 

@@ -21,6 +21,7 @@ using namespace tc;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStepK = 128;
+constexpr int kMaxSplit = 8;  // CTAs of a cluster
 
 struct FewArgs {
     const int8_t* a;
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, kTokens <= 2 || kTokens == 8 ? 3 : 2
     constexpr bool kMma = kTokens >= 8;
     constexpr int kTiles = kMma ? kTokens / 8 : kTokens;  // rows of a that a lane reads
     __shared__ int sums[kWarps][kTokens][16];
-    __shared__ int bounds[2];
+    __shared__ int bounds[2], total[kTokens * 16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = blockIdx.y, n0 = (int)(blockIdx.x / p.split) * 16;
     const uint32_t rank = p.split > 1 ? cluster_ctarank() : 0u;
@@ -151,24 +152,35 @@ __global__ void __launch_bounds__(kThreads, kTokens <= 2 || kTokens == 8 ? 3 : 2
             }
         }
         __syncthreads();
-        if (p.split > 1) cluster_sync();
-        // the CTAs of a cluster add up a share of the values each
-        for (int i = (int)rank * kThreads + threadIdx.x; i < kTokens * 16; i += p.split * kThreads) {
-            const int m = m0 + i / 16, n = n0 + i % 16;
-            if (m >= hi || n >= p.N) continue;
-            int sum = 0;
-            for (int k = 0; k < p.split; ++k)
+        // the warps' sums, then those of the cluster's CTAs, a share of the values each
+        static_assert(kTokens * 16 <= kThreads, "a value a thread");
+        int sum = 0;
+        if (threadIdx.x < kTokens * 16)
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    int s;
-                    if (p.split > 1)
+            for (int w = 0; w < kWarps; ++w) sum += (&sums[w][0][0])[threadIdx.x];
+        bool mine = threadIdx.x < kTokens * 16;
+        if (p.split > 1) {
+            if (mine) total[threadIdx.x] = sum;
+            cluster_sync();
+            mine = mine && threadIdx.x % p.split == rank;
+            if (mine) {
+                int s[kMaxSplit];
+#pragma unroll
+                for (int k = 0; k < kMaxSplit; ++k) {  // (all on their way at once)
+                    s[k] = 0;
+                    if (k < p.split)
                         asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                                     : "=r"(s)
-                                     : "r"(mapa_shared(smem_u32(&sums[w][0][0] + i), (uint32_t)k))
+                                     : "=r"(s[k])
+                                     : "r"(mapa_shared(smem_u32(total + threadIdx.x), (uint32_t)k))
                                      : "memory");
-                    else s = (&sums[w][0][0])[i];
-                    sum += s;
                 }
+                sum = 0;
+#pragma unroll
+                for (int k = 0; k < kMaxSplit; ++k) sum += s[k];
+            }
+        }
+        const int m = m0 + threadIdx.x / 16, n = n0 + threadIdx.x % 16;
+        if (mine && m < hi && n < p.N) {
             const float y = int8_scaled((float)sum, __ldg(p.b_scale + (int64_t)g * p.N + n), __ldg(p.a_scale + m));
             if constexpr (sizeof(Out) == 2) static_cast<uint16_t*>(p.out)[(int64_t)m * p.out_stride + n] = float_to_bf16_bits(y);
             else static_cast<float*>(p.out)[(int64_t)m * p.out_stride + n] = y;
@@ -224,7 +236,7 @@ cudaError_t launch_int8_few(const moe_int8_matmul_args& a, cudaStream_t s) {
     p.M = (int)a.M, p.N = (int)a.N, p.K = (int)a.K, p.groups = a.groups;
     // K over a cluster's CTAs where the weight rows give every SM less than a CTA, while every warp keeps a step
     p.split = 1;
-    while (p.split < 8 && (int64_t)(a.N + 15) / 16 * a.groups * p.split < tc_num_sms() && a.K >= (int64_t)kStepK * kWarps * 2 * p.split) p.split *= 2;
+    while (p.split < kMaxSplit && (int64_t)(a.N + 15) / 16 * a.groups * p.split < tc_num_sms() && a.K >= (int64_t)kStepK * kWarps * 2 * p.split) p.split *= 2;
     return a.out_type == MOE_TYPE_BF16 ? launch_out<__nv_bfloat16>(p, s) : launch_out<float>(p, s);
 }
 
