@@ -76,10 +76,11 @@ struct Cfg {
     static constexpr int kMiscOff = kBarOff + 8 * ((kNumBars + 1) & ~1);
     static constexpr int kTabOff = kMiscOff + 16;
     static constexpr int kMaxTab = 232448 - 1024 - kTabOff;
-    static size_t smem(int groups) { return 1024 + (size_t)kTabOff + 4 * (3 * groups + 4); }
+    static constexpr int kScales = kCtas == 1 ? 128 + kTokens : 0;  // floats of a split tile's scales, behind the table
+    static size_t smem(int groups) { return 1024 + (size_t)kTabOff + 4 * (3 * groups + 4) + 4 * kScales; }
     static constexpr int kCols = kHalves == 2 ? kN : kN / 2;  // sums of a lane of the epilogue
     static constexpr int kTmemA = 2 * kN;                     // first column of the weights' stages, kStageK / 2 columns each
-    static constexpr int kMaxGroups = kMaxTab / 12 - 2;       // whose table fits
+    static constexpr int kMaxGroups = (kMaxTab - 4 * kScales) / 12 - 2;  // whose table fits
     static constexpr int kMine = kBRows / 32;                 // 16-byte chunks of a token row that a converter thread takes
     static_assert(kMaxGroups >= 1, "shared memory");
     static_assert(kTmemA + kOps * (kStageK / 2) <= kTmemCols, "tensor memory");
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     int* tab = reinterpret_cast<int*>(smem + C::kTabOff);
+    float* tile_scales = reinterpret_cast<float*>(tab + 3 * p.groups + 4);  // (split tiles) of 128 weight rows, then of the tokens
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = kPair ? 1 : p.split;
@@ -374,6 +376,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             }
             __syncwarp();
             mbar_drain(end_bar, 0, p.hdr);
+        } else if (warp == 3 && !kPair && split > 1 && first < total) {
+            const Tile tl = decode<C>(first, tab, p.groups, p.n_tiles);
+            for (int i = lane; i < 128; i += 32) tile_scales[i] = tl.n0 + i < p.N ? __ldg(p.b_scale + (int64_t)tl.g * p.N + tl.n0 + i) : 0.0f;
+            for (int i = lane; i < C::kTokens; i += 32) tile_scales[128 + i] = tl.row0 + i < tl.hi ? __ldg(p.a_scale + tl.row0 + i) : 0.0f;
         }
     } else if (warp >= 4 + kEpiWarps) {  // (the last warps)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
@@ -572,11 +578,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tc_fence_after();
     if (!kPair && split > 1) {
         if (first < total) {
-            // every CTA adds its share of the tile's values
+            // every CTA adds up its share of the tile's values, of four weight rows of a token at a time
             const Tile tl = decode<C>(first, tab, p.groups, p.n_tiles);
-            const int rows = min(C::kTokens, tl.hi - tl.row0), n_end = min(128, p.N - tl.n0);
+            const int rows = min(C::kTokens, tl.hi - tl.row0);
             for (int i = (int)rank * C::kThreads + threadIdx.x; i < rows * 32; i += split * C::kThreads) {
-                const int j = i / 32, w = i % 32 * 4;  // token, and the first of four weight rows
+                const int j = i / 32, w = i % 32 * 4;  // token, and the first of the weight rows
                 int v[kMaxSplit][4];
 #pragma unroll
                 for (int k = 0; k < kMaxSplit; ++k) {  // (all on their way at once)
@@ -587,15 +593,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                                      : "memory");
                     else v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0;
                 }
-                const float as = __ldg(p.a_scale + tl.row0 + j);
-                const float* bs = p.b_scale + (int64_t)tl.g * p.N + tl.n0 + w;
                 Out* dst = static_cast<Out*>(p.out) + (int64_t)(tl.row0 + j) * p.out_stride + tl.n0 + w;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     int sum = 0;
 #pragma unroll
                     for (int k = 0; k < kMaxSplit; ++k) sum += v[k][e];
-                    if (w + e < n_end) store_if(true, dst + e, int8_scaled((float)sum, __ldg(bs + e), as));
+                    store_if(tl.n0 + w + e < p.N, dst + e, int8_scaled((float)sum, tile_scales[w + e], tile_scales[128 + j]));
                 }
             }
         }
@@ -617,38 +621,41 @@ using Pair = Cfg<2, 128, 1, 5, 4, 16, 104, 72>;
 using Mid = Cfg<1, 128, 1, 3, 3, 16, 104, 72>;
 using Small = Cfg<1, 64, 1, 5, 4, 16, 104, 72>;
 
+// Attributes of the kernel on the current device; resident[s]: clusters of s CTAs that run at once there (of 2 for pairs; of each size that a
+// tile may be split over, for the others). A cluster's CTAs share a GPC, so fewer fit than the SMs would hold.
 template <class C, typename Out>
-cudaError_t prepare_kernel(int* resident) {
-    static int clusters[kMaxDevices];
+cudaError_t prepare_kernel(const int** resident) {
+    static int clusters[kMaxDevices][kMaxSplit + 1];
     int device = 0;
     const cudaError_t err = once_per_device(&device, [](int dev) {
         cudaError_t e = cudaFuncSetAttribute(int8_matmul_kernel<C, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
         if (e == cudaSuccess) e = check_register_split(reinterpret_cast<const void*>(int8_matmul_kernel<C, Out>), C::kLaunchRegs);
-        if (C::kCtas == 1 || e != cudaSuccess) return e;
-        // pairs that can be resident at once (a pair needs two free SMs of one GPC)
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * std::max(1, tc_num_sms() / 2));
-        cfg.blockDim = dim3(C::kThreads);
-        cfg.dynamicSmemBytes = C::smem(1);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&clusters[dev], int8_matmul_kernel<C, Out>, &cfg) != cudaSuccess || clusters[dev] < 1) {
-            (void)cudaGetLastError();
-            clusters[dev] = std::max(1, tc_num_sms() / 2);
+        for (int size = C::kCtas; size <= (C::kCtas == 2 ? 2 : kMaxSplit) && e == cudaSuccess; ++size) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(size * std::max(1, tc_num_sms() / size));
+            cfg.blockDim = dim3(C::kThreads);
+            cfg.dynamicSmemBytes = C::smem(1);
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = size;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&clusters[dev][size], int8_matmul_kernel<C, Out>, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                clusters[dev][size] = 0;
+            }
         }
+        if (clusters[dev][C::kCtas] < 1) clusters[dev][C::kCtas] = std::max(1, tc_num_sms() / C::kCtas);
         return e;
     });
-    *resident = err == cudaSuccess ? clusters[device] : 0;
+    *resident = clusters[device];
     return err;
 }
 
 template <class C, typename Out>
-cudaError_t launch(const moe_int8_matmul_args& a, Args p, int split, cudaStream_t s) {
-    int resident = 0;
+cudaError_t launch(const moe_int8_matmul_args& a, Args p, cudaStream_t s) {
+    const int* resident;
     const cudaError_t err = prepare_kernel<C, Out>(&resident);
     if (err != cudaSuccess) return err;
     CUtensorMap ma, mb;
@@ -659,12 +666,17 @@ cudaError_t launch(const moe_int8_matmul_args& a, Args p, int split, cudaStream_
         !tc_make_map_nd(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.b, db, sb, boxb, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     p.n_tiles = (p.N + 128 * C::kCtas - 1) / (128 * C::kCtas);
-    p.split = split;
     // row tiles: at most one unfilled per group (and none for groups without rows)
     const int64_t row_tiles = (a.M + C::kTokens - 1) / C::kTokens + std::min<int64_t>(a.groups - 1, a.M);
     const int64_t tiles = row_tiles * p.n_tiles;
+    // few tiles: the stages are shared by as many CTAs of a cluster as all tiles' clusters run at once with, four stages each or more
+    int split = 1;
+    if (C::kCtas == 1 && a.groups == 1)
+        for (int size = 2; size <= kMaxSplit && p.kb_count >= 4 * size; ++size)
+            if (tiles <= resident[size]) split = size;
+    p.split = split;
     const int share = C::kCtas == 2 ? 2 : split;
-    const int64_t clusters = split > 1 ? tiles : std::min<int64_t>(tiles, C::kCtas == 2 ? resident : tc_num_sms());
+    const int64_t clusters = split > 1 ? tiles : std::min<int64_t>(tiles, resident[C::kCtas]);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * share));
     cfg.blockDim = dim3(C::kThreads);
@@ -684,16 +696,10 @@ cudaError_t launch_out(const moe_int8_matmul_args& a, const Args& p, cudaStream_
     const int sms = tc_num_sms();
     const int64_t n_tiles = (a.N + 255) / 256;
     if (a.groups == 1 ? a.M <= 16 : a.M <= 16 * a.groups && a.groups * ((a.N + 127) / 128) < sms) return launch_int8_few(a, s);
-    if (a.groups <= Large::kMaxGroups && a.M / a.groups >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, 1, s);
+    if (a.groups <= Large::kMaxGroups && a.M / a.groups >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, s);
     const int64_t row_tiles = (a.M + 127) / 128 + (a.groups > 1 ? std::min<int64_t>(a.groups, a.M) / 2 : 0);
-    if (a.M / a.groups > 16 && row_tiles * n_tiles * 4 >= sms) return launch<Pair, Out>(a, p, 1, s);
-    // few tiles: the stages are shared by a cluster's CTAs as long as all tiles run at once
-    const bool wide = a.M / a.groups > 64;
-    int split = 1;
-    const int64_t tokens = wide ? Mid::kTokens : Small::kTokens, tiles = ((a.M + tokens - 1) / tokens) * ((a.N + 127) / 128);
-    if (a.groups == 1)
-        while (split < kMaxSplit && tiles * split * 2 <= sms && p.kb_count >= split * 4) split *= 2;
-    return wide ? launch<Mid, Out>(a, p, split, s) : launch<Small, Out>(a, p, split, s);
+    if (a.M / a.groups > 16 && row_tiles * n_tiles * 4 >= sms) return launch<Pair, Out>(a, p, s);
+    return a.M / a.groups > 64 ? launch<Mid, Out>(a, p, s) : launch<Small, Out>(a, p, s);
 }
 
 }  // namespace

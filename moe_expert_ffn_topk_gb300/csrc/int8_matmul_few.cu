@@ -90,6 +90,8 @@ __global__ void __launch_bounds__(kThreads, kTokens <= 2 || kTokens == 8 ? 3 : 2
     const bool on0 = n0 + r < p.N, on1 = n0 + r + 8 < p.N;
     const int8_t* w0 = p.b + ((int64_t)g * p.N + n0 + r) * p.b_stride + at;
     const int8_t* w1 = w0 + 8 * p.b_stride;
+    // of the value that the thread writes; on its way during the product
+    const float b_scale = n0 + (int)threadIdx.x % 16 < p.N ? __ldg(p.b_scale + (int64_t)g * p.N + n0 + threadIdx.x % 16) : 0.0f;
     for (int m0 = lo; m0 < hi; m0 += kTokens) {
         int c[kTiles][4];
 #pragma unroll
@@ -179,14 +181,15 @@ __global__ void __launch_bounds__(kThreads, kTokens <= 2 || kTokens == 8 ? 3 : 2
                 for (int k = 0; k < kMaxSplit; ++k) sum += s[k];
             }
         }
+        // nobody leaves, or writes its next sums, while these are read (before the stores, which the barrier would wait for)
+        if (p.split > 1) cluster_sync();
+        else __syncthreads();
         const int m = m0 + threadIdx.x / 16, n = n0 + threadIdx.x % 16;
         if (mine && m < hi && n < p.N) {
-            const float y = int8_scaled((float)sum, __ldg(p.b_scale + (int64_t)g * p.N + n), __ldg(p.a_scale + m));
+            const float y = int8_scaled((float)sum, b_scale, __ldg(p.a_scale + m));
             if constexpr (sizeof(Out) == 2) static_cast<uint16_t*>(p.out)[(int64_t)m * p.out_stride + n] = float_to_bf16_bits(y);
             else static_cast<float*>(p.out)[(int64_t)m * p.out_stride + n] = y;
         }
-        if (p.split > 1) cluster_sync();  // nobody leaves, or writes its next sums, while these are read
-        else __syncthreads();
     }
 }
 
