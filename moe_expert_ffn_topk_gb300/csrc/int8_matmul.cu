@@ -13,8 +13,19 @@
 // bounds such a kernel is shared memory's 128 bytes a cycle (bytes in by TMA, out to the converters, f16 tokens in, and out to the
 // MMA), and weights that went back too would add half as much again.
 //
-// Warp roles: warp 0 TMA producer, warp 1 tensor-memory allocator and MMA issuer, warp 2 the groups' table, warps 4-11 take sums out and
-// write results, the others (8 or 16) convert.
+// Warp roles: warp 0 TMA producer, warp 1 tensor-memory allocator and MMA issuer, warp 2 the groups' table, warp 3 a split tile's scales,
+// warps 4-11 take sums out and write results, the others (8 or 16) convert.
+//
+// Measured, 8192 x 4096 x 7168 to bf16: 287 us (1.67 PFLOP/s; 0.86 of cuBLAS's bf16 burst rate, 0.95 of its sustained one). A stage of 128 of
+// K is 1024 cycles of MMAs on a 256 x 256 pair tile and takes some 1350: the same 1024 cycles of shared memory (32 KB each way in,
+// out, in and out) and half of the schedulers' slots contend with them; without converters and epilogue the loop takes 220 us. 4099
+// rows of 32 groups, 4096 x 2048: 89 us, 2.35 TB/s of weights; a stage is 512 cycles of MMAs on a 256 x 128 tile and takes 1080 (ALU
+// 63 % busy, tensor pipe 33 %). 133 x 2112 x 7168: 17 us, 14 stages a CTA at 980 cycles, 3 us before the first operands, 3 for the
+// cluster's sum.
+// What it took, on the first of these: 436 us with a forwarder that released the odd CTA's operands at cluster scope (850 cycles a stage);
+// 404 with converters of both CTAs arriving themselves; 310 with sums taken out in pauses of two steps and converters of both operands
+// in every warp; 305 with one commit a stage; 292 without a conversion to integers of every value of every chunk. Slower: sums read by
+// warps that sleep between their looks (315), packed bf16 stores of two rows (305), spinning tests instead of waits (298).
 //
 // Every wait is bounded (2 s); on time-out the CTA records MOE_ERR_TIMEOUT and leaves its loops.
 #include <cuda.h>
@@ -620,6 +631,7 @@ using Large = Cfg<2, 128, 2, 3, 4, 8, 160, 96>;
 using Pair = Cfg<2, 128, 1, 5, 4, 16, 104, 72>;
 using Mid = Cfg<1, 128, 1, 3, 3, 16, 104, 72>;
 using Small = Cfg<1, 64, 1, 5, 4, 16, 104, 72>;
+static_assert(Pair::kMaxGroups >= 1024 && Mid::kMaxGroups >= 1024 && Small::kMaxGroups >= 1024, "tables of as many groups as a call takes");
 
 // Attributes of the kernel on the current device; resident[s]: clusters of s CTAs that run at once there (of 2 for pairs; of each size that a
 // tile may be split over, for the others). A cluster's CTAs share a GPC, so fewer fit than the SMs would hold.
@@ -691,15 +703,23 @@ cudaError_t launch(const moe_int8_matmul_args& a, Args p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, int8_matmul_kernel<C, Out>, ma, mb, p);
 }
 
+// Tiles by sizes alone (times with N 4096, K 7168 where no other is given; `sms` 152 here)
 template <typename Out>
 cudaError_t launch_out(const moe_int8_matmul_args& a, const Args& p, cudaStream_t s) {
     const int sms = tc_num_sms();
-    const int64_t n_tiles = (a.N + 255) / 256;
-    if (a.groups == 1 ? a.M <= 16 : a.M <= 16 * a.groups && a.groups * ((a.N + 127) / 128) < sms) return launch_int8_few(a, s);
-    if (a.groups <= Large::kMaxGroups && a.M / a.groups >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, s);
+    const int64_t n_tiles = (a.N + 255) / 256, rows = a.M / a.groups;
+    // few rows: 16 rows 13.0 us there and 14.5 on Small, 32 rows 22 and 14. Of groups, where Small has a CTA for less than every SM: 64 rows of 8
+    // groups, N 512, 18 us and 30; of 32 groups, N 4096, K 2048 (1024 tiles) 48 and 41
+    if (a.groups == 1 ? a.M <= 16 : rows <= 16 && a.groups * ((a.N + 127) / 128) < sms) return launch_int8_few(a, s);
+    // 256 x 256: where 256 x 128 tiles take a second round of the pairs. 1000 rows 47 us and 59 on Pair, 512 rows, K 4096, 30 and 22; 16 groups of
+    // 256 rows, K 2048, 73 and 77, 32 of 128 rows 93 and 89
+    if (a.groups <= Large::kMaxGroups && rows >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, s);
+    // 256 x 128 on pairs: where they give half of the pairs a tile (fewer are split over K on one-CTA tiles). 384 rows 32 us and 37 on Mid, 256
+    // rows 32 and 25; 32 groups, K 2048: 64 rows each 63 and 84, 16 each 55 and 52 on Small
     const int64_t row_tiles = (a.M + 127) / 128 + (a.groups > 1 ? std::min<int64_t>(a.groups, a.M) / 2 : 0);
-    if (a.M / a.groups > 16 && row_tiles * n_tiles * 4 >= sms) return launch<Pair, Out>(a, p, s);
-    return a.M / a.groups > 64 ? launch<Mid, Out>(a, p, s) : launch<Small, Out>(a, p, s);
+    if (rows > 16 && row_tiles * n_tiles * 4 >= sms) return launch<Pair, Out>(a, p, s);
+    // 128 x 128 or 128 x 64: 100 rows 17 us and 22, 64 rows 18 and 15
+    return rows > 64 ? launch<Mid, Out>(a, p, s) : launch<Small, Out>(a, p, s);
 }
 
 }  // namespace

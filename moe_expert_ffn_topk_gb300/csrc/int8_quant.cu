@@ -4,6 +4,7 @@
 // y + r (x - y s) with fused multiply-adds is x / s rounded to nearest wherever nothing under- or overflows; s >= 1e-8 and
 // r >= 2^-122, so that only quotients far below one half do, whose code is 0 all the same), and adding 1.5 * 2^23 rounds it half to
 // even into the low bits. |x| / s is at most 127 (1 + 2^-22), so no code passes 127.
+// 8192 x 7168 bf16: 32.5 us, 0.81 of the copy rate (66 us with a division a value); issue slots 65 % busy beside it.
 #include <algorithm>
 
 #include "common.cuh"

@@ -73,9 +73,10 @@ def bits(t):
     return t.contiguous().view(torch.uint8)
 
 
-# the last sizes sort in a launch of their own (more than 2048 slots), runs of slots that end inside a group of 32
+# the last sizes sort in a launch of their own (more than 4096 slots), runs of slots that end inside a group of 32
 SIZES = [(1, 1, 1, 1), (1, 64, 4, 4), (3, 100, 5, 2), (7, 7168, 256, 8), (64, 384, 1024, 32), (65, 130, 3, 1), (341, 33, 60, 6),
-         (342, 33, 60, 6), (683, 64, 1, 3), (2049, 24, 1000, 1), (1111, 520, 64, 7), (4096, 16, 256, 8), (9000, 8, 7, 3)]
+         (342, 33, 60, 6), (683, 64, 1, 3), (2049, 24, 1000, 1), (1111, 520, 64, 7), (4096, 16, 256, 8), (9000, 8, 7, 3), (4096, 40, 5, 1),
+         (4097, 40, 5, 1), (5001, 24, 1000, 1), (1366, 33, 1024, 3)]
 
 
 @pytest.mark.parametrize("masked", [0.0, 0.3])
@@ -166,7 +167,8 @@ def slots(g, T, K, masked):
     return torch.where(torch.rand((T, K), generator=g, device="cuda") < masked, torch.full_like(row, -1), row).contiguous()
 
 
-BACK = [(1, 1, 1), (1, 8, 1), (2, 7168, 8), (5, 129, 6), (33, 1000, 32), (300, 40, 9), (1500, 264, 4), (800, 2051, 8)]
+BACK = [(1, 1, 1), (1, 8, 1), (2, 7168, 8), (5, 129, 6), (33, 1000, 32), (300, 40, 9), (1500, 264, 4), (800, 2051, 8), (60, 2048, 2),
+        (400, 4096, 7)]
 
 
 @pytest.mark.parametrize("weighted", [True, False])
