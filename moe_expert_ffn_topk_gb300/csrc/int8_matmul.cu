@@ -97,6 +97,9 @@ struct Cfg {
     static_assert(kTmemA + kOps * (kStageK / 2) <= kTmemCols, "tensor memory");
     static_assert(kCols % 16 == 0 && kCols <= 128 && kMine >= 1 && kMine <= 4 && kBRows == 32 * kMine, "tile");
     static_assert(kOps >= 2 * kStep, "two steps of operands");
+    // A slot of bytes is waited for by the same groups in every round: bytes may land out of order, and a group that waits for the round after one
+    // it has not seen land would pass for the wrong parity. (Slots of operands are freed in order, so their waits may change hands.)
+    static_assert(kRaw % (kGroups / 2) == 0 && kOps >= kGroups / 2, "rounds of the slots");
     static_assert(kCtas == 2 || kBarOff >= 4 * 128 * kTokens, "split sums use the stages' memory");
 };
 
@@ -628,9 +631,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 // ---------------------------------------------------------------------------------------
 
 using Large = Cfg<2, 128, 2, 3, 4, 8, 160, 96>;
-using Pair = Cfg<2, 128, 1, 5, 4, 16, 104, 72>;
-using Mid = Cfg<1, 128, 1, 3, 3, 16, 104, 72>;
-using Small = Cfg<1, 64, 1, 5, 4, 16, 104, 72>;
+using Pair = Cfg<2, 128, 1, 6, 4, 16, 104, 72>;
+using Mid = Cfg<1, 128, 1, 3, 3, 8, 160, 96>;
+using Small = Cfg<1, 64, 1, 6, 4, 16, 104, 72>;
 static_assert(Pair::kMaxGroups >= 1024 && Mid::kMaxGroups >= 1024 && Small::kMaxGroups >= 1024, "tables of as many groups as a call takes");
 
 // Attributes of the kernel on the current device; resident[s]: clusters of s CTAs that run at once there (of 2 for pairs; of each size that a
