@@ -713,7 +713,8 @@ cudaError_t launch_out(const moe_int8_matmul_args& a, const Args& p, cudaStream_
     const int64_t n_tiles = (a.N + 255) / 256, rows = a.M / a.groups;
     // few rows: 16 rows 13.0 us there and 14.5 on Small, 32 rows 22 and 14. Of groups, where Small has a CTA for less than every SM: 64 rows of 8
     // groups, N 512, 18 us and 30; of 32 groups, N 4096, K 2048 (1024 tiles) 48 and 41
-    if (a.groups == 1 ? a.M <= 16 : rows <= 16 && a.groups * ((a.N + 127) / 128) < sms) return launch_int8_few(a, s);
+    // (256 rows at most, for all of them may be one group's, which takes 16 at a time)
+    if (a.groups == 1 ? a.M <= 16 : rows <= 16 && a.M <= 256 && a.groups * ((a.N + 127) / 128) < sms) return launch_int8_few(a, s);
     // 256 x 256: where 256 x 128 tiles take a second round of the pairs. 1000 rows 47 us and 59 on Pair, 512 rows, K 4096, 30 and 22; 16 groups of
     // 256 rows, K 2048, 73 and 77, 32 of 128 rows 93 and 89
     if (a.groups <= Large::kMaxGroups && rows >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, s);

@@ -4,12 +4,12 @@
 // Sort. The row of a slot is (slots of lower experts) + (earlier slots of its expert), which fixes the order without atomics
 // whose order could change it: counts may be added up in any order, ranks are taken in the order of the slots.
 //   - up to kFewSlots slots: one launch in which every CTA has a token, counts all ids for itself (shared memory) and copies its row.
-//   - more: one cluster of eight CTAs, a run of slots a warp. Each warp counts its run, the CTAs exchange their totals through
-//     distributed shared memory, and each warp walks its run again and ranks 32 slots at a time with match.any. A second launch copies.
-// (H 4096, K 8, bf16: 128 tokens 3.9 us in one launch and 9.4 in two, 256 tokens 8.2 and 10.7, 512 tokens 14.4 and 14.3, 1024 tokens 32 and 21.)
+//   - more: the slots in up to 128 runs, a CTA each. One launch counts the runs' experts; in a second every CTA adds up the runs before its own,
+//     counts its warps' parts and ranks 32 slots at a time with match.any; a third copies.
+// (H 4096, K 8, bf16: 128 tokens 3.9 us in one launch and 9.4 in two, 256 tokens 8.2 and 10.7, 512 tokens 14.4 and 14.5, 1024 tokens 32 and 22.)
 //
-// Bound by HBM's writes: a token is read once and written K times. 8192 x 8 x 7168 bf16 (1.06 GB): 175 us, 6.05 TB/s, 0.90 of the copy
-// rate, where a fill alone runs at 4.0 TB/s. 7 x 8 x 7168 codes: 4.5 us on the device, the chain of ids, counts and copies.
+// Bound by HBM's writes: a token is read once and written K times. 8192 x 8 x 7168 bf16 (1.06 GB): 169 us, 6.26 TB/s, 0.93 of the copy
+// rate, where a fill alone runs at 4.0 TB/s; 9 us of them sort (a cluster of eight CTAs that exchanged its totals took 16). 7 x 8 x 7168 codes: 4.5 us on the device, the chain of ids, counts and copies.
 #include <algorithm>
 
 #include "common.cuh"
@@ -24,14 +24,19 @@ using namespace tc;
 
 constexpr int kFewSlots = 4096;
 constexpr int kFewThreads = 256;
-constexpr int kSortCtas = 8, kSortWarps = 32, kSortThreads = 32 * kSortWarps;
+constexpr int kSortWarps = 32, kSortThreads = 32 * kSortWarps;
+// Runs of slots that are sorted by a CTA each, and slots of one: every CTA reads all runs' counts (65536 slots of 256 experts, rows of 16 bytes: 128
+// runs of 512 16.9 us, 64 of 1024 14.3, 16 of 4096 16.0; 4.2 million slots 237 us with 128 runs, 287 with 64).
+constexpr int kMaxRuns = 128, kMinRun = 1024;
 constexpr int kCopyWarps = 8;
 constexpr int kCopyVecs = 4;  // vectors of a lane on their way at a time
 
 struct SortArgs {
     const int32_t* ids;
     int32_t *offsets, *row_src, *slot_row, *hdr;
+    int32_t* counts;  // [run][expert]
     int n, E, K;
+    int run, runs;    // slots of a run (whole groups of 32), and their number
 };
 
 struct CopyArgs {
@@ -149,42 +154,54 @@ __global__ void __launch_bounds__(kFewThreads) permute_few_kernel(SortArgs p, Co
     if (c.scale && warp == 0) copy_scales(c, t, row, lane);
 }
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(SortArgs p) {
-    extern __shared__ int hist[];  // [warp][expert]: the warp's slots of the expert, then where the next of them goes
-    __shared__ int total[kRowExperts], warp_sum[kSortWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    // runs of whole groups of 32 slots
-    const int run = ((p.n + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
-    const int s0 = min((int64_t)p.n, (int64_t)((int)rank * kSortWarps + warp) * run), s1 = min((int64_t)p.n, (int64_t)s0 + run);
-    int* mine = hist + warp * p.E;
-    for (int i = threadIdx.x; i < kSortWarps * p.E; i += kSortThreads) hist[i] = 0;
+__global__ void __launch_bounds__(kSortThreads) count_kernel(SortArgs p) {
+    __shared__ int count[kRowExperts];
+    if (threadIdx.x < p.E) count[threadIdx.x] = 0;
     __syncthreads();
+    const int64_t s1 = min((int64_t)p.n, (int64_t)(blockIdx.x + 1) * p.run);
 #pragma unroll 4
-    for (int s = s0 + lane; s < s1; s += 32) {
-        const int e = slot_expert(p, s);
-        if (e >= 0) atomicAdd(mine + e, 1);
+    for (int64_t s = (int64_t)blockIdx.x * p.run + threadIdx.x; s < s1; s += kSortThreads) {
+        const int e = slot_expert(p, (int)s);
+        if (e >= 0) atomicAdd(count + e, 1);
     }
     __syncthreads();
-    const int e = threadIdx.x;
-    int sum = 0;
-    if (e < p.E)
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int v = hist[w * p.E + e];
-            hist[w * p.E + e] = sum;
+    if (threadIdx.x < p.E) p.counts[(int64_t)blockIdx.x * p.E + threadIdx.x] = count[threadIdx.x];
+}
+
+__global__ void __launch_bounds__(kSortThreads) place_kernel(SortArgs p) {
+    extern __shared__ int hist[];  // [warp][expert]: the warp's slots of the expert, then where the next of them goes
+    __shared__ int all[kRowExperts], lower[kRowExperts];  // slots of the expert, and those of the runs before
+    __shared__ int warp_sum[kSortWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
+    if (e < p.E) all[e] = lower[e] = 0;
+    for (int i = threadIdx.x; i < kSortWarps * p.E; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    // the threads share the runs where there are fewer experts than threads
+    const int parts = kSortThreads / p.E, part = threadIdx.x / p.E, at = threadIdx.x - part * p.E;
+    if (part < parts) {
+        int sum = 0, before = 0;
+#pragma unroll 16
+        for (int r = part; r < p.runs; r += parts) {
+            const int v = __ldg(p.counts + (int64_t)r * p.E + at);
             sum += v;
+            if (r < (int)blockIdx.x) before += v;
         }
-    total[e] = sum;
-    cluster_sync();
-    int all = 0, lower = 0;
-    if (e < p.E)
-        for (int c = 0; c < kSortCtas; ++c) {
-            int v;
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(total + e), (uint32_t)c)) : "memory");
-            all += v;
-            if (c < (int)rank) lower += v;
-        }
-    int scan = all;
+        if (sum) atomicAdd(all + at, sum);
+        if (before) atomicAdd(lower + at, before);
+    }
+    // parts of a run: whole groups of 32 slots
+    const int per = (p.run / 32 + kSortWarps - 1) / kSortWarps * 32;
+    const int64_t end = min((int64_t)p.n, (int64_t)(blockIdx.x + 1) * p.run);
+    const int64_t s0 = min(end, (int64_t)blockIdx.x * p.run + warp * per), s1 = min(end, s0 + per);
+    int* mine = hist + warp * p.E;
+#pragma unroll 4
+    for (int64_t s = s0 + lane; s < s1; s += 32) {
+        const int id = slot_expert(p, (int)s);
+        if (id >= 0) atomicAdd(mine + id, 1);
+    }
+    __syncthreads();
+    const int own = e < p.E ? all[e] : 0;
+    int scan = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, scan, o);
@@ -193,31 +210,39 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     if (lane == 31) warp_sum[warp] = scan;
     __syncthreads();
     int ahead = 0, routed = 0;
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
         const int v = warp_sum[w];
         if (w < warp) ahead += v;
         routed += v;
     }
-    const int first = ahead + scan - all;
-    if (rank == 0) {
+    const int first = ahead + scan - own;
+    if (blockIdx.x == 0) {
         if (e < p.E) p.offsets[e] = first;
         if (e == 0) p.offsets[p.E] = routed;
     }
-    if (e < p.E)
-        for (int w = 0; w < kSortWarps; ++w) hist[w * p.E + e] += first + lower;
-    cluster_sync();  // nobody leaves while its totals are read; the rows are in place
-    for (int s = s0 + lane; s - lane < s1; s += 32) {
-        const int id = s < s1 ? slot_expert(p, s) : -1;
+    if (e < p.E) {
+        int next = first + lower[e];
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int v = hist[w * p.E + e];
+            hist[w * p.E + e] = next;
+            next += v;
+        }
+    }
+    __syncthreads();
+    for (int64_t s = s0 + lane; s - lane < s1; s += 32) {
+        const int id = s < s1 ? slot_expert(p, (int)s) : -1;
         const uint32_t same = __match_any_sync(0xffffffffu, id);
-        const int at = __popc(same & ((1u << lane) - 1));
-        const int row = id >= 0 ? mine[id] + at : -1;
+        const int rank = __popc(same & ((1u << lane) - 1));
+        const int row = id >= 0 ? mine[id] + rank : -1;
         __syncwarp();
-        if (id >= 0 && at == 0) mine[id] += __popc(same);
+        if (id >= 0 && rank == 0) mine[id] += __popc(same);
         __syncwarp();
         if (s < s1) p.slot_row[s] = row;
-        if (row >= 0) p.row_src[row] = s;
+        if (row >= 0) p.row_src[row] = (int)s;
     }
-    for (int r = routed + (int)rank * kSortThreads + threadIdx.x; r < p.n; r += kSortCtas * kSortThreads) p.row_src[r] = -1;
+    for (int64_t r = routed + (int64_t)blockIdx.x * kSortThreads + threadIdx.x; r < p.n; r += (int64_t)gridDim.x * kSortThreads) p.row_src[r] = -1;
 }
 
 template <int V>
@@ -238,13 +263,14 @@ cudaError_t launch_v(const SortArgs& p, CopyArgs c, cudaStream_t s) {
         permute_few_kernel<V><<<c.T + 1, kFewThreads, 0, s>>>(p, c);
         return cudaGetLastError();
     }
-    static_assert(sizeof(int) * kSortWarps * kRowExperts + 8192 <= 232448, "shared memory");
+    static_assert(sizeof(int) * kSortWarps * kRowExperts + 16384 <= 232448, "shared memory");
     int device = 0;
     const cudaError_t e = once_per_device(&device, [](int) {
-        return cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(int) * kSortWarps * kRowExperts);
+        return cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(int) * kSortWarps * kRowExperts);
     });
     if (e != cudaSuccess) return e;
-    sort_kernel<<<kSortCtas, kSortThreads, sizeof(int) * kSortWarps * p.E, s>>>(p);
+    count_kernel<<<p.runs, kSortThreads, 0, s>>>(p);
+    place_kernel<<<p.runs, kSortThreads, sizeof(int) * kSortWarps * p.E, s>>>(p);
     const int64_t per_row = (c.bytes / V + 32 * kCopyVecs - 1) / (32 * kCopyVecs);
     c.segments = (int)per_row;
     const int64_t ctas = (c.T * per_row + kCopyWarps - 1) / kCopyWarps;
@@ -254,9 +280,19 @@ cudaError_t launch_v(const SortArgs& p, CopyArgs c, cudaStream_t s) {
 
 }  // namespace
 
+size_t permute_workspace(int64_t slots, int E) {
+    return sizeof(int32_t) * (kOpsHeaderInts + (slots > kFewSlots ? (size_t)kMaxRuns * E : 0));
+}
+
 cudaError_t launch_permute(const moe_permute_args& a, int T, int K, int E, int32_t* hdr, cudaStream_t s) {
     const int size = a.type == MOE_TYPE_F32 ? 4 : a.type == MOE_TYPE_BF16 ? 2 : 1;
-    SortArgs p = {a.topk_ids, a.offsets, a.row_src, a.slot_row, hdr, T * K, E, K};
+    SortArgs p = {};
+    p.ids = a.topk_ids;
+    p.offsets = a.offsets, p.row_src = a.row_src, p.slot_row = a.slot_row;
+    p.hdr = hdr, p.counts = hdr + kOpsHeaderInts;
+    p.n = T * K, p.E = E, p.K = K;
+    p.run = std::max(kMinRun, (p.n + kMaxRuns - 1) / kMaxRuns + 31) / 32 * 32;
+    p.runs = (p.n + p.run - 1) / p.run;
     CopyArgs c = {};
     c.x = static_cast<const uint8_t*>(a.x);
     c.rows = static_cast<uint8_t*>(a.rows);

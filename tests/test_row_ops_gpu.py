@@ -354,6 +354,24 @@ def test_row_ops_on_other_streams_and_in_a_graph(moe):
         assert all(torch.equal(a, b) for a, b in zip(want, captured))
 
 
+def test_permute_of_many_slots(moe):
+    """More slots than the runs' shortest lengths make up (128 of 1024), a last run that is cut, experts of very different popularity."""
+    g = gen(10)
+    T, H, E, K = 30011, 4, 200, 7
+    ids = (torch.rand((T, K), generator=g, device="cuda") ** 3 * E).to(torch.int32)
+    ids[torch.rand((T, K), generator=g, device="cuda") < 0.05] = -1
+    x = values(g, T, H, torch.float32)
+    rows, out, _, status = permute(moe, x, ids, E)
+    flat = ids.flatten().cpu()
+    order = torch.sort(torch.where(flat < 0, E, flat), stable=True).indices
+    R = int((flat >= 0).sum())
+    assert status == moe.MOE_OK and out["offsets"][-1] == R and torch.equal(out["row_src"][:R].cpu().long(), order[:R])
+    assert torch.equal(out["offsets"].cpu().long().diff(), torch.bincount(flat[flat >= 0].long(), minlength=E))
+    want = torch.full((T * K,), -1, dtype=torch.int64)
+    want[order[:R]] = torch.arange(R)
+    assert torch.equal(out["slot_row"].flatten().cpu().long(), want) and torch.equal(rows[:R], x[(order[:R] // K).cuda()])
+
+
 def test_permute_offsets_past_32_bits(moe):
     """Rows whose byte offsets pass 2^32 (and element offsets 2^31)."""
     T, H, K = 70000, 4096, 8  # 560000 rows of 4096 bytes in each of codes: 2.3 GB; of bf16: 4.6 GB
