@@ -46,8 +46,7 @@ struct GroupTile {
     int g, n_tile, row0, hi;  // column tile n_tile of group g; rows [row0, hi)
 };
 
-// Tile t of (row tiles) x (n_tiles column tiles): group by group, column tile by column tile, row tile by row tile. (32-bit numbers where
-// they suffice: a 64-bit division takes a few hundred cycles, and every role looks for every tile of its CTA.)
+// Tile t of (row tiles) x (n_tiles column tiles): group by group, column tile by column tile, row tile by row tile. Int holds every tile's number.
 template <typename Int>
 __device__ __forceinline__ GroupTile find_group_tile_as(Int t, const int* tab, int groups, int n_tiles, int tile_rows) {
     const int *off = tab, *lo = tab + groups + 1, *hi = lo + groups;
@@ -66,6 +65,8 @@ __device__ __forceinline__ GroupTile find_group_tile_as(Int t, const int* tab, i
     return tl;
 }
 
+// In 32 bits where they suffice: a 64-bit division takes a few hundred cycles, which counts where every role looks for every tile of its CTA
+// (where a CTA has one tile the second way's instructions cost more than they save: the few-row FP8 product 10.4 and 10.6 us).
 __device__ __forceinline__ GroupTile find_group_tile(int64_t t, const int* tab, int groups, int n_tiles, int tile_rows) {
     if ((int64_t)tab[groups] * n_tiles < (int64_t(1) << 31)) return find_group_tile_as<uint32_t>((uint32_t)t, tab, groups, n_tiles, tile_rows);
     return find_group_tile_as<uint64_t>((uint64_t)t, tab, groups, n_tiles, tile_rows);
