@@ -88,7 +88,7 @@ struct Tile {
 
 template <class C>
 __device__ __forceinline__ Tile decode(int64_t t, const int* tab, int groups, int n_tiles) {
-    const GroupTile f = find_group_tile_as<int64_t>(t, tab, groups, n_tiles, C::kTileRows);
+    const GroupTile f = find_group_tile(t, tab, groups, n_tiles, C::kTileRows);
     return {f.g, f.n_tile * C::kBN, f.row0, f.hi};
 }
 

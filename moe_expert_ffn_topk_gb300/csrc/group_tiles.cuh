@@ -46,30 +46,23 @@ struct GroupTile {
     int g, n_tile, row0, hi;  // column tile n_tile of group g; rows [row0, hi)
 };
 
-// Tile t of (row tiles) x (n_tiles column tiles): group by group, column tile by column tile, row tile by row tile. Int holds every tile's number.
-template <typename Int>
-__device__ __forceinline__ GroupTile find_group_tile_as(Int t, const int* tab, int groups, int n_tiles, int tile_rows) {
+// Tile t of (row tiles) x (n_tiles column tiles): group by group, column tile by column tile, row tile by row tile. (A division in 32 bits
+// where the numbers fit gained nothing on either product.)
+__device__ __forceinline__ GroupTile find_group_tile(int64_t t, const int* tab, int groups, int n_tiles, int tile_rows) {
     const int *off = tab, *lo = tab + groups + 1, *hi = lo + groups;
     int a = 0, b = groups - 1;
     while (a < b) {
         const int mid = (a + b + 1) >> 1;
-        if ((Int)off[mid] * (Int)n_tiles <= t) a = mid; else b = mid - 1;
+        if ((int64_t)off[mid] * n_tiles <= t) a = mid; else b = mid - 1;
     }
-    const Int mt = (Int)(off[a + 1] - off[a]);
-    const Int local = t - (Int)off[a] * (Int)n_tiles, column = local / mt;
+    const int mt = off[a + 1] - off[a];
+    const int64_t local = t - (int64_t)off[a] * n_tiles;
     GroupTile tl;
     tl.g = a;
-    tl.n_tile = (int)column;
-    tl.row0 = lo[a] + (int)(local - column * mt) * tile_rows;
+    tl.n_tile = (int)(local / mt);
+    tl.row0 = lo[a] + (int)(local % mt) * tile_rows;
     tl.hi = hi[a];
     return tl;
-}
-
-// In 32 bits where they suffice: a 64-bit division takes a few hundred cycles, which counts where every role looks for every tile of its CTA
-// (where a CTA has one tile the second way's instructions cost more than they save: the few-row FP8 product 10.4 and 10.6 us).
-__device__ __forceinline__ GroupTile find_group_tile(int64_t t, const int* tab, int groups, int n_tiles, int tile_rows) {
-    if ((int64_t)tab[groups] * n_tiles < (int64_t(1) << 31)) return find_group_tile_as<uint32_t>((uint32_t)t, tab, groups, n_tiles, tile_rows);
-    return find_group_tile_as<uint64_t>((uint64_t)t, tab, groups, n_tiles, tile_rows);
 }
 
 }  // namespace moe
