@@ -9,6 +9,7 @@ library has not been built, importing this module raises ``ImportError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -538,18 +539,21 @@ _COPIED_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32, tor
                  torch.uint8: MOE_TYPE_CODES8, torch.float8_e4m3fn: MOE_TYPE_CODES8, torch.float8_e5m2: MOE_TYPE_CODES8}
 
 
+_I32, _F32 = torch.int32, torch.float32
+
+
 def _there(t, what, dtype, shape, device):
     """Address of a contiguous tensor of that type and shape on that device (each tensor is looked at once: a small call's time is
     the host's)."""
+    if t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.get_device() != device:
         raise ValueError(f"{what} must be on device {device}, with the other tensors, not on {t.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be contiguous")
 
 
 def _rows_there(t, what, rows, cols, device):
@@ -568,6 +572,11 @@ def _space_there(workspace, device):
     if workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous memory of device {device}")
     return workspace.data_ptr(), workspace.nbytes
+
+
+@functools.lru_cache(maxsize=1024)
+def _row_dims(tokens, topk):
+    return MoeDims(tokens, 0, 0, 0, topk, 0)
 
 
 def moe_permute(x, topk_ids, d: MoeDims, rows, offsets, row_src, slot_row, workspace, scale=None, row_scale=None, stream=None):
@@ -589,13 +598,12 @@ def moe_permute(x, topk_ids, d: MoeDims, rows, offsets, row_src, slot_row, works
     scales, from_scale, to_scale = 0, None, None
     if scale is not None:
         scales = scale.shape[-1]
-        from_scale = _there(scale, "scale", torch.float32, (T, scales), device)
-        to_scale = _there(row_scale, "row_scale", torch.float32, (T * K, scales), device)
+        from_scale = _there(scale, "scale", _F32, (T, scales), device)
+        to_scale = _there(row_scale, "row_scale", _F32, (T * K, scales), device)
     ws, nbytes = _space_there(workspace, device)
-    i32 = torch.int32
-    args = MoePermuteArgs(x.data_ptr(), from_scale, _there(topk_ids, "topk_ids", i32, (T, K), device), rows.data_ptr(), to_scale,
-                          _there(offsets, "offsets", i32, (E + 1,), device), _there(row_src, "row_src", i32, (T * K,), device),
-                          _there(slot_row, "slot_row", i32, (T, K), device), H, _rows_there(x, "x", T, H, device),
+    args = MoePermuteArgs(x.data_ptr(), from_scale, _there(topk_ids, "topk_ids", _I32, (T, K), device), rows.data_ptr(), to_scale,
+                          _there(offsets, "offsets", _I32, (E + 1,), device), _there(row_src, "row_src", _I32, (T * K,), device),
+                          _there(slot_row, "slot_row", _I32, (T, K), device), H, _rows_there(x, "x", T, H, device),
                           _rows_there(rows, "rows", T * K, H, device), kind, scales)
     status = LIB.moe_permute(args, d, ws, nbytes, handle)
     if status:
@@ -608,9 +616,9 @@ def moe_unpermute(rows, slot_row, y, weights=None, stream=None):
     T, K = slot_row.shape
     H, device = y.shape[-1], rows.get_device()
     status = LIB.moe_unpermute(rows.data_ptr(), _float_type(rows, "rows"), _rows_there(rows, "rows", T * K, H, device),
-                               _there(slot_row, "slot_row", torch.int32, (T, K), device),
-                               None if weights is None else _there(weights, "weights", torch.float32, (T, K), device),
-                               MoeDims(T, 0, 0, 0, K), H, y.data_ptr(), _float_type(y, "y"), _rows_there(y, "y", T, H, device),
+                               _there(slot_row, "slot_row", _I32, (T, K), device),
+                               None if weights is None else _there(weights, "weights", _F32, (T, K), device),
+                               _row_dims(T, K), H, y.data_ptr(), _float_type(y, "y"), _rows_there(y, "y", T, H, device),
                                _handle(stream, rows))
     if status:
         raise MoeError(status, "moe_unpermute")
@@ -628,11 +636,11 @@ def moe_unpermute_backward(dy, slot_row, d_rows, weights=None, rows=None, d_weig
         if rows.dtype is not d_rows.dtype:
             raise TypeError(f"d_rows must be {rows.dtype}, as rows is")
         values, stride = rows.data_ptr(), _rows_there(rows, "rows", T * K, H, device)
-        gradient = _there(d_weights, "d_weights", torch.float32, (T, K), device)
+        gradient = _there(d_weights, "d_weights", _F32, (T, K), device)
     status = LIB.moe_unpermute_backward(dy.data_ptr(), _float_type(dy, "dy"), _rows_there(dy, "dy", T, H, device), values,
-                                        _float_type(d_rows, "d_rows"), stride, _there(slot_row, "slot_row", torch.int32, (T, K), device),
-                                        None if weights is None else _there(weights, "weights", torch.float32, (T, K), device),
-                                        MoeDims(T, 0, 0, 0, K), H, d_rows.data_ptr(), _rows_there(d_rows, "d_rows", T * K, H, device),
+                                        _float_type(d_rows, "d_rows"), stride, _there(slot_row, "slot_row", _I32, (T, K), device),
+                                        None if weights is None else _there(weights, "weights", _F32, (T, K), device),
+                                        _row_dims(T, K), H, d_rows.data_ptr(), _rows_there(d_rows, "d_rows", T * K, H, device),
                                         gradient, _handle(stream, dy))
     if status:
         raise MoeError(status, "moe_unpermute_backward")
@@ -645,7 +653,7 @@ def moe_int8_quantize(x, q, scale, stream=None):
     if q.dtype is not torch.int8:
         raise TypeError("q must be int8")
     status = LIB.moe_int8_quantize(x.data_ptr(), _float_type(x, "x"), M, K, _rows_there(x, "x", M, K, device), q.data_ptr(),
-                                   _rows_there(q, "q", M, K, device), _there(scale, "scale", torch.float32, (M,), device),
+                                   _rows_there(q, "q", M, K, device), _there(scale, "scale", _F32, (M,), device),
                                    _handle(stream, x))
     if status:
         raise MoeError(status, "moe_int8_quantize")
@@ -675,9 +683,9 @@ def moe_int8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream
     if G * N == 1:
         b_stride = K
     ws, nbytes = _space_there(workspace, device)
-    args = MoeInt8MatmulArgs(a.data_ptr(), _there(a_scale, "a_scale", torch.float32, (M,), device), b.data_ptr(),
-                             _there(b_scale, "b_scale", torch.float32, (N,) if b_scale.dim() == 1 and G == 1 else (G, N), device),
-                             None if offsets is None else _there(offsets, "offsets", torch.int32, (G + 1,), device), out.data_ptr(), M,
+    args = MoeInt8MatmulArgs(a.data_ptr(), _there(a_scale, "a_scale", _F32, (M,), device), b.data_ptr(),
+                             _there(b_scale, "b_scale", _F32, (N,) if b_scale.dim() == 1 and G == 1 else (G, N), device),
+                             None if offsets is None else _there(offsets, "offsets", _I32, (G + 1,), device), out.data_ptr(), M,
                              N, K, _rows_there(a, "a", M, K, device), b_stride, _rows_there(out, "out", M, N, device), G,
                              _float_type(out, "out"))
     status = LIB.moe_int8_matmul(args, ws, nbytes, _handle(stream, a))
