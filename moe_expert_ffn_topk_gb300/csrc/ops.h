@@ -61,7 +61,7 @@ cudaError_t launch_fp8_matmul(const moe_fp8_matmul_args& a, void* workspace, cud
 // Slots (tokens x K) of a routing call, its experts and the experts of one token.
 constexpr int64_t kMaxSlots = int64_t(1) << 24;
 constexpr int kRowExperts = 1024, kRowTopk = 32;
-size_t permute_workspace(int64_t slots, int E);
+size_t permute_workspace(int64_t T, int K, int E);
 cudaError_t launch_permute(const moe_permute_args& a, int T, int K, int E, int32_t* hdr, cudaStream_t s);
 
 struct UnpermuteArgs {

@@ -107,7 +107,7 @@ moe_status moe_fp8_matmul(const moe_fp8_matmul_args* a, void* workspace, size_t 
 
 size_t moe_permute_workspace_bytes(const moe_dims* d) {
     if (!row_dims_ok(d) || d->num_experts < 1 || d->num_experts > kRowExperts) return 0;
-    return permute_workspace((int64_t)d->num_tokens * d->topk, d->num_experts);
+    return permute_workspace(d->num_tokens, d->topk, d->num_experts);
 }
 
 moe_status moe_permute(const moe_permute_args* a, const moe_dims* d, void* workspace, size_t workspace_bytes,

@@ -3,13 +3,13 @@
 //
 // Sort. The row of a slot is (slots of lower experts) + (earlier slots of its expert), which fixes the order without atomics
 // whose order could change it: counts may be added up in any order, ranks are taken in the order of the slots.
-//   - up to kFewSlots slots: one launch in which every CTA has a token, counts all ids for itself (shared memory) and copies its row.
+//   - few slots: one launch in which every CTA has a token, counts all ids for itself (shared memory) and copies its row.
 //   - more: the slots in up to 128 runs, a CTA each. One launch counts the runs' experts; in a second every CTA adds up the runs before its own,
 //     counts its warps' parts and ranks 32 slots at a time with match.any; a third copies.
-// (H 4096, K 8, bf16: 128 tokens 3.9 us in one launch and 9.4 in two, 256 tokens 8.2 and 10.7, 512 tokens 14.4 and 14.5, 1024 tokens 32 and 22.)
 //
 // Bound by HBM's writes: a token is read once and written K times. 8192 x 8 x 7168 bf16 (1.06 GB): 169 us, 6.26 TB/s, 0.93 of the copy
-// rate, where a fill alone runs at 4.0 TB/s; 9 us of them sort (a cluster of eight CTAs that exchanged its totals took 16). 7 x 8 x 7168 codes: 4.5 us on the device, the chain of ids, counts and copies.
+// rate, where a fill alone runs at 4.0 TB/s; 9 us of them sort (a cluster of eight CTAs that exchanged its totals took 16).
+// 7 x 8 x 7168 codes: 4.5 us on the device, the chain of ids, counts and copies.
 #include <algorithm>
 
 #include "common.cuh"
@@ -22,7 +22,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kFewSlots = 4096;
+// Slots up to which one launch does it all, and tokens x slots, the ids that its CTAs count together. bf16, one launch and three, H 1024 / 7168:
+// 512 x 8 6.7 / 14.1 and 10.8 / 16.4 us, 1024 x 4 8.6 / 16.2 and 9.5 / 16.2, 512 x 16 11.2 / 35.1 and 12.6 / 27.4; 2048 x 1 7.7 / 10.9 and 9.0 /
+// 12.7, 2896 x 1 12.5 / 17.4 and 9.4 / 15.3, 4096 x 1 19.2 / 27.3 and 10.3 / 23.9, 2048 x 2 11.0 / 18.2 and 9.6 / 17.3.
+constexpr int64_t kFewSlots = 4096, kFewIds = int64_t(1) << 22;
+inline bool few_slots(int64_t T, int64_t K) { return T * K <= kFewSlots && T * T * K <= kFewIds; }
+
 constexpr int kFewThreads = 256;
 constexpr int kSortWarps = 32, kSortThreads = 32 * kSortWarps;
 // Runs of slots that are sorted by a CTA each, and slots of one: every CTA reads all runs' counts (65536 slots of 256 experts, rows of 16 bytes: 128
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps) copy_kernel(CopyArgs c) {
 
 template <int V>
 cudaError_t launch_v(const SortArgs& p, CopyArgs c, cudaStream_t s) {
-    if (p.n <= kFewSlots) {
+    if (few_slots(c.T, c.K)) {
         permute_few_kernel<V><<<c.T + 1, kFewThreads, 0, s>>>(p, c);
         return cudaGetLastError();
     }
@@ -280,8 +285,8 @@ cudaError_t launch_v(const SortArgs& p, CopyArgs c, cudaStream_t s) {
 
 }  // namespace
 
-size_t permute_workspace(int64_t slots, int E) {
-    return sizeof(int32_t) * (kOpsHeaderInts + (slots > kFewSlots ? (size_t)kMaxRuns * E : 0));
+size_t permute_workspace(int64_t T, int K, int E) {
+    return sizeof(int32_t) * (kOpsHeaderInts + (few_slots(T, K) ? 0 : (size_t)kMaxRuns * E));
 }
 
 cudaError_t launch_permute(const moe_permute_args& a, int T, int K, int E, int32_t* hdr, cudaStream_t s) {

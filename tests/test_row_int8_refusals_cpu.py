@@ -41,6 +41,9 @@ def test_permute_workspace(moe):
     d = moe.dims(4, 0, 0, 8, 2)
     assert moe.moe_permute_workspace_bytes(d) == 256
     assert permute(moe, ws=None) == WORKSPACE and permute(moe, ws=P + 16) == WORKSPACE and permute(moe, nbytes=255) == WORKSPACE
+    for K in (1, 2, 7, 8, 32):  # enough for fewer tokens, too
+        need = [moe.moe_permute_workspace_bytes(moe.dims(T, 0, 0, 64, K)) for T in range(1, 4200)]
+        assert need == sorted(need) and need[-1] == 256 + 4 * 128 * 64
     for bad in ((4, 0, 0, 0, 2), (4, 0, 0, 8, 33), (-1, 0, 0, 8, 2), (1 << 23, 0, 0, 8, 4)):
         assert moe.moe_permute_workspace_bytes(moe.dims(*bad)) == 0
     with pytest.raises(ValueError):

@@ -73,10 +73,11 @@ def bits(t):
     return t.contiguous().view(torch.uint8)
 
 
-# the last sizes sort in a launch of their own (more than 4096 slots), runs of slots that end inside a group of 32
+# the last sizes sort in launches of their own (more than 4096 slots, or many tokens of a slot each), runs of slots that end inside a group of 32
 SIZES = [(1, 1, 1, 1), (1, 64, 4, 4), (3, 100, 5, 2), (7, 7168, 256, 8), (64, 384, 1024, 32), (65, 130, 3, 1), (341, 33, 60, 6),
          (342, 33, 60, 6), (683, 64, 1, 3), (2049, 24, 1000, 1), (1111, 520, 64, 7), (4096, 16, 256, 8), (9000, 8, 7, 3), (4096, 40, 5, 1),
-         (4097, 40, 5, 1), (5001, 24, 1000, 1), (1366, 33, 1024, 3)]
+         (4097, 40, 5, 1), (5001, 24, 1000, 1), (1366, 33, 1024, 3),
+         (512, 72, 256, 8), (2048, 16, 64, 1), (2049, 16, 64, 1), (4096, 16, 1, 1), (1449, 8, 6, 2)]
 
 
 @pytest.mark.parametrize("masked", [0.0, 0.3])
