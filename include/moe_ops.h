@@ -190,9 +190,9 @@ MOE_API moe_status moe_layer(const moe_layer_args* args, const moe_dims* d, void
  *   offsets    device int32 [E+1]: expert e's rows are [offsets[e], offsets[e+1]) (what the grouped products take)
  *   row_src    device int32 [T*K]: the slot of row p, -1 for p >= R
  *   slot_row   device int32 [T*K]: the row of each slot, -1 without one (what moe_unpermute takes)
- * Rows from R on are not written; the outputs overlap no input. The order is fixed by the ids alone, unlike moe_plan's. The gradient with respect to x is
- * moe_unpermute of the rows' gradients, without weights. T = d->num_tokens, K = d->topk, E = d->num_experts; the other
- * sizes in d are not read. Errors: MOE_ERR_INVALID_ARG (sizes outside 1 <= K <= 32, 1 <= E <= 1024, T*K <= 2^24,
+ * Rows from R on are not written; the outputs overlap no input. The order is fixed by the ids alone, unlike moe_plan's.
+ * The gradient with respect to x is moe_unpermute of the rows' gradients, without weights. T = d->num_tokens, K = d->topk,
+ * E = d->num_experts; the other sizes in d are not read. Errors: MOE_ERR_INVALID_ARG (sizes outside 1 <= K <= 32, 1 <= E <= 1024, T*K <= 2^24,
  * 1 <= H <= 2^30, 0 <= scales <= 2^20; short strides; a missing or misaligned pointer), MOE_ERR_WORKSPACE, MOE_ERR_CUDA. */
 typedef struct {
     const void* x;

@@ -1,6 +1,6 @@
-// Rows of x in int8 with a scale each (moe_int8_quantize in moe_ops.h). A CTA has a row: its values stay in registers between the largest
-// magnitude and the codes, where they fit, so x is read once. Bound by HBM: 2 (bf16) or 4 (fp32) bytes read and 1 written an
-// element. That takes the division out of the way: x / s is Markstein's quotient from r = 1/s rounded to nearest (y = x r, then
+// Rows of x in int8 with a scale each (moe_int8_quantize in moe_ops.h). A CTA has a row, or lanes of a warp where rows are short and many:
+// its values stay in registers between the largest magnitude and the codes, where they fit, so x is read once. Bound by HBM: 2 (bf16)
+// or 4 (fp32) bytes read and 1 written an element. That takes the division out of the way: x / s is Markstein's quotient from r = 1/s rounded to nearest (y = x r, then
 // y + r (x - y s) with fused multiply-adds is x / s rounded to nearest wherever nothing under- or overflows; s >= 1e-8 and
 // r >= 2^-122, so that only quotients far below one half do, whose code is 0 all the same), and adding 1.5 * 2^23 rounds it half to
 // even into the low bits. |x| / s is at most 127 (1 + 2^-22), so no code passes 127.
@@ -69,6 +69,8 @@ __device__ __forceinline__ void put(int8_t* row, int64_t c, int64_t cols, const 
     }
 }
 
+constexpr int kShortThreads = 128;
+
 // kHold: parts of a thread at most (all of them in registers); 0: rows of any length, read twice
 template <typename T, bool kVec, int kHold, int kThreads>
 __global__ void __launch_bounds__(kThreads)
@@ -123,6 +125,44 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// Short rows: L lanes have kRows of them at a time, so that their loads are on their way together.
+template <typename T, bool kVec, int kHold, int L, int kRows>
+__global__ void __launch_bounds__(kShortThreads)
+    quantize_short_kernel(const T* __restrict__ x, int cols, int64_t x_stride, int8_t* __restrict__ q, int64_t q_stride,
+                          float* __restrict__ scale, int64_t rows) {
+    using P = Part<T, kVec>;
+    constexpr int kGroups = kShortThreads / L;
+    const int at = threadIdx.x % L, c0 = at * P::kPer;
+    for (int64_t base = (int64_t)blockIdx.x * kGroups * kRows; base < rows; base += (int64_t)gridDim.x * kGroups * kRows) {
+        const int64_t first = base + threadIdx.x / L;
+        P v[kRows][kHold];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = first + i * kGroups;
+#pragma unroll
+            for (int h = 0; h < kHold; ++h) v[i][h].load(x + r * x_stride, c0 + h * L * P::kPer, r < rows ? cols : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t r = first + i * kGroups;
+            uint32_t top = 0;
+#pragma unroll
+            for (int h = 0; h < kHold; ++h)
+#pragma unroll
+                for (int j = 0; j < P::kPer; ++j) top = max(top, v[i][h].bits(j) & 0x7fffffffu);
+#pragma unroll
+            for (int o = L / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float s = __fmul_rn(__uint_as_float(top), 1.0f / 127.0f);
+            if (s < 1e-8f) s = 1e-8f;
+            const bool finite = s < INFINITY;
+            const float inv = __fdiv_rn(1.0f, s);
+            if (at == 0 && r < rows) scale[r] = s;
+#pragma unroll
+            for (int h = 0; h < kHold; ++h) put(q + r * q_stride, c0 + h * L * P::kPer, r < rows ? cols : 0, v[i][h], s, inv, finite);
+        }
+    }
+}
+
 template <typename T>
 cudaError_t launch(const T* x, int64_t rows, int64_t cols, int64_t x_stride, int8_t* q, int64_t q_stride, float* scale,
                    cudaStream_t s) {
@@ -136,7 +176,29 @@ cudaError_t launch(const T* x, int64_t rows, int64_t cols, int64_t x_stride, int
     const int64_t parts = (cols + 128 * (vec ? kPer : 1) - 1) / (128 * (vec ? kPer : 1));
 #define MOE_QUANT(vec, hold, threads) \
     quantize_kernel<T, vec, hold, threads><<<grid, threads, 0, s>>>(x, cols, x_stride, q, q_stride, scale, rows)
-    if (vec) {
+#define MOE_QUANT_SHORT(vec, hold, lanes, per_lane)                                                                                  \
+    quantize_short_kernel<T, vec, hold, lanes, per_lane>                                                                             \
+        <<<(unsigned)std::min<int64_t>((rows + kShortThreads / lanes * per_lane - 1) / (kShortThreads / lanes * per_lane), 0x7fffffff), \
+           kShortThreads, 0, s>>>(x, (int)cols, x_stride, q, q_stride, scale, rows)
+    // Short rows, where there are more of them than the SMs' first CTAs: lanes share a warp (bf16, CTAs of a row and lanes: 2^20 x 64 683 and 41 us,
+    // 2^18 x 256 174 and 42, 65536 x 1024 57 and 33, 8192 x 256 7.3 and 3.2, 1216 x 256 2.1 and 1.7, but 152 x 256 1.5 and 1.7). Eight vectors or
+    // sixteen values a lane from 32 rows an SM on (32768 x 2048 37 and 33, 8192 x 2048 10.4 and 9.8, 1216 x 2048 3.2 and 3.5).
+    const int64_t per_sm = rows / tc_num_sms(), unit = vec ? kPer : 2;
+    if (per_sm >= (cols <= 128 * unit ? 4 : 32) && cols <= 256 * unit) {
+        const int64_t units = (cols + unit - 1) / unit;
+        if (vec) {
+            if (units <= 4) MOE_QUANT_SHORT(true, 1, 4, 2);
+            else if (units <= 8) MOE_QUANT_SHORT(true, 1, 8, 2);
+            else if (units <= 16) MOE_QUANT_SHORT(true, 1, 16, 2);
+            else if (units <= 32) MOE_QUANT_SHORT(true, 1, 32, 2);
+            else if (units <= 64) MOE_QUANT_SHORT(true, 2, 32, 2);
+            else if (units <= 128) MOE_QUANT_SHORT(true, 4, 32, 1);
+            else MOE_QUANT_SHORT(true, 8, 32, 1);
+        } else if (units <= 32) MOE_QUANT_SHORT(false, 2, 32, 4);
+        else if (units <= 64) MOE_QUANT_SHORT(false, 4, 32, 2);
+        else if (units <= 128) MOE_QUANT_SHORT(false, 8, 32, 1);
+        else MOE_QUANT_SHORT(false, 16, 32, 1);
+    } else if (vec) {
         if (parts <= 2) MOE_QUANT(true, 2, 128);
         else if (parts <= 4) MOE_QUANT(true, 4, 128);
         else if (parts <= 8) MOE_QUANT(true, 8, 128);
@@ -150,6 +212,7 @@ cudaError_t launch(const T* x, int64_t rows, int64_t cols, int64_t x_stride, int
         else MOE_QUANT(false, 0, 256);
     }
 #undef MOE_QUANT
+#undef MOE_QUANT_SHORT
     return cudaGetLastError();
 }
 

@@ -1,7 +1,7 @@
 // The rows of a token's experts back to the token, weighted, and the gradients (moe_unpermute, moe_unpermute_backward in moe_ops.h).
 //
 // Bound by HBM: every row is read once (and its gradient written). Forward: a warp has a segment of a token's columns and
-// adds the K rows in the order of k, eight loads on their way a lane. Backward: a group of warps has a slot; it reads the row and the
+// adds the K rows in the order of k, eight loads on their way a lane (of several segments where K is small). Backward: a group of warps has a slot; it reads the row and the
 // token's gradient (which the token's other slots find in cache), writes the row's gradient and adds up their product.
 // Measured: forward 8192 x 8 x 7168 bf16 (1.06 GB) 167 us, 0.95 of the copy rate (281 with one load on its way at a time); backward 16384 x
 // 2 x 4096 bf16 (0.67 GB) 99 us, the copy rate; 333 x 6 x 1531 fp32 (27 MB, single columns) 8.0 us, 0.49, a wave of short runs of loads.
@@ -78,9 +78,10 @@ __device__ __forceinline__ int slot_row_of(const UnpermuteArgs& p, int64_t slot,
     return r >= 0 && r < p.T * p.K ? r : -1;
 }
 
+// S segments of 8 / S rows are on their way at a time (S > 1: of all the token's rows).
 // A warp's item is a token's run of `per` segments of 32 * N columns; the next item's slots and weights are on their way while one is
 // worked on (an item's own are a load that its rows' loads wait for).
-template <typename R, typename Y, int N>
+template <typename R, typename Y, int N, int S>
 __global__ void __launch_bounds__(kThreads, 3) unpermute_kernel(UnpermuteArgs p, int64_t parts, int64_t per) {
     const int lane = threadIdx.x & 31;
     const int64_t items = p.T * parts, step = (int64_t)gridDim.x * kWarps;
@@ -101,26 +102,45 @@ __global__ void __launch_bounds__(kThreads, 3) unpermute_kernel(UnpermuteArgs p,
         const float my_w = my_row >= 0 ? next_w : 0.0f;
         fetch(item + step);
         const int64_t c1 = min(p.H, c0 + per * (32 * N));
-        for (int64_t c = c0 + lane * N; c - lane * N < c1; c += 32 * N) {
-            float acc[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-            constexpr int kBatch = 8;  // rows on their way
-            for (int k0 = 0; k0 < p.K; k0 += kBatch) {
-                Packed<R, N> v[kBatch];
+        for (int64_t c = c0 + lane * N; c - lane * N < c1; c += S * 32 * N) {
+            constexpr int kBatch = 8 / S;  // rows on their way
+            Packed<R, N> v[S][kBatch];
+            auto load = [&](int k0) {
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     const int r = __shfl_sync(0xffffffffu, my_row, (k0 + b) & 31);
-                    v[b].load(rows + (int64_t)r * p.rows_stride + c, r >= 0 && k0 + b < p.K && c < c1);
+#pragma unroll
+                    for (int i = 0; i < S; ++i) {
+                        const int64_t at = c + i * 32 * N;
+                        v[i][b].load(rows + (int64_t)r * p.rows_stride + at, r >= 0 && k0 + b < p.K && at < c1);
+                    }
                 }
+            };
+            auto add = [&](int k0, int i, float (&acc)[N]) {
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {  // (a slot without a row: 0 * 0)
                     const float w = __shfl_sync(0xffffffffu, my_w, (k0 + b) & 31);
 #pragma unroll
-                    for (int j = 0; j < N; ++j) acc[j] = __fmaf_rn(w, v[b].at(j), acc[j]);
+                    for (int j = 0; j < N; ++j) acc[j] = __fmaf_rn(w, v[i][b].at(j), acc[j]);
                 }
+            };
+            if constexpr (S > 1) load(0);  // (all of the token's rows)
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                float acc[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+                if constexpr (S > 1) {
+                    add(0, i, acc);
+                } else {
+                    for (int k0 = 0; k0 < p.K; k0 += kBatch) {
+                        load(k0);
+                        add(k0, 0, acc);
+                    }
+                }
+                const int64_t at = c + i * 32 * N;
+                if (at < c1) store<Y, N>(static_cast<Y*>(p.out) + t * p.out_stride + at, acc);
             }
-            if (c < c1) store<Y, N>(static_cast<Y*>(p.out) + t * p.out_stride + c, acc);
         }
     }
 }
@@ -179,15 +199,24 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(UnpermuteArgs p) {
     if (sub == 0 && lane == 0 && slot < slots) p.d_weights[slot] = dot;
 }
 
+template <typename R, typename Y, int N, int S>
+cudaError_t launch_segments(const UnpermuteArgs& a, int64_t segments, int64_t resident, cudaStream_t s) {
+    // longer runs a warp where that leaves every resident warp several items
+    int64_t per = S;
+    while (per < 4 && per * 2 <= segments && a.T * ((segments + 2 * per - 1) / (2 * per)) >= 8 * resident) per *= 2;
+    const int64_t parts = (segments + per - 1) / per, ctas = (a.T * parts + kWarps - 1) / kWarps;
+    unpermute_kernel<R, Y, N, S><<<(unsigned)std::min<int64_t>(ctas, resident / kWarps), kThreads, 0, s>>>(a, parts, per);
+    return cudaGetLastError();
+}
+
 template <typename R, typename Y, int N>
 cudaError_t launch_forward(const UnpermuteArgs& a, cudaStream_t s) {
     const int64_t segments = (a.H + 32 * N - 1) / (32 * N), resident = (int64_t)tc_num_sms() * 3 * kWarps;
-    // longer runs a warp where that leaves every resident warp several items
-    int64_t per = 1;
-    while (per < 4 && per * 2 <= segments && a.T * ((segments + 2 * per - 1) / (2 * per)) >= 8 * resident) per *= 2;
-    const int64_t parts = (segments + per - 1) / per, ctas = (a.T * parts + kWarps - 1) / kWarps;
-    unpermute_kernel<R, Y, N><<<(unsigned)std::min<int64_t>(ctas, resident / kWarps), kThreads, 0, s>>>(a, parts, per);
-    return cudaGetLastError();
+    // A token of few rows: several segments at a time, where every resident warp has an item all the same (bf16, one and several: 16384 x 2 x 4096
+    // 115 and 65 us, 1024 x 2 x 4096 10.2 and 5.0, 16384 x 2 x 2047 279 and 116, 16384 x 4 x 2048 64.5 and 55.4).
+    if (a.K <= 2 && segments >= 4 && a.T * (segments / 4) >= resident) return launch_segments<R, Y, N, 4>(a, segments, resident, s);
+    if (a.K <= 4 && segments >= 2 && a.T * (segments / 2) >= resident) return launch_segments<R, Y, N, 2>(a, segments, resident, s);
+    return launch_segments<R, Y, N, 1>(a, segments, resident, s);
 }
 
 template <typename R, typename Y, int N>

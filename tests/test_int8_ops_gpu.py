@@ -45,6 +45,24 @@ def test_quantize(moe, M, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [1231, 5003])
+@pytest.mark.parametrize("K", [1, 3, 4, 8, 16, 24, 40, 61, 72, 129, 248, 256, 264, 511, 512, 520, 1000, 1032, 2048])
+def test_quantize_many_short_rows(moe, M, K, dtype):
+    """Rows that lanes of a warp have: strided, some of them zeros, infinite or NaN, the largest value anywhere."""
+    g = gen(M + K)
+    x = torch.randn((M, K + 8), generator=g, device="cuda") * torch.randn((M, 1), generator=g, device="cuda").mul(4).exp()
+    x[5::97], x[6::97, K // 2], x[7::97, 0], x[8::97, K - 1] = 0.0, math.inf, -math.inf, math.nan
+    x = x.to(dtype)[:, :K]
+    q, scale = torch.full((M + 1, K + 16), 99, dtype=torch.int8, device="cuda"), torch.full((M + 1,), -1.0, device="cuda")
+    moe.moe_int8_quantize(x, q[:M, :K], scale[:M])
+    want_q, want_scale = quantize_by_definition(x)
+    finite = want_scale < math.inf  # (the codes of the others are zero)
+    want_q[~finite] = 0
+    assert torch.equal(scale[:M].cpu().nan_to_num(nan=-2.0), want_scale.nan_to_num(nan=-2.0)) and torch.equal(q[:M, :K].cpu(), want_q)
+    assert (q[:, K:] == 99).all() and (q[M] == 99).all() and scale[M] == -1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("K", [64, 61])
 def test_quantize_ties_zeros_and_extremes(moe, K, dtype):
     big, small = torch.finfo(dtype).max, 2.0 ** -126
