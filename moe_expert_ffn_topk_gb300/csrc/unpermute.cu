@@ -199,6 +199,60 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(UnpermuteArgs p) {
     if (sub == 0 && lane == 0 && slot < slots) p.d_weights[slot] = dot;
 }
 
+// Q slots a warp, of rows that fit in a Q-th of its loads
+template <typename R, typename Y, int N, int Q>
+__global__ void __launch_bounds__(kThreads) backward_short_kernel(UnpermuteArgs p) {
+    constexpr int kBatch = (N == 1 ? kBatch1 : kBatchN) / Q;
+    const int lane = threadIdx.x & 31;
+    const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * Q, slots = (int64_t)p.T * p.K;
+    int row[Q];
+    float w[Q];
+    Packed<Y, N> a[Q][kBatch];
+    Packed<R, N> b[Q][kBatch];
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const bool there = first + i < slots;
+        row[i] = slot_row_of(p, first + i, there);
+        w[i] = p.weights && there ? __ldg(p.weights + first + i) : 1.0f;
+        const Y* dy = static_cast<const Y*>(p.dy) + (there ? (first + i) / p.K : 0) * p.dy_stride;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t c = (j * 32 + lane) * N;
+            a[i][j].load(dy + c, there && c < p.H);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const R* in = static_cast<const R*>(p.rows) + (int64_t)row[i] * p.rows_stride;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t c = (j * 32 + lane) * N;
+            b[i][j].load(in + c, p.d_weights && row[i] >= 0 && c < p.H);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        R* out = static_cast<R*>(p.out) + (int64_t)row[i] * p.out_stride;
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t c = (j * 32 + lane) * N;
+            if (row[i] < 0 || c >= p.H) continue;
+            float grad[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                dot = __fmaf_rn(a[i][j].at(e), b[i][j].at(e), dot);
+                grad[e] = a[i][j].at(e) * w[i];
+            }
+            store<R, N>(out + c, grad);
+        }
+        if (!p.d_weights) continue;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0 && first + i < slots) p.d_weights[first + i] = dot;
+    }
+}
+
 template <typename R, typename Y, int N, int S>
 cudaError_t launch_segments(const UnpermuteArgs& a, int64_t segments, int64_t resident, cudaStream_t s) {
     // longer runs a warp where that leaves every resident warp several items
@@ -226,6 +280,19 @@ cudaError_t launch_back(const UnpermuteArgs& a, cudaStream_t s) {
     // all, 48 each (bf16, H 4096: 512 slots 2.9 us with four and 4.8 with one, 2048 slots 8.0 with two, 9.6 with one, 11.6 with eight)
     int G = 1;
     while (G < kWarps && (a.H + part - 1) / part > G && slots * G * 2 <= (int64_t)tc_num_sms() * 48) G *= 2;
+    // short rows: several slots a warp, where every resident warp has some all the same (bf16, one and several: 32768 x 8 x 256 114 and 57 us,
+    // 4096 x 8 x 256 13.8 and 8.6, 16384 x 8 x 512 69 and 50, 16384 x 8 x 63 52 and 19)
+    if (G == 1) {
+        const int64_t resident = (int64_t)tc_num_sms() * 48;
+        if (a.H <= part / 4 && slots >= resident * 4) {
+            backward_short_kernel<R, Y, N, 4><<<(unsigned)((slots + 4 * kWarps - 1) / (4 * kWarps)), kThreads, 0, s>>>(a);
+            return cudaGetLastError();
+        }
+        if (a.H <= part / 2 && slots >= resident * 2) {
+            backward_short_kernel<R, Y, N, 2><<<(unsigned)((slots + 2 * kWarps - 1) / (2 * kWarps)), kThreads, 0, s>>>(a);
+            return cudaGetLastError();
+        }
+    }
     const unsigned ctas = (unsigned)((slots * G + kWarps - 1) / kWarps);
     if (G == 1) backward_kernel<R, Y, N, 1><<<ctas, kThreads, 0, s>>>(a);
     else if (G == 2) backward_kernel<R, Y, N, 2><<<ctas, kThreads, 0, s>>>(a);
