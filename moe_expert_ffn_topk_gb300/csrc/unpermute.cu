@@ -301,7 +301,7 @@ cudaError_t launch_back(const UnpermuteArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// 16 bytes of a row at a time where every row of either matrix starts on 16 bytes and has a multiple of eight columns
+// 16 bytes of a row at a time where every row of either matrix starts on 16 bytes and has whole vectors of the experts' rows
 bool vectors(const UnpermuteArgs& a) {
     const uint64_t r = a.type == MOE_TYPE_BF16 ? 2 : 4, t = a.token_type == MOE_TYPE_BF16 ? 2 : 4;
     const bool back = a.dy != nullptr;
@@ -309,7 +309,7 @@ bool vectors(const UnpermuteArgs& a) {
     low |= (uint64_t)a.out_stride * (back ? r : t);
     if (a.rows) low |= (uint64_t)a.rows_stride * r;
     if (back) low |= (uint64_t)a.dy_stride * t;
-    return low % 16 == 0 && a.H % 8 == 0;
+    return low % 16 == 0 && a.H % (int64_t)(16 / r) == 0;
 }
 
 template <bool kBack, typename R, typename Y>

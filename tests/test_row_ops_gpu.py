@@ -170,7 +170,7 @@ def slots(g, T, K, masked):
 
 BACK = [(1, 1, 1), (1, 8, 1), (2, 7168, 8), (5, 129, 6), (33, 1000, 32), (300, 40, 9), (1500, 264, 4), (800, 2051, 8), (60, 2048, 2),
         (400, 4096, 7), (4099, 1032, 2), (1000, 517, 1), (2500, 1000, 3), (950, 517, 4), (4801, 248, 7),
-        (3001, 504, 5), (9800, 63, 3), (5000, 121, 3)]
+        (3001, 504, 5), (9800, 63, 3), (5000, 121, 3), (60, 1532, 6), (700, 132, 5)]
 
 
 @pytest.mark.parametrize("weighted", [True, False])
