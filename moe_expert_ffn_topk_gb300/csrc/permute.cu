@@ -5,7 +5,8 @@
 // whose order could change it: counts may be added up in any order, ranks are taken in the order of the slots.
 //   - few slots: one launch in which every CTA has a token, counts all ids for itself (shared memory) and copies its row.
 //   - more: the slots in up to 128 runs, a CTA each. One launch counts the runs' experts; in a second every CTA adds up the runs before its own,
-//     counts its warps' parts and ranks 32 slots at a time with match.any; a third copies.
+//     counts its warps' parts and ranks 32 slots at a time with match.any; a third copies and clears
+//     the counts.
 //
 // Bound by HBM's writes: a token is read once and written K times. 8192 x 8 x 7168 bf16 (1.06 GB): 169 us, 6.26 TB/s, 0.93 of the copy
 // rate, where a fill alone runs at 4.0 TB/s; 9 us of them sort (a cluster of eight CTAs that exchanged its totals took 16).
@@ -31,7 +32,7 @@ inline bool few_slots(int64_t T, int64_t K) { return T * K <= kFewSlots && T * T
 constexpr int kFewThreads = 256;
 constexpr int kSortWarps = 32, kSortThreads = 32 * kSortWarps;
 // Runs of slots that are sorted by a CTA each, and slots of one: every CTA reads all runs' counts (65536 slots of 256 experts, rows of 16 bytes: 128
-// runs of 512 16.9 us, 64 of 1024 14.3, 16 of 4096 16.0; 4.2 million slots 237 us with 128 runs, 287 with 64).
+// runs of 512 16.9 us, 64 of 1024 14.3, 16 of 4096 16.0; 4.2 million slots 237 us with 128 runs, 287 with 64, before the counts were cleared: 239).
 constexpr int kMaxRuns = 128, kMinRun = 1024;
 constexpr int kCopyWarps = 8;
 constexpr int kCopyVecs = 4;  // vectors of a lane on their way at a time
@@ -51,7 +52,8 @@ struct CopyArgs {
     float* row_scale;
     const int32_t* slot_row;
     int64_t bytes, x_stride, rows_stride;  // bytes of a row and between rows
-    int T, K, n, scales, segments;
+    int32_t* counts;                       // the runs' counts, and how many there are
+    int T, K, scales, segments, num_counts;
 };
 
 // expert of a slot, -1 without one; ids that name no expert are reported
@@ -254,6 +256,10 @@ template <int V>
 __global__ void __launch_bounds__(32 * kCopyWarps) copy_kernel(CopyArgs c) {
     const int lane = threadIdx.x & 31;
     const int64_t vecs = c.bytes / V, items = (int64_t)c.T * c.segments;
+    // the workspace goes back as zeros, which the next call on it may count on (other operators keep counters there)
+    static_assert(kMaxRuns * kRowExperts <= 32 * kCopyWarps << 16, "the first 2^16 CTAs have all counts");
+    if (blockIdx.x < 1u << 16)
+        for (int i = blockIdx.x * (32 * kCopyWarps) + threadIdx.x; i < c.num_counts; i += min(gridDim.x, 1u << 16) * (32 * kCopyWarps)) c.counts[i] = 0;
     for (int64_t item = (int64_t)blockIdx.x * kCopyWarps + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * kCopyWarps) {
         const int64_t t = item / c.segments, seg = item - t * c.segments, v0 = seg * (32 * kCopyVecs);
         const int row = lane < c.K ? __ldg(c.slot_row + t * c.K + lane) : -1;
@@ -278,6 +284,7 @@ cudaError_t launch_v(const SortArgs& p, CopyArgs c, cudaStream_t s) {
     place_kernel<<<p.runs, kSortThreads, sizeof(int) * kSortWarps * p.E, s>>>(p);
     const int64_t per_row = (c.bytes / V + 32 * kCopyVecs - 1) / (32 * kCopyVecs);
     c.segments = (int)per_row;
+    c.counts = p.counts, c.num_counts = p.runs * p.E;
     const int64_t ctas = (c.T * per_row + kCopyWarps - 1) / kCopyWarps;
     copy_kernel<V><<<(unsigned)std::min<int64_t>(ctas, 0x7fffffff), 32 * kCopyWarps, 0, s>>>(c);
     return cudaGetLastError();
@@ -305,7 +312,7 @@ cudaError_t launch_permute(const moe_permute_args& a, int T, int K, int E, int32
     c.row_scale = a.row_scale;
     c.slot_row = a.slot_row;
     c.bytes = a.H * size, c.x_stride = a.x_stride * size, c.rows_stride = a.rows_stride * size;
-    c.T = T, c.K = K, c.n = T * K, c.scales = a.scales;
+    c.T = T, c.K = K, c.scales = a.scales;
     // the widest vector that every row starts and ends on
     const uint64_t low = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.rows) | (uint64_t)c.bytes |
                          (uint64_t)c.x_stride | (uint64_t)c.rows_stride;
