@@ -22,7 +22,7 @@
 // rows of 32 groups, 4096 x 2048: 89 us, 2.35 TB/s of weights; a stage is 512 cycles of MMAs on a 256 x 128 tile and takes 1080 (ALU
 // 63 % busy, tensor pipe 33 %). 133 x 2112 x 7168: 17 us, 14 stages a CTA at 980 cycles, 3 us before the first operands, 3 for the
 // cluster's sum.
-// What it took, on the first of these: 436 us with a forwarder that released the odd CTA's operands at cluster scope (850 cycles a stage);
+// What it took, on the first of these: 436 us with a forwarder that released everything of the odd CTA's at cluster scope (850 cycles a stage);
 // 404 with converters of both CTAs arriving themselves; 310 with sums taken out in pauses of two steps and converters of both operands
 // in every warp; 305 with one commit a stage; 292 without a conversion to integers of every value of every chunk. Slower: sums read by
 // warps that sleep between their looks (315), packed bf16 stores of two rows (305), spinning tests instead of waits (298).
@@ -169,7 +169,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // A test and a bounded wait that begins with it: a try_wait costs 170-280 cycles when the phase has long completed, a test a fraction.
-// kCluster: for a barrier that the other CTA of the pair arrives on, too (what that CTA wrote is seen).
+// kCluster: for a barrier that the other CTA of the pair, or its MMAs' commits, arrive on, too (what that CTA did is seen).
 template <bool kCluster = false>
 __device__ __forceinline__ bool completed(uint32_t bar, uint32_t parity) {
     if constexpr (!kCluster) return mbar_test(bar, parity);
@@ -188,14 +188,20 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int32_t*
     return !kCluster || completed<kCluster>(bar, parity);
 }
 
-// Arrives on a barrier of either CTA of the pair for operands that this warp has written to its own CTA's shared memory (and made visible to
-// the MMA by fence.proxy.async) or tensor memory (tcgen05.wait::st): the tensor cores of the CTA that holds them read them, so
-// the release of CTA scope suffices. One of cluster scope waits for all of the warp's accesses and took 850 cycles a stage.
+// Arrives on a barrier of either CTA of the pair for operands that this warp has written to its own CTA's shared memory (each lane's made visible
+// to the MMA by its fence.proxy.async) and tensor memory (tcgen05.wait::st and the fence after it, which an execution order of
+// cluster scope completes). The fence releases the former to the pair: it covers shared memory alone, so it waits for no access to
+// any other. A release of cluster scope of everything (arrive.release or fence.acq_rel) took 463 and 469 us where this takes 288
+// (8192 x 4096 x 7168), 132 and 135 where this takes 91 (4099 rows of 32 groups).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+        : "memory");
 }
 
-// Arrives on a barrier of either CTA of the pair after this warp's reads of tensor memory (ordered by tcgen05.wait::ld) alone.
+// Arrives on a barrier of either CTA of the pair after this warp's reads of tensor memory alone: tcgen05.wait::ld and the fence after it order
+// them, with the fence that the MMA warp has after its wait.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -324,7 +330,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             };
             auto test_ops = [&](int i) { ready_op = completed<kPair>(op_full(i % C::kOps), (uint32_t)(i / C::kOps) & 1u); };
             auto wait_acc = [&](int a, int times) {
-                ok = __all_sync(0xffffffffu, wait_for(acc_free(a), ((uint32_t)times & 1u) ^ 1u, p.hdr, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_for<kPair>(acc_free(a), ((uint32_t)times & 1u) ^ 1u, p.hdr, abort_flag));
                 if (ok) tc_fence_after();
                 return ok;
             };
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 const uint32_t o = turn % C::kOps;
                 if (!__all_sync(0xffffffffu, landed && freed)) {
                     ok = wait_for(raw_full(s), parity, p.hdr, abort_flag) &&
-                         wait_for(op_free(o), (turn / C::kOps & 1u) ^ 1u, p.hdr, abort_flag);
+                         wait_for<kPair>(op_free(o), (turn / C::kOps & 1u) ^ 1u, p.hdr, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                 }
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 if (s >= C::kRaw) s -= C::kRaw, parity ^= 1u;
                 turn += C::kGroups / 2;
                 landed = completed(raw_full(s), parity);
-                freed = completed(op_free(turn % C::kOps), (turn / C::kOps & 1u) ^ 1u);
+                freed = completed<kPair>(op_free(turn % C::kOps), (turn / C::kOps & 1u) ^ 1u);
                 const uint32_t dst = base + C::kOpOff + o * C::kOpBytes + i * C::kAtomBytes + row * 128;
 #pragma unroll
                 for (int j = 0; j < C::kMine; ++j) {
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < C::kCols; ++j) acc[j] = 0;
             auto take = [&](int a, uint32_t parity) {
-                ok = __all_sync(0xffffffffu, wait_for(acc_full(a), parity, p.hdr, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_for<kPair>(acc_full(a), parity, p.hdr, abort_flag));
                 if (!ok) return;
                 tc_fence_after();
                 if (live) {
