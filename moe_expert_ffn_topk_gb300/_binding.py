@@ -451,6 +451,8 @@ def moe_fp8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream=
     if b.dim() == 3:
         G, N, k2 = b.shape
         between, b_stride, one = b.stride()
+        if N == 1:
+            b_stride = between
         if G > 1 and between != N * b_stride:
             raise ValueError("the groups of b must follow each other")
         b_scale_shape = (G, (N + 127) // 128, kb)
@@ -674,6 +676,8 @@ def moe_int8_matmul(a, a_scale, b, b_scale, out, workspace, offsets=None, stream
     if b.dim() == 3:
         G, N, k2 = b.shape
         between, b_stride, one = b.stride()
+        if N == 1:
+            b_stride = between
         if G > 1 and between != N * b_stride:
             raise ValueError("the groups of b must follow each other")
     else:
