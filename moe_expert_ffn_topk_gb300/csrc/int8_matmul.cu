@@ -717,10 +717,13 @@ template <typename Out>
 cudaError_t launch_out(const moe_int8_matmul_args& a, const Args& p, cudaStream_t s) {
     const int sms = tc_num_sms();
     const int64_t n_tiles = (a.N + 255) / 256, rows = a.M / a.groups;
-    // few rows: 16 rows 13.0 us there and 14.5 on Small, 32 rows 22 and 14. Of groups, where Small has a CTA for less than every SM: 64 rows of 8
-    // groups, N 512, 18 us and 30; of 32 groups, N 4096, K 2048 (1024 tiles) 48 and 41
-    // (256 rows at most, for all of them may be one group's, which takes 16 at a time)
-    if (a.groups == 1 ? a.M <= 16 : rows <= 16 && a.M <= 256 && a.groups * ((a.N + 127) / 128) < sms) return launch_int8_few(a, s);
+    // Few rows: 16 rows 13.0 us there and 14.5 on Small, 32 rows 22 and 14. Of groups, where Small has a CTA for less than every SM, but rows may all be
+    // one group's, which takes 16 of them at a time. `tiles`, those of the groups that can have rows: up to half of the SMs Small's CTAs are alone
+    // with their K, beyond it they are as fast from 32 rows on. K 7168, rows spread evenly / all in one group, here and on Small: 32 tiles (8 groups,
+    // N 512) 64 rows 13.4 / 21.4 us and 29.5 / 29.9, 128 rows 13.4 / 40.5 and 29.6 / 30.1; 64 tiles (16 groups) 256 rows 23.3 / 79 and 29.8 / 30.3;
+    // 128 tiles (32 groups) 32 rows 38 / 21 and 31 / 29, 64 rows 38 / 38 and 31 / 30, 256 rows 39 / 141 and 31 / 31.
+    const int64_t n128 = (a.N + 127) / 128, tiles = std::min<int64_t>(a.groups, a.M) * n128;
+    if (a.groups == 1 ? a.M <= 16 : rows <= 16 && a.groups * n128 < sms && a.M <= (2 * tiles <= sms ? 256 : 32)) return launch_int8_few(a, s);
     // 256 x 256: where 256 x 128 tiles take a second round of the pairs. 1000 rows 47 us and 59 on Pair, 512 rows, K 4096, 30 and 22; 16 groups of
     // 256 rows, K 2048, 73 and 77, 32 of 128 rows 93 and 89
     if (a.groups <= Large::kMaxGroups && rows >= 256 && ((a.M + 255) / 256) * n_tiles * 4 >= sms) return launch<Large, Out>(a, p, s);
