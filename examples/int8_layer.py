@@ -70,7 +70,7 @@ def product(codes, scale, w, w_scale, offsets, dtype):
 def by_parts(layer, x, ids, weights):
     codes, scale = quantized(x)
     rows, offsets, slot_row, row_scale = sorted_rows(codes, ids, layer.experts, scale)
-    h = product(rows, row_scale, layer.w1, layer.s1, offsets, torch.float32)  # (rows without a route are not written, and not read below)
+    h = product(rows, row_scale, layer.w1, layer.s1, offsets, torch.float32)  # (rows without a route hold whatever was there; no slot names what is made of them below)
     act = torch.nn.functional.silu(h[:, :layer.inter]) * h[:, layer.inter:]
     out = product(*quantized(act), layer.w2, layer.s2, offsets, torch.bfloat16)
     y = torch.empty_like(x)

@@ -16,11 +16,11 @@
 // Warp roles: warp 0 TMA producer, warp 1 tensor-memory allocator and MMA issuer, warp 2 the groups' table, warp 3 a split tile's scales,
 // warps 4-11 take sums out and write results, the others (8 or 16) convert.
 //
-// Measured, 8192 x 4096 x 7168 to bf16: 287 us (1.67 PFLOP/s; 0.86 of cuBLAS's bf16 burst rate, 0.95 of its sustained one). A stage of 128 of
+// Measured, 8192 x 4096 x 7168 to bf16: 288 us (1.67 PFLOP/s; 0.86 of cuBLAS's bf16 burst rate, 0.94 of its sustained one). A stage of 128 of
 // K is 1024 cycles of MMAs on a 256 x 256 pair tile and takes some 1350: the same 1024 cycles of shared memory (32 KB each way in,
 // out, in and out) and half of the schedulers' slots contend with them; without converters and epilogue the loop takes 220 us. 4099
-// rows of 32 groups, 4096 x 2048: 89 us, 2.35 TB/s of weights; a stage is 512 cycles of MMAs on a 256 x 128 tile and takes 1080 (ALU
-// 63 % busy, tensor pipe 33 %). 133 x 2112 x 7168: 17 us, 14 stages a CTA at 980 cycles, 3 us before the first operands, 3 for the
+// rows of 32 groups, 4096 x 2048: 91 us, 2.6 TB/s of weights (28 groups have rows); a stage is 512 cycles of MMAs on a 256 x 128 tile and takes 1100
+// (ALU 61 % busy, tensor pipe 32 %). 133 x 2112 x 7168: 17 us, 14 stages a CTA at 980 cycles, 3 us before the first operands, 3 for the
 // cluster's sum.
 // What it took, on the first of these: 436 us with a forwarder that released everything of the odd CTA's at cluster scope (850 cycles a stage);
 // 404 with converters of both CTAs arriving themselves; 310 with sums taken out in pauses of two steps and converters of both operands
@@ -76,7 +76,6 @@ struct Cfg {
     static_assert(kThreads * kLaunchRegs <= 65536 && (kGroups == 2 || kGroups == 4), "warps");
     static constexpr int kCtas = kCtas_, kN = kN_, kHalves = kHalves_, kRaw = kRaw_, kOps = kOps_;
     static constexpr int kStep = kHalves;                   // stages of a step
-    static constexpr int kChunkSteps = kChunkStages / kStep;  // steps of an exact fp32 sum
     static constexpr int kTokens = kN * kHalves;
     static constexpr int kBRows = kTokens / kCtas, kHalfRows = kN / kCtas;
     static constexpr int kRawA = 128 * kStageK, kRawBytes = kRawA + kBRows * kStageK;
@@ -117,10 +116,11 @@ __device__ __forceinline__ Tile decode(int64_t t, const int* tab, int groups, in
 
 // Whether the sum of a half is taken out after step d of n. The halves' MMAs alternate as 0 1 | 1 0 | 0 1 | ..., so the half that was first
 // in step 0 has a gap of two steps of the other half's after every even step, the other one after every odd step: the sums are
-// taken out in these gaps. At most C::kChunkSteps steps, 1024 of K, are added up.
+// taken out in these gaps. At most kSteps steps, 1024 of K, are added up.
 template <class C>
 __device__ __forceinline__ bool taken_out(bool first, int d, int n) {
-    return d == n - 1 || d % C::kChunkSteps == C::kChunkSteps - (first ? 2 : 1);
+    constexpr int kSteps = kChunkStages / C::kStep;
+    return d == n - 1 || d % kSteps == kSteps - (first ? 2 : 1);
 }
 
 // four codes as f16 numbers: c + 128 is put into the fraction of 1024, from which 1152 is subtracted

@@ -3,9 +3,9 @@
 // the registers that mma.sync m16n8k32 on int8 takes (the order of K within a row's 128 codes is the same for both operands, so
 // it need not be the instruction's), eight tokens a time. The sums are integers, so their order does not matter.
 //
-// mma.sync on int8 runs at 150 TOP/s, dp4a too: eight rows of a take as long there as their weights' bytes from HBM, so up to four are
-// multiplied by dp4a, which does no work for rows that are not there. Measured on 4096 x 7168 (29 MB, 4.4 us at the copy rate; graph
-// of calls, inputs rotated past L2): 1 row 7.4 us, 4 rows 9.0, 8 rows 9.7, 16 rows 13.0 (1 row by mma.sync 9.1). What is left is start,
+// mma.sync on int8 runs at 150 TOP/s, dp4a too: eight rows of a take 0.7 of the time there that their weights' bytes take from HBM, sixteen 1.4. Up to
+// four are multiplied by dp4a, which does no work for rows that are not there. Measured on 4096 x 7168 (29 MB, 4.4 us at the copy rate; graph
+// of calls, inputs rotated past L2): 1 row 7.4-7.7 us, 4 rows 9.0-9.3, 8 rows 9.6, 16 rows 12.9 (1 row by mma.sync 9.1). What is left is start,
 // two steps of loads in flight a warp, and the sum: a third and a fourth step spilled and gained nothing.
 #include <cuda_runtime.h>
 
